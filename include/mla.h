@@ -364,6 +364,161 @@ mla_status mla_attend_materialised(const mla_shape* shape, const void* q_nope,
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Draft trees and eviction.  A serving loop that drafts a small tree of tokens for every
+ * sequence, verifies it in one attention call and keeps the accepted path, over a ring whose
+ * sequences have lengths of their own.  The lengths live on the device, so that a captured
+ * loop can be replayed while they change:
+ *
+ *   window [B, 3] int32: for each sequence its first slot, its context rows and its draft
+ *   nodes.  Logical row j of sequence b is ring slot (first + j) mod S: rows 0 .. rows - 1 are
+ *   the context, rows + i is node i.  Values outside the ring are clipped: first to
+ *   [0, S - 1], rows to [0, S], nodes to [0, min(n_nodes, S - rows)].
+ *
+ * n_nodes is the stride of the per-node tensors and the most nodes a sequence can have; a
+ * sequence's nodes past its own count are not read, and their results are left as they were.
+ * The arrays named here and below by their element type (window, token, position, weights, lse)
+ * need that type's alignment only; tree and accept are bytes.
+ * The order of the context rows does not matter to the attention (a cached key carries its
+ * rotation), which is what lets rows move when others leave.
+ *
+ *   tree [B, n_nodes, n_nodes] bytes or NULL: node i sees node k iff tree[b][i][k] != 0 (a
+ *   node sees itself only if its own byte says so).  NULL: node i sees the nodes k <= i (a
+ *   chain; one new token is n_nodes = 1).  Every node sees the whole context.
+ */
+
+/*
+ * mla_tree_write — mla_cache_write for draft nodes: every node at its own position, every
+ * sequence at its own slots (a tree's siblings share a position; "The RoPE problem, and the
+ * decoupled fix": the cached key carries its position).
+ *
+ * For b < B and i < nodes of window[b], with r = (first + rows + i) mod S:
+ *   cache[b][r][0 : d_latent]        = h[b][i] . w_dkv
+ *   cache[b][r][d_latent : +d_rope]  = RoPE3D(h[b][i] . w_kr, position of token[b][i])
+ *   position[b][r]                   = token[b][i]        (if position != NULL)
+ *
+ *   h        [B, n_nodes, d_model]   read       token [B, n_nodes] int32, >= 0, read
+ *   w_dkv, w_kr, cache               as in mla_cache_write
+ *   position [B, S] int32 or NULL    written at the nodes' slots
+ * Errors: MLA_ERR_ARG for a NULL tensor, d_model < 1 or n_nodes < 0; MLA_ERR_RANGE if n_nodes > S;
+ * MLA_ERR_UNSUPPORTED if B * n_nodes passes 2^31 - 1; MLA_ERR_ALIGN.
+ */
+mla_status mla_tree_write(const mla_shape* shape, const void* h, int32_t d_model,
+                          int64_t n_nodes, const int32_t* window, const int32_t* token,
+                          const void* w_dkv, const void* w_kr, void* cache,
+                          int32_t* position, void* stream);
+
+/*
+ * mla_tree_absorb_q — mla_absorb_q with a position for every query:
+ *   q_abs[b][i][h] = [q_nope[b][i][h] . w_uk[h] || RoPE3D(q_rope[b][i][h], position of token[b][i])]
+ * for all n_nodes queries of every sequence (those past a sequence's nodes are whatever their
+ * inputs give; no later call reads them).  Tensors as in mla_absorb_q, token [B, n_nodes] int32.
+ * Errors: MLA_ERR_ARG; MLA_ERR_RANGE if n_nodes > S; MLA_ERR_UNSUPPORTED if
+ * B * n_nodes * n_heads passes 2^31 - 1; MLA_ERR_ALIGN.
+ */
+mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const void* q_rope,
+                             int64_t n_nodes, const int32_t* token, const void* w_uk,
+                             void* q_abs, void* stream);
+
+/*
+ * mla_attend_tree_workspace_size — bytes of device workspace that lets mla_attend_tree split
+ * a tile's keys across SMs (as mla_attend_workspace_size).  May be 0.
+ */
+size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes);
+
+/*
+ * mla_attend_tree — absorbed attention of draft nodes over the context and their ancestors
+ * (mla_attend's scores and values, with the mask of a tree in place of the frames').  For
+ * b < B, i < nodes of window[b] and every head h, over the visible rows j (j < rows, or
+ * j = rows + k with node k seen by node i), c_j = cache[b][(first + j) mod S]:
+ *   s(j)   = softmax_scale * (q_abs[b][i][h] . c_j)
+ *   o_lat[b][i][h] = sum_j softmax(s)(j) * c_j[0 : d_latent]
+ *   lse[b][i][h]   = log(sum_j exp(s(j)))    (natural log, float32; if lse != NULL)
+ * A node that sees nothing (no context and an empty tree row) gets o_lat = 0, lse = -inf.  What
+ * a hidden node's row holds, infinities and NaN included, does not reach a node that does not
+ * see it.
+ *
+ *   q_abs [B, n_nodes, n_h, d_latent + d_rope]  read    o_lat [B, n_nodes, n_h, d_latent] written
+ *   cache [B, S, d_latent + d_rope]             read    lse   [B, n_nodes, n_h] float32 or NULL
+ *   (a given lse is 16-byte aligned)
+ *   workspace: as in mla_attend (NULL with 0 bytes keeps tiles whole).  Calls that share a
+ *   workspace must not run concurrently.
+ * Errors: MLA_ERR_ARG (NULL tensor, n_nodes < 0, softmax_scale not positive, workspace smaller
+ * than mla_attend_tree_workspace_size()); MLA_ERR_RANGE if n_nodes > S; MLA_ERR_UNSUPPORTED if
+ * n_nodes > 65535 or B * n_nodes * n_heads passes 2^31 - 1; MLA_ERR_ALIGN.
+ */
+mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_nodes,
+                           const void* cache, const int32_t* window, const uint8_t* tree,
+                           float softmax_scale, void* o_lat, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * mla_attend_weight — the attention weight each cached row received, added to a running total
+ * (the score by which eviction ranks rows).  With the nodes, tree and lse of mla_attend_tree, for
+ * every row j < rows + nodes of window[b], r = (first + j) mod S:
+ *   weight_out[b][r] = w0 + sum over i < nodes, h of query_weight[b][i] * exp(s(b, i, h, j) - lse[b][i][h])
+ * over the (i, h) that see row j, with w0 = weight_in[b][r] for a context row and 0 for a node's
+ * row.  A query whose lse is -inf, or whose query_weight is 0, adds nothing.  The sums are
+ * float32 and their order is fixed: the same inputs give the same bits.
+ *
+ *   q_abs, cache, window, tree, softmax_scale   as in mla_attend_tree
+ *   lse          [B, n_nodes, n_h] float32      read
+ *   query_weight [B, n_nodes] float32 or NULL (all 1), finite: 0 for nodes that were rejected
+ *   weight_in    [B, S] float32 or NULL (0)     read; may be the same array as weight_out
+ *   weight_out   [B, S] float32                 written at the window's slots only
+ * Errors: as mla_attend_tree (without o_lat and workspace; lse must not be NULL).
+ */
+mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t n_nodes,
+                             const void* cache, const int32_t* window, const uint8_t* tree,
+                             float softmax_scale, const float* lse, const float* query_weight,
+                             const float* weight_in, float* weight_out, void* stream);
+
+/*
+ * mla_cache_evict_workspace_size — bytes of device workspace mla_cache_evict and
+ * mla_tree_accept need: the list of rows to move, two int32 slots each.
+ */
+size_t mla_cache_evict_workspace_size(const mla_shape* shape);
+
+/*
+ * mla_tree_accept — keep the accepted nodes of every sequence as context.  With
+ * count = the accepted nodes among i < nodes of window[b]: nodes i < count that were not
+ * accepted are overwritten, in ascending order, by the accepted nodes i >= count, in ascending
+ * order (cached row, weight and position); then window[b] = {first, rows + count, 0}.
+ *
+ *   accept   [B, n_nodes] bytes (non-zero: accepted)   read
+ *   cache    [B, S, d_latent + d_rope]                 rows moved
+ *   weight   [B, S] float32 or NULL, position [B, S] int32 or NULL    moved with the rows
+ *   window   [B, 3] int32                              read and written
+ *   workspace: at least mla_cache_evict_workspace_size() bytes (required); calls that share
+ *   one must not run concurrently.
+ * Errors: MLA_ERR_ARG, MLA_ERR_RANGE (n_nodes > S), MLA_ERR_ALIGN.
+ */
+mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
+                           const uint8_t* accept, int32_t* window, float* weight,
+                           int32_t* position, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * mla_cache_evict — drop the context rows that attention has used least.  For every sequence
+ * with rows > n_keep: rows are ranked, those first whose position is below n_sink or among the
+ * last n_recent positions (position > largest position of the context - n_recent), the others
+ * by weight, largest first, a NaN weight last; of equal rank the lower logical row comes first.
+ * The first n_keep rows by rank stay.  Rows that leave and lie at logical row < n_keep are
+ * overwritten, in ascending order, by the staying rows at n_keep and beyond, in ascending order
+ * (cached row, weight and position); then window[b] = {first, n_keep, 0}.  Rows that stay below
+ * n_keep do not move, and what lies past the new end is left as it was.  A sequence with
+ * rows <= n_keep keeps its rows; its nodes are set to 0 too (accept comes before evict).
+ *
+ *   weight [B, S] float32, position [B, S] int32       read, moved with the rows
+ *   cache, window, workspace                           as in mla_tree_accept
+ * Errors: MLA_ERR_ARG for a NULL tensor or workspace, one that is too small, or a negative
+ * n_keep, n_sink or n_recent; MLA_ERR_RANGE for n_keep > S; MLA_ERR_ALIGN.
+ */
+mla_status mla_cache_evict(const mla_shape* shape, void* cache, int64_t n_keep, int32_t n_sink,
+                           int32_t n_recent, int32_t* window, float* weight, int32_t* position,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * mla_kernel_launches — number of kernels this library has launched in this process
  * (a host-side counter, incremented at every successful launch).  Diagnostic only.
  */

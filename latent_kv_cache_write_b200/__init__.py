@@ -19,7 +19,20 @@ chunk's queries attending to the n_keys window tokens starting at k0)::
     mla.mla_attend(shape, q_abs, T, g0, cache, k0, n_keys, scale, o_lat, lse, ws)
     mla.mla_up_v(shape, o_lat, T, w_uv, out)                             # [B, T, H, 128]
 
-``mla_attend_materialised`` replaces the last three calls with the non-absorbed form;
+A serving loop with draft trees and sequences of their own lengths keeps those on the device
+(``window`` int32 [B, 3]: first slot, context rows, nodes) and runs, per step::
+
+    mla.mla_tree_write(shape, h, d_model, n, window, token, w_dkv, w_kr, cache, position)
+    mla.mla_tree_absorb_q(shape, q_nope, q_rope, n, token, w_uk, q_abs)
+    mla.mla_attend_tree(shape, q_abs, n, cache, window, tree, scale, o_lat, lse, ws)
+    mla.mla_up_v(shape, o_lat, n, w_uv, out)
+    # ... choose the accepted nodes ...
+    mla.mla_attend_weight(shape, q_abs, n, cache, window, tree, scale, lse, accepted.float(),
+                          weight, weight)
+    mla.mla_tree_accept(shape, cache, n, accepted, window, weight, position, ews)
+    mla.mla_cache_evict(shape, cache, n_keep, n_sink, n_recent, window, weight, position, ews)
+
+``mla_attend_materialised`` replaces the last three calls of the chunk step with the non-absorbed form;
 ``mla_cache_shift_frames`` re-indexes the window's RoPE keys by whole frames;
 ``mla_cache_quantise`` / ``mla_cache_dequantise`` convert ring rows to and from the
 low-bit ring.  Errors raise ``MlaError`` with the library's status.
@@ -37,6 +50,9 @@ __all__ = ["mla_cache_write", "mla_absorb_q", "mla_attend", "mla_attend_workspac
            "mla_attend_fixed_scratch", "mla_attend_materialised", "mla_attend_quantised",
            "mla_cache_shift_frames",
            "mla_cache_quantise", "mla_cache_dequantise",
+           "mla_tree_write", "mla_tree_absorb_q", "mla_attend_tree",
+           "mla_attend_tree_workspace_size", "mla_attend_weight", "mla_tree_accept",
+           "mla_cache_evict", "mla_cache_evict_workspace_size",
            "mla_attend_materialised_workspace_size", "mla_up_v", "mla_device_error",
            "mla_kernel_launches", "mla_device_error_info", "mla_check_wait_timeout", "make_shape",
            "MlaShape", "MlaError", "MLA_FIXED_SCRATCH_BYTES"]
@@ -153,6 +169,67 @@ def mla_attend_materialised(shape: MlaShape, q_nope, q_rope, n_q: int, q_first_t
 def mla_up_v(shape: MlaShape, o_lat, n_q: int, w_uv, out, stream=None) -> None:
     native.check("mla_up_v", native.lib().mla_up_v(
         ctypes.byref(shape), _ptr(o_lat), n_q, _ptr(w_uv), _ptr(out), _stream(stream)))
+
+
+def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
+    if workspace_bytes is not None:
+        return workspace_bytes
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
+                   cache, position=None, stream=None) -> None:
+    native.check("mla_tree_write", native.lib().mla_tree_write(
+        ctypes.byref(shape), _ptr(h), d_model, n_nodes, _ptr(window), _ptr(token), _ptr(w_dkv),
+        _ptr(w_kr), _ptr(cache), _ptr(position), _stream(stream)))
+
+
+def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
+                      stream=None) -> None:
+    native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
+        ctypes.byref(shape), _ptr(q_nope), _ptr(q_rope), n_nodes, _ptr(token), _ptr(w_uk),
+        _ptr(q_abs), _stream(stream)))
+
+
+def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
+    return int(native.lib().mla_attend_tree_workspace_size(ctypes.byref(shape), n_nodes))
+
+
+def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
+                    softmax_scale: float, o_lat, lse=None, workspace=None,
+                    workspace_bytes: Optional[int] = None, stream=None) -> None:
+    native.check("mla_attend_tree", native.lib().mla_attend_tree(
+        ctypes.byref(shape), _ptr(q_abs), n_nodes, _ptr(cache), _ptr(window), _ptr(tree),
+        softmax_scale, _ptr(o_lat), _ptr(lse), _ptr(workspace), _bytes(workspace, workspace_bytes),
+        _stream(stream)))
+
+
+def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
+                      softmax_scale: float, lse, query_weight, weight_in, weight_out,
+                      stream=None) -> None:
+    native.check("mla_attend_weight", native.lib().mla_attend_weight(
+        ctypes.byref(shape), _ptr(q_abs), n_nodes, _ptr(cache), _ptr(window), _ptr(tree),
+        softmax_scale, _ptr(lse), _ptr(query_weight), _ptr(weight_in), _ptr(weight_out),
+        _stream(stream)))
+
+
+def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
+    return int(native.lib().mla_cache_evict_workspace_size(ctypes.byref(shape)))
+
+
+def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
+                    workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    native.check("mla_tree_accept", native.lib().mla_tree_accept(
+        ctypes.byref(shape), _ptr(cache), n_nodes, _ptr(accept), _ptr(window), _ptr(weight),
+        _ptr(position), _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
+                    weight, position, workspace, workspace_bytes: Optional[int] = None,
+                    stream=None) -> None:
+    native.check("mla_cache_evict", native.lib().mla_cache_evict(
+        ctypes.byref(shape), _ptr(cache), n_keep, n_sink, n_recent, _ptr(window), _ptr(weight),
+        _ptr(position), _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def mla_kernel_launches() -> int:

@@ -42,13 +42,21 @@ inline cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, uns
 // Host-side count of kernels launched by the library (see mla_kernel_launches).
 void count_launches(int n);
 
+// Where the rows of draft nodes go: behind the context of each sequence's window, rotated at
+// token's positions, which also go to `position` (or null).
+struct NodePlaces {
+  const int32_t* window;                    // [B, 3]
+  const int32_t* token;                     // [B, n_nodes]
+  int32_t* position;                        // [B, S]
+};
+
 // SIMT CUDA-core path: every dtype and shape (float32 storage uses it throughout).
 cudaError_t simt_cache_write(const Geo& g, bool bf, const void* h, int d_model, int64_t n_tok,
                              int64_t first_tok, const void* w_dkv, const void* w_kr,
-                             void* cache, int32_t* slots, cudaStream_t st);
+                             void* cache, int32_t* slots, const NodePlaces* at, cudaStream_t st);
 cudaError_t simt_absorb_q(const Geo& g, bool bf, const void* q_nope, const void* q_rope,
-                          int64_t n_q, int64_t q_first, const void* w_uk, void* q_abs,
-                          cudaStream_t st);
+                          int64_t n_q, int64_t q_first, const int32_t* token, const void* w_uk,
+                          void* q_abs, cudaStream_t st);
 cudaError_t simt_attend(const Geo& g, bool bf, const void* q_abs, int64_t n_q, int64_t q_first,
                         const void* cache, int64_t k_first, int64_t n_keys, float scale,
                         void* o_lat, float* lse, cudaStream_t st);
@@ -59,10 +67,11 @@ cudaError_t simt_up_v(const Geo& g, bool bf, const void* o_lat, int64_t n_q, con
 bool tc_gemm_supported(const Geo& g, int d_model);
 cudaError_t tc_cache_write(const Geo& g, const void* h, int d_model, int64_t n_tok,
                            int64_t first_tok, const void* w_dkv, const void* w_kr, void* cache,
-                           int32_t* slots, unsigned int* err, cudaStream_t st);
+                           int32_t* slots, const NodePlaces* at, unsigned int* err,
+                           cudaStream_t st);
 cudaError_t tc_absorb_q(const Geo& g, const void* q_nope, const void* q_rope, int64_t n_q,
-                        int64_t q_first, const void* w_uk, void* q_abs, unsigned int* err,
-                        cudaStream_t st);
+                        int64_t q_first, const int32_t* token, const void* w_uk, void* q_abs,
+                        unsigned int* err, cudaStream_t st);
 cudaError_t tc_up_v(const Geo& g, const void* o_lat, int64_t n_q, const void* w_uv, void* out,
                     unsigned int* err, cudaStream_t st);
 // out[b][slot][h] = w[h] . cache[b][slot][0 : d_latent] for every ring slot (the per-head
@@ -120,6 +129,25 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
                            int64_t n_keys, float scale, void* o_lat, float* lse,
                            void* workspace, size_t workspace_bytes, unsigned int* err,
                            cudaStream_t st);
+
+// Draft trees over ragged windows (tree_simt.cu): attention of the nodes, and the attention
+// weight every row of the windows received.
+cudaError_t simt_attend_tree(const Geo& g, bool bf, const void* q_abs, int64_t n_nodes,
+                             const void* cache, const int32_t* window, const uint8_t* tree,
+                             float scale, void* o_lat, float* lse, cudaStream_t st);
+cudaError_t simt_attend_weight(const Geo& g, bool bf, const void* q_abs, int64_t n_nodes,
+                               const void* cache, const int32_t* window, const uint8_t* tree,
+                               float scale, const float* lse, const float* qw, const float* win,
+                               float* wout, cudaStream_t st);
+
+// Rows that move up when others leave (evict.cu).
+size_t evict_workspace(const Geo& g);
+cudaError_t tree_accept(const Geo& g, bool bf, void* cache, int64_t n_nodes, const uint8_t* accept,
+                        int32_t* window, float* weight, int32_t* position, void* workspace,
+                        cudaStream_t st);
+cudaError_t cache_evict(const Geo& g, bool bf, void* cache, int64_t n_keep, int32_t n_sink,
+                        int32_t n_recent, int32_t* window, float* weight, int32_t* position,
+                        void* workspace, cudaStream_t st);
 
 // Address of the static split-key scratch (MLA_FIXED_SCRATCH_BYTES) on the current device.
 cudaError_t fixed_scratch(void** ptr);

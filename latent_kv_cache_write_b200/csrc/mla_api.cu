@@ -35,6 +35,8 @@ unsigned int* device_error_word() {
 namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// arrays read and written element by element (32-bit): NULL passes
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 mla_status check_shape(const mla_shape* s, Geo* g) {
   if (!s) return MLA_ERR_ARG;
@@ -106,6 +108,33 @@ mla_status check_attend(const mla_shape* shape, Geo* g, const void* q_abs, int64
   return MLA_OK;
 }
 
+// the checks mla_attend_tree and mla_attend_weight share
+mla_status check_tree(const mla_shape* shape, Geo* g, const void* q_abs, int64_t n_nodes,
+                      const void* cache, const int32_t* window, float softmax_scale) {
+  mla_status st = check_shape(shape, g);
+  if (st != MLA_OK) return st;
+  if (n_nodes < 0 || !q_abs || !cache || !window) return MLA_ERR_ARG;
+  if (!(softmax_scale > 0.f)) return MLA_ERR_ARG;
+  if (n_nodes > g->S) return MLA_ERR_RANGE;
+  if (n_nodes > 65535 || (int64_t)g->B * n_nodes * g->H > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (!aligned16(q_abs) || !aligned16(cache) || !aligned4(window)) return MLA_ERR_ALIGN;
+  return MLA_OK;
+}
+
+// the checks mla_tree_accept and mla_cache_evict share
+mla_status check_move(const mla_shape* shape, Geo* g, const void* cache, const int32_t* window,
+                      const float* weight, const int32_t* position, const void* workspace,
+                      size_t workspace_bytes) {
+  mla_status st = check_shape(shape, g);
+  if (st != MLA_OK) return st;
+  if (!cache || !window || !workspace || workspace_bytes < evict_workspace(*g))
+    return MLA_ERR_ARG;
+  if (!aligned16(cache) || !aligned4(window) || !aligned4(weight) || !aligned4(position) ||
+      !aligned16(workspace))
+    return MLA_ERR_ALIGN;
+  return MLA_OK;
+}
+
 // the launches of a checked attention call (n_q > 0)
 mla_status run_attend(const mla_shape* shape, const Geo& g, const void* q_abs, int64_t n_q,
                       int64_t q_first_tok, const void* cache, int64_t k_first_tok,
@@ -158,9 +187,9 @@ mla_status mla_cache_write(const mla_shape* shape, const void* h, int32_t d_mode
   cudaStream_t s = (cudaStream_t)stream;
   if (bf && g.Dr > 0 && tc_gemm_supported(g, d_model))
     return cuda_status(tc_cache_write(g, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache,
-                                      slots_out, device_error_word(), s));
+                                      slots_out, nullptr, device_error_word(), s));
   return cuda_status(simt_cache_write(g, bf, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache,
-                                      slots_out, s));
+                                      slots_out, nullptr, s));
 }
 
 mla_status mla_absorb_q(const mla_shape* shape, const void* q_nope, const void* q_rope,
@@ -178,9 +207,9 @@ mla_status mla_absorb_q(const mla_shape* shape, const void* q_nope, const void* 
   if (n_q == 0) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
   if (bf && tc_gemm_supported(g, 0))
-    return cuda_status(tc_absorb_q(g, q_nope, q_rope, n_q, q_first_tok, w_uk, q_abs,
+    return cuda_status(tc_absorb_q(g, q_nope, q_rope, n_q, q_first_tok, nullptr, w_uk, q_abs,
                                    device_error_word(), (cudaStream_t)stream));
-  return cuda_status(simt_absorb_q(g, bf, q_nope, q_rope, n_q, q_first_tok, w_uk, q_abs,
+  return cuda_status(simt_absorb_q(g, bf, q_nope, q_rope, n_q, q_first_tok, nullptr, w_uk, q_abs,
                                    (cudaStream_t)stream));
 }
 
@@ -359,6 +388,129 @@ mla_status mla_attend_materialised(const mla_shape* shape, const void* q_nope,
     e = tc_attend_mat(g, q_nope, q_rope, n_q, q_first_tok, cache, k_mat, v_mat, k_first_tok,
                       n_keys, softmax_scale, out, lse, err, s);
   return cuda_status(e);
+}
+
+mla_status mla_tree_write(const mla_shape* shape, const void* h, int32_t d_model,
+                          int64_t n_nodes, const int32_t* window, const int32_t* token,
+                          const void* w_dkv, const void* w_kr, void* cache,
+                          int32_t* position, void* stream) {
+  Geo g;
+  mla_status st = check_shape(shape, &g);
+  if (st != MLA_OK) return st;
+  if (d_model < 1 || n_nodes < 0) return MLA_ERR_ARG;
+  if (!h || !window || !token || !w_dkv || !cache || (g.Dr > 0 && !w_kr)) return MLA_ERR_ARG;
+  if (n_nodes > g.S) return MLA_ERR_RANGE;
+  if ((int64_t)g.B * n_nodes > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (!aligned16(h) || !aligned4(window) || !aligned4(token) || !aligned16(w_dkv) ||
+      (w_kr && !aligned16(w_kr)) || !aligned16(cache) || !aligned4(position))
+    return MLA_ERR_ALIGN;
+  if (n_nodes == 0) return MLA_OK;
+  const bool bf = shape->dtype == MLA_BF16;
+  cudaStream_t s = (cudaStream_t)stream;
+  const NodePlaces at{window, token, position};
+  if (bf && g.Dr > 0 && tc_gemm_supported(g, d_model))
+    return cuda_status(tc_cache_write(g, h, d_model, n_nodes, 0, w_dkv, w_kr, cache, nullptr, &at,
+                                      device_error_word(), s));
+  return cuda_status(simt_cache_write(g, bf, h, d_model, n_nodes, 0, w_dkv, w_kr, cache, nullptr,
+                                      &at, s));
+}
+
+mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const void* q_rope,
+                             int64_t n_nodes, const int32_t* token, const void* w_uk,
+                             void* q_abs, void* stream) {
+  Geo g;
+  mla_status st = check_shape(shape, &g);
+  if (st != MLA_OK) return st;
+  if (n_nodes < 0 || !q_nope || !token || !w_uk || !q_abs || (g.Dr > 0 && !q_rope))
+    return MLA_ERR_ARG;
+  if (n_nodes > g.S) return MLA_ERR_RANGE;
+  if (n_nodes > INT32_MAX / 2 || (int64_t)g.B * n_nodes * g.H > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  if (!aligned16(q_nope) || (q_rope && !aligned16(q_rope)) || !aligned4(token) ||
+      !aligned16(w_uk) || !aligned16(q_abs))
+    return MLA_ERR_ALIGN;
+  if (n_nodes == 0) return MLA_OK;
+  const bool bf = shape->dtype == MLA_BF16;
+  if (bf && tc_gemm_supported(g, 0))
+    return cuda_status(tc_absorb_q(g, q_nope, q_rope, n_nodes, 0, token, w_uk, q_abs,
+                                   device_error_word(), (cudaStream_t)stream));
+  return cuda_status(simt_absorb_q(g, bf, q_nope, q_rope, n_nodes, 0, token, w_uk, q_abs,
+                                   (cudaStream_t)stream));
+}
+
+size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes) {
+  (void)shape; (void)n_nodes;
+  return 0;
+}
+
+mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_nodes,
+                           const void* cache, const int32_t* window, const uint8_t* tree,
+                           float softmax_scale, void* o_lat, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  Geo g;
+  mla_status st = check_tree(shape, &g, q_abs, n_nodes, cache, window, softmax_scale);
+  if (st != MLA_OK) return st;
+  if (!o_lat) return MLA_ERR_ARG;
+  if (!aligned16(o_lat) || (lse && !aligned16(lse))) return MLA_ERR_ALIGN;
+  const size_t need = mla_attend_tree_workspace_size(shape, n_nodes);
+  if ((workspace || workspace_bytes > 0) && (!workspace || workspace_bytes < need))
+    return MLA_ERR_ARG;
+  if (workspace && !aligned16(workspace)) return MLA_ERR_ALIGN;
+  if (n_nodes == 0) return MLA_OK;
+  const bool bf = shape->dtype == MLA_BF16;
+  return cuda_status(simt_attend_tree(g, bf, q_abs, n_nodes, cache, window, tree, softmax_scale,
+                                      o_lat, lse, (cudaStream_t)stream));
+}
+
+mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t n_nodes,
+                             const void* cache, const int32_t* window, const uint8_t* tree,
+                             float softmax_scale, const float* lse, const float* query_weight,
+                             const float* weight_in, float* weight_out, void* stream) {
+  Geo g;
+  mla_status st = check_tree(shape, &g, q_abs, n_nodes, cache, window, softmax_scale);
+  if (st != MLA_OK) return st;
+  if (!lse || !weight_out) return MLA_ERR_ARG;
+  if (!aligned4(lse) || !aligned4(query_weight) || !aligned4(weight_in) || !aligned4(weight_out))
+    return MLA_ERR_ALIGN;
+  if (n_nodes == 0) return MLA_OK;
+  const bool bf = shape->dtype == MLA_BF16;
+  return cuda_status(simt_attend_weight(g, bf, q_abs, n_nodes, cache, window, tree, softmax_scale,
+                                        lse, query_weight, weight_in, weight_out,
+                                        (cudaStream_t)stream));
+}
+
+size_t mla_cache_evict_workspace_size(const mla_shape* shape) {
+  Geo g;
+  if (check_shape(shape, &g) != MLA_OK) return 0;
+  return evict_workspace(g);
+}
+
+mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
+                           const uint8_t* accept, int32_t* window, float* weight,
+                           int32_t* position, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  Geo g;
+  mla_status st = check_move(shape, &g, cache, window, weight, position, workspace,
+                             workspace_bytes);
+  if (st != MLA_OK) return st;
+  if (n_nodes < 0 || !accept) return MLA_ERR_ARG;
+  if (n_nodes > g.S) return MLA_ERR_RANGE;
+  if (n_nodes == 0) return MLA_OK;
+  return cuda_status(tree_accept(g, shape->dtype == MLA_BF16, cache, n_nodes, accept, window,
+                                 weight, position, workspace, (cudaStream_t)stream));
+}
+
+mla_status mla_cache_evict(const mla_shape* shape, void* cache, int64_t n_keep, int32_t n_sink,
+                           int32_t n_recent, int32_t* window, float* weight, int32_t* position,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  Geo g;
+  mla_status st = check_move(shape, &g, cache, window, weight, position, workspace,
+                             workspace_bytes);
+  if (st != MLA_OK) return st;
+  if (!weight || !position || n_keep < 0 || n_sink < 0 || n_recent < 0) return MLA_ERR_ARG;
+  if (n_keep > g.S) return MLA_ERR_RANGE;
+  return cuda_status(cache_evict(g, shape->dtype == MLA_BF16, cache, n_keep, n_sink, n_recent,
+                                 window, weight, position, workspace, (cudaStream_t)stream));
 }
 
 mla_status mla_check_wait_timeout(void* stream) {

@@ -2,6 +2,7 @@
 // workloads (tensor cores would round to tf32) and any shape the tensor-core kernels
 // do not take.  Accumulation is float32 throughout.
 #include "launch.h"
+#include "window.cuh"
 
 namespace mla {
 namespace {
@@ -19,6 +20,8 @@ struct GemmArgs {
   int M, N, K, zH;
   // cache epilogue
   Geo geo; int64_t first_tok; int32_t* slots;
+  // draft nodes (window != null): rows go behind each sequence's context, at their own positions
+  const int32_t* window; const int32_t* token; int32_t* position;
 };
 
 template <typename T, int EPI>
@@ -75,8 +78,16 @@ __global__ void __launch_bounds__(NT) gemm_simt_kernel(GemmArgs a) {
     const int m = m0 + ty * 4 + i;
     if (m >= a.M) continue;
     if (EPI == EPI_CACHE) {
-      const int64_t g = a.first_tok + m;
-      const int64_t slot = g % a.geo.S;
+      int64_t g = a.first_tok + m;
+      int64_t slot = g % a.geo.S;
+      if (a.window) {
+        const Window w = load_window(a.window, zb, a.geo.S, a.M);
+        if (m >= w.nodes) continue;
+        slot = w.slot((int64_t)w.rows + m, a.geo.S);
+        g = a.token[(int64_t)zb * a.M + m];
+        if (a.position && blockIdx.y == 0 && tx == 0)
+          a.position[(int64_t)zb * a.geo.S + slot] = (int32_t)g;
+      }
       T* row = C + ((int64_t)zb * a.geo.S + slot) * a.ldc;
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
@@ -111,7 +122,8 @@ cudaError_t run_gemm(const GemmArgs& a, int zcount, cudaStream_t st) {
 
 // q_abs[b,i,h,Dc:] = RoPE(q_rope[b,i,h,:], q_first + i)
 template <typename T>
-__global__ void rope_q_kernel(Geo g, const T* q_rope, int64_t n_q, int64_t q_first, T* q_abs) {
+__global__ void rope_q_kernel(Geo g, const T* q_rope, int64_t n_q, int64_t q_first,
+                              const int32_t* token, T* q_abs) {
   const int half = g.Dr / 2;
   const int64_t total = (int64_t)g.B * n_q * g.H * half;
   for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < total;
@@ -121,7 +133,7 @@ __global__ void rope_q_kernel(Geo g, const T* q_rope, int64_t n_q, int64_t q_fir
     const int64_t i = (bih / g.H) % n_q;
     float a = to_f32(q_rope[bih * g.Dr + 2 * p]);
     float b = to_f32(q_rope[bih * g.Dr + 2 * p + 1]);
-    rope_rotate(a, b, rope_angle(g, q_first + i, p));
+    rope_rotate(a, b, rope_angle(g, token ? token[bih / g.H] : q_first + i, p));
     T* dst = q_abs + bih * g.row + g.Dc;
     dst[2 * p] = from_f32<T>(a);
     dst[2 * p + 1] = from_f32<T>(b);
@@ -193,8 +205,11 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(Geo g, const T* q_abs,
 template <typename T>
 cudaError_t run_cache_write(const Geo& g, const void* h, int d_model, int64_t n_tok,
                             int64_t first_tok, const void* w_dkv, const void* w_kr,
-                            void* cache, int32_t* slots, cudaStream_t st) {
+                            void* cache, int32_t* slots, const NodePlaces* at, cudaStream_t st) {
   GemmArgs a{};
+  if (at) {
+    a.window = at->window; a.token = at->token; a.position = at->position;
+  }
   a.A = h; a.lda = d_model; a.a_sb = n_tok * d_model; a.a_sh = 0;
   a.B = w_dkv; a.ldb = g.Dc; a.b_sh = 0; a.b_kmajor = 0;
   a.B2 = w_kr; a.ldb2 = g.Dr; a.n_split = g.Dc;
@@ -206,7 +221,8 @@ cudaError_t run_cache_write(const Geo& g, const void* h, int d_model, int64_t n_
 
 template <typename T>
 cudaError_t run_absorb(const Geo& g, const void* q_nope, const void* q_rope, int64_t n_q,
-                       int64_t q_first, const void* w_uk, void* q_abs, cudaStream_t st) {
+                       int64_t q_first, const int32_t* token, const void* w_uk, void* q_abs,
+                       cudaStream_t st) {
   GemmArgs a{};
   a.A = q_nope; a.lda = (int64_t)g.H * g.Dn; a.a_sb = n_q * g.H * g.Dn; a.a_sh = g.Dn;
   a.B = w_uk; a.ldb = g.Dc; a.b_sh = (int64_t)g.Dn * g.Dc; a.b_kmajor = 0;
@@ -216,7 +232,7 @@ cudaError_t run_absorb(const Geo& g, const void* q_nope, const void* q_rope, int
   if (e != cudaSuccess || g.Dr == 0) return e;
   const int64_t total = (int64_t)g.B * n_q * g.H * (g.Dr / 2);
   const int blocks = (int)((total + 255) / 256 < 148 * 16 ? (total + 255) / 256 : 148 * 16);
-  rope_q_kernel<T><<<blocks, 256, 0, st>>>(g, (const T*)q_rope, n_q, q_first, (T*)q_abs);
+  rope_q_kernel<T><<<blocks, 256, 0, st>>>(g, (const T*)q_rope, n_q, q_first, token, (T*)q_abs);
   e = cudaGetLastError();
   if (e == cudaSuccess) count_launches(1);
   return e;
@@ -237,16 +253,16 @@ cudaError_t run_up_v(const Geo& g, const void* o_lat, int64_t n_q, const void* w
 
 cudaError_t simt_cache_write(const Geo& g, bool bf, const void* h, int d_model, int64_t n_tok,
                              int64_t first_tok, const void* w_dkv, const void* w_kr,
-                             void* cache, int32_t* slots, cudaStream_t st) {
-  return bf ? run_cache_write<bf16>(g, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache, slots, st)
-            : run_cache_write<float>(g, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache, slots, st);
+                             void* cache, int32_t* slots, const NodePlaces* at, cudaStream_t st) {
+  return bf ? run_cache_write<bf16>(g, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache, slots, at, st)
+            : run_cache_write<float>(g, h, d_model, n_tok, first_tok, w_dkv, w_kr, cache, slots, at, st);
 }
 
 cudaError_t simt_absorb_q(const Geo& g, bool bf, const void* q_nope, const void* q_rope,
-                          int64_t n_q, int64_t q_first, const void* w_uk, void* q_abs,
-                          cudaStream_t st) {
-  return bf ? run_absorb<bf16>(g, q_nope, q_rope, n_q, q_first, w_uk, q_abs, st)
-            : run_absorb<float>(g, q_nope, q_rope, n_q, q_first, w_uk, q_abs, st);
+                          int64_t n_q, int64_t q_first, const int32_t* token, const void* w_uk,
+                          void* q_abs, cudaStream_t st) {
+  return bf ? run_absorb<bf16>(g, q_nope, q_rope, n_q, q_first, token, w_uk, q_abs, st)
+            : run_absorb<float>(g, q_nope, q_rope, n_q, q_first, token, w_uk, q_abs, st);
 }
 
 cudaError_t simt_attend(const Geo& g, bool bf, const void* q_abs, int64_t n_q, int64_t q_first,

@@ -12,6 +12,7 @@
 #include "launch.h"
 #include "tc_ptx.cuh"
 #include "tmap.h"
+#include "window.cuh"
 
 #include <mutex>
 
@@ -54,6 +55,11 @@ struct TcGemm {
   int64_t first_tok;        // cache: first token; absorb: first query token
   int32_t* slots;
   const bf16* q_rope;       // absorb: RoPE part input
+  // draft nodes: positions per row (cache, absorb), and for the cache each sequence's window,
+  // behind whose context its rows go, and the positions array to keep them in (may be null)
+  const int32_t* token;
+  const int32_t* window;
+  int32_t* position;
   unsigned int* err;
 };
 
@@ -271,7 +277,21 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
       if (p.mode == MODE_CACHE) {
         const int64_t b = m / p.rows_per_batch;
         g = p.first_tok + (m - b * p.rows_per_batch);
-        base = (b * G.S + g % G.S) * G.row;
+        if (p.window == nullptr) {
+          base = (b * G.S + g % G.S) * G.row;
+        } else {
+          base = -1;                              // rows past a sequence's nodes are not stored
+          if (row_ok) {
+            const Window w = load_window(p.window, b, G.S, p.rows_per_batch);
+            const int64_t i = m - b * p.rows_per_batch;
+            if (i < w.nodes) {
+              g = p.token[m];
+              const int64_t at = b * G.S + w.slot(w.rows + i, G.S);
+              base = at * G.row;
+              if (p.position && n0 == 0) p.position[at] = (int32_t)g;
+            }
+          }
+        }
         if (row_ok && G.Dr > 0) ax = rope_axes(G, g);
       } else if (p.mode == MODE_ABSORB) {
         base = (m * G.H + z) * G.row;
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
           for (int i = 0; i < 4; ++i) {
             const int rr = 8 * i + (lane >> 2), j = lane & 3;      // row of the warp, chunk
             const int64_t rbase = __shfl_sync(0xffffffffu, base, rr);
-            if (m0 + (warp & 3) * 32 + rr < p.M) {
+            if (m0 + (warp & 3) * 32 + rr < p.M && rbase >= 0) {
               const uint4 w = reinterpret_cast<const uint4*>(stg + rr * 64)[j ^ ((rr >> 1) & 3)];
               *reinterpret_cast<uint4*>(p.out + rbase + n + 8 * j) = w;
             }
@@ -379,7 +399,8 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
         p.slots[m] = (int32_t)(g % G.S);
       if (rope_q && ok && qa0 < qa1) {
         // q_abs[.., Dc:] = RoPE(q_R) for the pairs [qa0, qa1) of this row
-        const RopeAxes qa = rope_axes(G, p.first_tok + m % p.rows_per_batch);
+        const RopeAxes qa =
+            rope_axes(G, p.token ? p.token[m] : p.first_tok + m % p.rows_per_batch);
         uint4* dst = reinterpret_cast<uint4*>(p.out + (m * G.H + z) * G.row + G.Dc);
         for (int c = qa0 / 4; c < qa1 / 4; c += 2) {
           uint4 in[2] = {rin[0], rin[1]};
@@ -497,7 +518,8 @@ bool tc_gemm_supported(const Geo& g, int d_model) {
 
 cudaError_t tc_cache_write(const Geo& g, const void* h, int d_model, int64_t n_tok,
                            int64_t first_tok, const void* w_dkv, const void* w_kr, void* cache,
-                           int32_t* slots, unsigned int* err, cudaStream_t st) {
+                           int32_t* slots, const NodePlaces* at, unsigned int* err,
+                           cudaStream_t st) {
   CUtensorMap A, B, B2;
   const uint64_t rows = (uint64_t)g.B * n_tok;
   {
@@ -524,12 +546,15 @@ cudaError_t tc_cache_write(const Geo& g, const void* h, int d_model, int64_t n_t
   p.M = (int)rows; p.N = g.row; p.K = d_model; p.mode = MODE_CACHE; p.b_mn = 1;
   p.n_split = g.Dc; p.out = (bf16*)cache; p.rows_per_batch = n_tok; p.geo = g;
   p.first_tok = first_tok; p.slots = slots; p.err = err;
+  if (at) {
+    p.window = at->window; p.token = at->token; p.position = at->position;
+  }
   return launch(A, B, B2, B, p, 1, st);       // the cache write stores without TMA
 }
 
 cudaError_t tc_absorb_q(const Geo& g, const void* q_nope, const void* q_rope, int64_t n_q,
-                        int64_t q_first, const void* w_uk, void* q_abs, unsigned int* err,
-                        cudaStream_t st) {
+                        int64_t q_first, const int32_t* token, const void* w_uk, void* q_abs,
+                        unsigned int* err, cudaStream_t st) {
   CUtensorMap A, B;
   const uint64_t rows = (uint64_t)g.B * n_q;
   {
@@ -547,7 +572,7 @@ cudaError_t tc_absorb_q(const Geo& g, const void* q_nope, const void* q_rope, in
   TcGemm p{};
   p.M = (int)rows; p.N = g.Dc; p.K = g.Dn; p.mode = MODE_ABSORB; p.b_mn = 1;
   p.n_split = 1 << 30; p.out = (bf16*)q_abs; p.rows_per_batch = n_q; p.geo = g;
-  p.first_tok = q_first; p.q_rope = (const bf16*)q_rope; p.err = err;
+  p.first_tok = q_first; p.q_rope = (const bf16*)q_rope; p.token = token; p.err = err;
   CUtensorMap O;
   {
     // q_abs as (d_c + d_R, heads, rows): 64-column boxes of 128 rows of one head

@@ -49,6 +49,14 @@ SIGNATURES = {
     "mla_attend_materialised_workspace_size": (_sz, [_P]),
     "mla_attend_materialised": (_i32, [_P, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _vp,
                                        _vp, _vp, _vp, _sz, _vp]),
+    "mla_tree_write": (_i32, [_P, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mla_tree_absorb_q": (_i32, [_P, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "mla_attend_tree_workspace_size": (_sz, [_P, _i64]),
+    "mla_attend_tree": (_i32, [_P, _vp, _i64, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "mla_attend_weight": (_i32, [_P, _vp, _i64, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "mla_cache_evict_workspace_size": (_sz, [_P]),
+    "mla_tree_accept": (_i32, [_P, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mla_cache_evict": (_i32, [_P, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mla_status_string": (ctypes.c_char_p, [_i32]),
     "mla_device_error": (_i32, [_vp]),
     "mla_check_wait_timeout": (_i32, [_vp]),

@@ -1,0 +1,105 @@
+"""Argument checks of the draft-tree and eviction calls (no GPU: refused before any launch)."""
+
+import ctypes
+
+import pytest
+
+from latent_kv_cache_write_b200 import build, native
+from synth import configs as C
+
+FAKE, ODD, BYTE = 0x10000, 0x10008, 0x10001
+OK, ARG, UNS, ALIGN, RANGE = (native.MLA_OK, native.MLA_ERR_ARG, native.MLA_ERR_UNSUPPORTED,
+                              native.MLA_ERR_ALIGN, native.MLA_ERR_RANGE)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return native.lib()
+
+
+def shape(**kw):
+    s = native.make_shape(C.DECODE)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+CALLS = {
+    # name: (argument names in order, defaults)
+    "mla_tree_write": dict(h=FAKE, d_model=4096, n=4, window=FAKE, token=FAKE, w_dkv=FAKE,
+                           w_kr=FAKE, cache=FAKE, position=FAKE),
+    "mla_tree_absorb_q": dict(q_nope=FAKE, q_rope=FAKE, n=4, token=FAKE, w_uk=FAKE, q_abs=FAKE),
+    "mla_attend_tree": dict(q_abs=FAKE, n=4, cache=FAKE, window=FAKE, tree=FAKE, scale=0.07,
+                            o_lat=FAKE, lse=FAKE, ws=None, ws_bytes=0),
+    "mla_attend_weight": dict(q_abs=FAKE, n=4, cache=FAKE, window=FAKE, tree=FAKE, scale=0.07,
+                              lse=FAKE, query_weight=FAKE, weight_in=FAKE, weight_out=FAKE),
+    "mla_tree_accept": dict(cache=FAKE, n=4, accept=FAKE, window=FAKE, weight=FAKE, position=FAKE,
+                            ws=FAKE, ws_bytes=1 << 30),
+    "mla_cache_evict": dict(cache=FAKE, keep=4, sink=0, recent=0, window=FAKE, weight=FAKE,
+                            position=FAKE, ws=FAKE, ws_bytes=1 << 30),
+}
+OPTIONAL = {"mla_tree_write": {"position"}, "mla_attend_tree": {"tree", "lse", "ws"},
+            "mla_attend_weight": {"tree", "query_weight", "weight_in"},
+            "mla_tree_accept": {"weight", "position"}}
+WIDE_ALIGN = {"h", "w_dkv", "w_kr", "cache", "q_nope", "q_rope", "w_uk", "q_abs", "o_lat"}
+
+
+def call(L, name, s=None, **kw):
+    args = dict(CALLS[name], **kw)
+    s = s or shape()
+    return getattr(L, name)(ctypes.byref(s), *args.values(), None)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_pointers(L, name):
+    for k, v in CALLS[name].items():
+        if v != FAKE:
+            continue
+        if k not in OPTIONAL.get(name, ()):
+            assert call(L, name, **{k: None}) == ARG, k
+        if k not in ("tree", "accept"):
+            assert call(L, name, **{k: BYTE}) == ALIGN, k
+        if k in WIDE_ALIGN or k == "ws" or (k == "lse" and name == "mla_attend_tree"):
+            assert call(L, name, **{k: ODD}) == ALIGN, k
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "mla_cache_evict"])
+def test_node_counts(L, name):
+    assert call(L, name, n=-1) == ARG
+    assert call(L, name, n=8193) == RANGE                    # more nodes than slots
+    assert call(L, name, n=0) == OK                            # nothing to do
+    assert call(L, name, shape(batch=0)) == ARG
+    assert call(L, name, shape(ring_slots=1 << 31)) == UNS
+
+
+def test_sizes_beyond_32_bits(L):
+    big = shape(batch=500, n_heads=128, ring_slots=60000)
+    for name in ("mla_tree_absorb_q", "mla_attend_tree", "mla_attend_weight"):
+        assert call(L, name, big, n=40000) == UNS, name
+    tall = shape(batch=1, ring_slots=70000)
+    for name in ("mla_attend_tree", "mla_attend_weight"):
+        assert call(L, name, tall, n=65536) == UNS, name
+
+
+def test_scales_and_workspaces(L):
+    for bad in (0.0, -1.0, float("nan")):
+        assert call(L, "mla_attend_tree", scale=bad) == ARG
+        assert call(L, "mla_attend_weight", scale=bad) == ARG
+    assert call(L, "mla_attend_tree", ws=None, ws_bytes=1 << 20) == ARG
+    s = shape()
+    need = L.mla_attend_tree_workspace_size(ctypes.byref(s), 4)
+    if need:
+        assert call(L, "mla_attend_tree", ws=FAKE, ws_bytes=need - 1) == ARG
+    need = L.mla_cache_evict_workspace_size(ctypes.byref(s))
+    # a count per sequence, and two lists of half the ring
+    assert need == 4 * (64 + 64 * 2 * (8192 // 2 + 1))
+    for name in ("mla_tree_accept", "mla_cache_evict"):
+        assert call(L, name, ws_bytes=need - 1) == ARG
+    assert L.mla_cache_evict_workspace_size(ctypes.byref(shape(batch=0))) == 0
+
+
+def test_evict_budgets(L):
+    for k in ("keep", "sink", "recent"):
+        assert call(L, "mla_cache_evict", **{k: -1}) == ARG
+    assert call(L, "mla_cache_evict", keep=8193) == RANGE
