@@ -12,51 +12,49 @@ namespace {
 using tc::pack_bf16;
 
 // CSPLIT warps per row of a split tile, 8 / CSPLIT rows per CTA: warp k of a row merges
-// pieces p0 + k, p0 + k + CSPLIT, ... (with several warps per row, four pieces' loads in
+// pieces k, k + CSPLIT, ... (with several warps per row, four pieces' loads in
 // flight at a time) and the row's warps add their sums in shared memory.  One warp per
 // row suits tiles cut in a few pieces (the chunk shapes); more suit a tile cut across
 // every cluster (decode of a few sequences).  Lane l holds latent dims [16 l, 16 l + 16)
 // (d_c = 512).  The output is the partials weighted by exp(lse_p - lse),
 // lse = log sum_p exp(lse_p), each half of the dims with the log-sum-exps of the CTA half
 // that computed it.
-template <int CSPLIT>
-__global__ void __launch_bounds__(256)
-    combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CombineList cl) {
-  constexpr int CROWS = 8 / CSPLIT;
-  __shared__ float red[CSPLIT > 1 ? 8 * 32 * 17 : 1];     // [row][warp][lane][16 sums + w]
-  tc::grid_dep_wait();                             // the attention's partials are visible
-  tc::grid_dep_launch();
-  const int i = blockIdx.x / (TM / CROWS);
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = wid / CSPLIT, part = wid % CSPLIT;
-  const int r = (blockIdx.x % (TM / CROWS)) * CROWS + rr;
-  const TileGeo tg =
-      tile_geo(a.g, a.n_q, a.q_first, a.k_first, a.n_keys, a.tiles_per_batch, cl.tile[i], a.bn);
-  const bool row_ok = tg.row0 + r < tg.rows_b;
-  const int p0 = cl.piece0[i], p1 = cl.piece0[i + 1];
+//
+// Row r of the tile (if row_ok) becomes row grow of the outputs; piece p of np is in workspace
+// slot slot(p).  NANS: a NaN piece makes the row NaN (draft trees: a node that sees a NaN row),
+// otherwise it counts as empty.
+template <int CSPLIT, bool NANS, typename Slot>
+__device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_lse, float* red,
+                                            int rr, int part, int lane, int r, bool row_ok,
+                                            int64_t grow, int np, const Slot& slot) {
   const int d = lane * 16;
   const int half = d / HALF;                 // the CTA half these dims were computed in
   // each half's largest log-sum-exp over the row's pieces, the lanes taking pieces in turn
   float m0 = -INFINITY, m1 = -INFINITY;
+  bool nan = false;
   if (row_ok)
-    for (int p = p0 + lane; p < p1; p += 32) {
-      m0 = fmaxf(m0, a.ws_lse[((int64_t)p * 2) * TM + r]);
-      m1 = fmaxf(m1, a.ws_lse[((int64_t)p * 2 + 1) * TM + r]);
+    for (int p = lane; p < np; p += 32) {
+      const float l0 = ws_lse[((int64_t)slot(p) * 2) * TM + r];
+      const float l1 = ws_lse[((int64_t)slot(p) * 2 + 1) * TM + r];
+      m0 = fmaxf(m0, l0);
+      m1 = fmaxf(m1, l1);
+      if (NANS) nan = nan || l0 != l0 || l1 != l1;
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
-  const float mx = half ? m1 : m0;
-  const float* lse_h = a.ws_lse + half * TM + r;   // + p * 2 * TM: piece p
+  float mx = half ? m1 : m0;
+  if (NANS && __any_sync(0xffffffffu, nan) && mx == -INFINITY) mx = 0.f;
+  const float* lse_h = ws_lse + half * TM + r;   // + slot * 2 * TM
   float acc[16];
 #pragma unroll
   for (int q = 0; q < 16; ++q) acc[q] = 0.f;
   float wsum = 0.f;
   // a piece's 16 dims of this lane: two 16-byte vectors of bf16
   auto add = [&](float lp, const uint4 (&v)[2]) {
-    const float w = lp > -INFINITY ? expf(lp - mx) : 0.f;
+    const float w = (NANS ? lp != -INFINITY : lp > -INFINITY) ? expf(lp - mx) : 0.f;
     wsum += w;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -69,17 +67,16 @@ __global__ void __launch_bounds__(256)
     }
   };
   if (row_ok && mx > -INFINITY) {
-    int p = p0 + part;
+    int p = part;
     if constexpr (CSPLIT > 1) {
-      for (; p + 3 * CSPLIT < p1; p += 4 * CSPLIT) {
+      for (; p + 3 * CSPLIT < np; p += 4 * CSPLIT) {
         float lp[4];
         uint4 v[4][2];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int pu = p + u * CSPLIT;
-          lp[u] = lse_h[(int64_t)pu * 2 * TM];
-          const uint4* o =
-              reinterpret_cast<const uint4*>(a.ws_o + ((int64_t)pu * TM + r) * a.g.Dc + d);
+          const int64_t pu = slot(p + u * CSPLIT);
+          lp[u] = lse_h[pu * 2 * TM];
+          const uint4* o = reinterpret_cast<const uint4*>(a.ws_o + (pu * TM + r) * a.g.Dc + d);
 #pragma unroll
           for (int q = 0; q < 2; ++q) v[u][q] = o[q];
         }
@@ -87,12 +84,13 @@ __global__ void __launch_bounds__(256)
         for (int u = 0; u < 4; ++u) add(lp[u], v[u]);
       }
     }
-    for (; p < p1; p += CSPLIT) {
+    for (; p < np; p += CSPLIT) {
       uint4 v[2];
-      const uint4* o = reinterpret_cast<const uint4*>(a.ws_o + ((int64_t)p * TM + r) * a.g.Dc + d);
+      const int64_t ps = slot(p);
+      const uint4* o = reinterpret_cast<const uint4*>(a.ws_o + (ps * TM + r) * a.g.Dc + d);
 #pragma unroll
       for (int q = 0; q < 2; ++q) v[q] = o[q];
-      add(lse_h[(int64_t)p * 2 * TM], v);
+      add(lse_h[ps * 2 * TM], v);
     }
   }
   if constexpr (CSPLIT > 1) {
@@ -111,8 +109,8 @@ __global__ void __launch_bounds__(256)
   } else {
     if (!row_ok) return;
   }
-  const int64_t grow = tg.grow0 + r;
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const bool any = NANS ? wsum != 0.f : wsum > 0.f;
+  const float inv = any ? 1.f / wsum : 0.f;
   uint4* dst = reinterpret_cast<uint4*>(a.o_lat + grow * a.g.Dc + d);
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -120,7 +118,95 @@ __global__ void __launch_bounds__(256)
                         pack_bf16(acc[8 * q + 2] * inv, acc[8 * q + 3] * inv),
                         pack_bf16(acc[8 * q + 4] * inv, acc[8 * q + 5] * inv),
                         pack_bf16(acc[8 * q + 6] * inv, acc[8 * q + 7] * inv));
-  if (lane == 0 && a.lse) a.lse[grow] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[grow] = any ? mx + logf(wsum) : -INFINITY;
+}
+
+template <int CSPLIT>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CombineList cl) {
+  constexpr int CROWS = 8 / CSPLIT;
+  __shared__ float red[CSPLIT > 1 ? 8 * 32 * 17 : 1];     // [row][warp][lane][16 sums + w]
+  tc::grid_dep_wait();                             // the attention's partials are visible
+  tc::grid_dep_launch();
+  const int i = blockIdx.x / (TM / CROWS);
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = wid / CSPLIT, part = wid % CSPLIT;
+  const int r = (blockIdx.x % (TM / CROWS)) * CROWS + rr;
+  const TileGeo tg =
+      tile_geo(a.g, a.n_q, a.q_first, a.k_first, a.n_keys, a.tiles_per_batch, cl.tile[i], a.bn);
+  const int p0 = cl.piece0[i];
+  combine_row<CSPLIT, false>(a, a.ws_lse, red, rr, part, lane, r, tg.row0 + r < tg.rows_b, tg.grow0 + r,
+                             cl.piece0[i + 1] - p0, [&](int p) { return p0 + p; });
+}
+
+// Draft trees: the clusters' cuts are known on the device only.  Cut i (the start of cluster i)
+// splits a tile when it lies inside it; the first such cut of a tile stands for the tile, whose
+// pieces are the segment of cluster i - 1 that reached the cut and the first segments of the
+// clusters that start inside it.  Every block lists the split tiles for itself (at most MAXC cuts)
+// and the grid takes their rows in turn.
+template <int CSPLIT>
+__device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws_lse, float* red,
+                                              const int4* cut, const int* first,
+                                              const int* pieces, int n) {
+  constexpr int CROWS = 8 / CSPLIT;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = wid / CSPLIT, part = wid % CSPLIT;
+  for (int it = blockIdx.x; it < n * (TM / CROWS); it += gridDim.x) {
+    const int e = it / (TM / CROWS), i = first[e];
+    const int r = (it % (TM / CROWS)) * CROWS + rr;
+    const int4 c = cut[i], before = cut[i - 1];
+    const Window w = load_window(a.window, c.x, a.g.S, a.n_q);
+    const int64_t row = (int64_t)c.y * TM + r;
+    // the segment before the cut is its cluster's first when that cluster starts this tile
+    const int s0 = 2 * (i - 1) + (before.x == c.x && before.y == c.y ? 0 : 1);
+    combine_row<CSPLIT, true>(a, ws_lse, red, rr, part, lane, r, row < (int64_t)w.nodes * a.g.H,
+                              (int64_t)c.x * a.n_q * a.g.H + row, pieces[e],
+                              [&](int p) { return p == 0 ? s0 : 2 * (i + p - 1); });
+    if (CSPLIT > 1) __syncthreads();               // `red` is the next row's
+  }
+}
+
+__global__ void __launch_bounds__(256)
+    combine_tree_kernel(const __grid_constant__ AttnArgs a, int clusters) {
+  __shared__ float red[8 * 32 * 17];
+  __shared__ int4 cut[MAXC];
+  __shared__ int first[MAXC], pieces[MAXC];
+  __shared__ int n_sh, most_sh;
+  tc::grid_dep_wait();                             // the attention's partials are visible
+  tc::grid_dep_launch();
+  for (int i = threadIdx.x; i < clusters; i += blockDim.x) cut[i] = a.cuts[i];
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int n = 0, most = 0;
+    for (int i0 = 0; i0 < clusters; i0 += 32) {
+      const int i = i0 + threadIdx.x;
+      // a cut inside a tile has a block > 0; the tile's first one stands for it
+      bool is = i > 0 && i < clusters && cut[i].z > 0;
+      if (is) is = !(cut[i - 1].z > 0 && cut[i - 1].x == cut[i].x && cut[i - 1].y == cut[i].y);
+      const unsigned m = __ballot_sync(0xffffffffu, is);
+      if (is) {
+        int k = i + 1;
+        while (k < clusters && cut[k].z > 0 && cut[k].x == cut[i].x && cut[k].y == cut[i].y) ++k;
+        const int e = n + __popc(m & ((1u << threadIdx.x) - 1u));
+        first[e] = i;
+        pieces[e] = k - i + 1;
+        most = max(most, k - i + 1);
+      }
+      n += __popc(m);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (threadIdx.x == 0) {
+      n_sh = n;
+      most_sh = most;
+    }
+  }
+  __syncthreads();
+  if (most_sh >= 32)
+    combine_tiles<8>(a, a.ws_lse, red, cut, first, pieces, n_sh);
+  else if (most_sh >= 8)
+    combine_tiles<4>(a, a.ws_lse, red, cut, first, pieces, n_sh);
+  else
+    combine_tiles<1>(a, a.ws_lse, red, cut, first, pieces, n_sh);
 }
 
 }  // namespace
@@ -135,6 +221,10 @@ cudaError_t launch_combine(const AttnArgs& a, const CombineList& cl, cudaStream_
   if (most >= 8)
     return launch_dependent(combine_kernel<4>, (unsigned)(cl.n * (TM / 2)), 256, 0, st, 1u, a, cl);
   return launch_dependent(combine_kernel<1>, (unsigned)(cl.n * (TM / 8)), 256, 0, st, 1u, a, cl);
+}
+
+cudaError_t launch_combine_tree(const AttnArgs& a, int clusters, cudaStream_t st) {
+  return launch_dependent(combine_tree_kernel, 148u * 4u, 256, 0, st, 1u, a, clusters);
 }
 
 }  // namespace attn

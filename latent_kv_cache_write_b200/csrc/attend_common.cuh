@@ -3,6 +3,7 @@
 #pragma once
 
 #include "launch.h"
+#include "window.cuh"
 
 namespace mla {
 namespace attn {
@@ -31,6 +32,10 @@ struct AttnArgs {
   const float* sc_c;        // [B][S]
   const float* sc_r;        // [B][S]
   int cbits, rbits;
+  // draft trees: ragged windows (null otherwise), and which node sees which
+  const int32_t* window;    // [B][3]
+  const uint8_t* tree;      // [B][n_q][n_q] bytes, or null (a chain)
+  int4* cuts;               // where each cluster starts: (sequence, tile, block), [MAXC]
   unsigned int* err;
 };
 
@@ -63,6 +68,14 @@ struct TileGeo {
   Blocks blk;
 };
 
+// A key range of L logical rows from ring slot p1, in at most two contiguous slot runs.
+__host__ __device__ inline void lay_blocks(Blocks& k, int64_t S, int bn) {
+  k.n1 = k.L < S - k.p1 ? k.L : S - k.p1;
+  k.bn = bn;
+  k.nb1 = (int)((k.n1 + bn - 1) / bn);
+  k.nblk = k.nb1 + (int)((k.L - k.n1 + bn - 1) / bn);
+}
+
 // one past the last key query i sees (frame-block-causal, clipped to the key window)
 __host__ __device__ inline int64_t key_end(const Geo& G, int64_t q_first, int64_t k_lim,
                                            int64_t i) {
@@ -85,10 +98,27 @@ __host__ __device__ inline TileGeo tile_geo(const Geo& G, int64_t n_q, int64_t q
   k.k_first = k_first;
   k.L = key_end(G, q_first, k_first + n_keys, t.i_last) - k_first;
   k.p1 = k_first % G.S;
-  k.n1 = k.L < G.S - k.p1 ? k.L : G.S - k.p1;
-  k.bn = bn;
-  k.nb1 = (int)((k.n1 + bn - 1) / bn);
-  k.nblk = k.nb1 + (int)((k.L - k.n1 + bn - 1) / bn);
+  lay_blocks(k, G.S, bn);
+  return t;
+}
+
+// Draft trees: a sequence's tiles of 128 (node, head) rows, and the key blocks (context, then
+// nodes) that each of them walks.
+struct TreeGeo {
+  int32_t ctx;              // context rows
+  int tiles;
+  Blocks blk;
+};
+
+__device__ __forceinline__ TreeGeo tree_geo(const AttnArgs& a, int64_t b) {
+  const Window w = load_window(a.window, b, a.g.S, a.n_q);
+  TreeGeo t;
+  t.ctx = w.rows;
+  t.tiles = (int)(((int64_t)w.nodes * a.g.H + TM - 1) / TM);
+  t.blk.k_first = 0;                       // global tokens become logical rows
+  t.blk.p1 = w.first;
+  t.blk.L = w.len();
+  lay_blocks(t.blk, a.g.S, a.bn);
   return t;
 }
 
@@ -99,6 +129,11 @@ struct CombineList {
   int32_t tile[MAXC];
   int32_t piece0[MAXC + 1];
 };
+
+// Merge the partials of the tiles that mla_attend_tree's clusters split: cluster c's first
+// segment left its partial in workspace slot 2 c, its last in 2 c + 1 (cuts: a.cuts, `clusters`
+// of them).
+cudaError_t launch_combine_tree(const AttnArgs& a, int clusters, cudaStream_t st);
 
 // Merge the partials of the split tiles listed in `cl` into o_lat (and lse).
 cudaError_t launch_combine(const AttnArgs& a, const CombineList& cl, cudaStream_t st);

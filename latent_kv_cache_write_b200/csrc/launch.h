@@ -130,6 +130,15 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
                            void* workspace, size_t workspace_bytes, unsigned int* err,
                            cudaStream_t st);
 
+// The attention of draft nodes (bf16, d_c = 512, d_R = 64 or 512, at most 6144 sequences).  Its
+// workspace may be null: tiles then stay whole.
+bool tc_attend_tree_supported(const Geo& g);
+size_t tc_attend_tree_workspace(const Geo& g);
+cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                           const int32_t* window, const uint8_t* tree, float scale, void* o_lat,
+                           float* lse, void* workspace, size_t workspace_bytes, unsigned int* err,
+                           cudaStream_t st);
+
 // Draft trees over ragged windows (tree_simt.cu): attention of the nodes, and the attention
 // weight every row of the windows received.
 cudaError_t simt_attend_tree(const Geo& g, bool bf, const void* q_abs, int64_t n_nodes,

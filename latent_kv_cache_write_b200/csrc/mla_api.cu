@@ -439,7 +439,10 @@ mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const v
 }
 
 size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes) {
-  (void)shape; (void)n_nodes;
+  (void)n_nodes;
+  Geo g;
+  if (check_shape(shape, &g) != MLA_OK) return 0;
+  if (shape->dtype == MLA_BF16 && tc_attend_tree_supported(g)) return tc_attend_tree_workspace(g);
   return 0;
 }
 
@@ -458,6 +461,10 @@ mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_
   if (workspace && !aligned16(workspace)) return MLA_ERR_ALIGN;
   if (n_nodes == 0) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
+  if (bf && tc_attend_tree_supported(g))
+    return cuda_status(tc_attend_tree(g, q_abs, n_nodes, cache, window, tree, softmax_scale, o_lat,
+                                      lse, workspace, workspace_bytes, device_error_word(),
+                                      (cudaStream_t)stream));
   return cuda_status(simt_attend_tree(g, bf, q_abs, n_nodes, cache, window, tree, softmax_scale,
                                       o_lat, lse, (cudaStream_t)stream));
 }

@@ -129,7 +129,9 @@ struct Lay {
   static constexpr int B_SGE = B_SGF + NSG;    // staging slot read (64)               [NSG]
   static constexpr int NBAR = B_SGE + NSG;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 48 + 1024;   // TMEM slot, abort flag, votes [2][4]
+  // draft trees: (sequence, tile) of each round, behind the TMEM slot, abort flag, votes [2][4]
+  static constexpr int OFF_ROUNDS = OFF_MISC + 48;
+  static constexpr int SMEM = OFF_ROUNDS + 32 * 8 + 1024;
   static_assert(SMEM <= 227 * 1024, "dynamic shared memory of one CTA");
   static_assert(OFF_SG % 1024 == 0 && OFF_SGR % 128 == 0 && OFF_SGS % 128 == 0 &&
                 OFF_QR % 1024 == 0 && OFF_X % 1024 == 0 && OFF_P % 1024 == 0,
@@ -192,6 +194,262 @@ struct SegWalk {
     load(a);
   }
 };
+
+// Draft trees: the windows are known on the device only, so every CTA plans for itself.  The key
+// blocks of all tiles, sequence after sequence, make one line of W blocks.  Cluster c of G gets an
+// equal share of it in two parts:
+//   - a head of R rounds, tile c + r G in round r.  The clusters then work on G neighbouring tiles
+//     at a time, which share the keys of a few sequences: each key block comes from HBM about
+//     once, however many tiles a sequence has.  R is the largest number of rounds (at most
+//     TREE_MAXR) that leaves no cluster with more blocks than its share;
+//   - a tail: a range [p0, p1) of the line's rest, which evens out what the rounds left uneven
+//     and may start and end inside tiles.
+// Rounds are taken only when the sequences' keys crowd L2 and sequences have several tiles
+// (sc.l2_blocks); otherwise R = 0 and a cluster's share is one range.
+struct TreeSched {
+  int split;                // tiles may be split (there is a workspace)
+  int64_t l2_blocks;        // key blocks beyond which tiles go in rounds
+};
+
+constexpr int TREE_MAXB = 6144;                // sequences the plan's arrays hold
+constexpr int TREE_MAXR = 32;                  // rounds
+// The plan's arrays (shared memory, where the K/V ring will be), and what stays of it: the
+// sequence and tile of each round.
+struct TreePlan {
+  int64_t pre[TREE_MAXB];                      // blocks of the line up to each sequence's end
+  int32_t tpre[TREE_MAXB];                     // tiles likewise
+  int32_t nblk[TREE_MAXB];                     // key blocks of each sequence's tiles
+};
+struct TreeScratch {                           // shared memory, next to the plan
+  int64_t start[MAXC + 1];                     // where each cluster's tail starts
+  int64_t sums[2][16];
+  unsigned long long cost[2], keys;
+  int rounds;
+};
+
+// The first sequence whose part of a line ends past p.
+template <typename T>
+__device__ __forceinline__ int tree_find(const T* pre, int B, int64_t p) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] > p) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// The segments of one cluster's share, as SegWalk.  A cluster has at most two partial segments,
+// the first and the last of its tail: workspace slots 2 c and 2 c + 1.
+struct TreeWalk {
+  int64_t left;             // blocks of the tail from its current segment on
+  int r, R;                 // round, rounds
+  const int2* rounds;       // (sequence, tile) of each round
+  int tail_b, tail_tb, tail_jb;
+  int tb, tiles, jb, je;    // tile of the sequence, its tiles, this segment's blocks
+  int ctx;                  // context rows of the sequence
+  int k, gbase, nbase[2], slot;
+  TileGeo tg;
+
+  __device__ void begin(const AttnArgs& a, const TreePlan& pl, const int2* list, int n_rounds,
+                        int64_t p0, int64_t p1, int c) {
+    k = 0;
+    gbase = 0;
+    nbase[0] = nbase[1] = 0;
+    slot = 2 * c;
+    r = 0;
+    R = n_rounds;
+    rounds = list;
+    left = p1 - p0;
+    tail_b = tail_tb = -1;
+    tail_jb = 0;
+    if (left > 0) {
+      tail_b = tree_find(pl.pre, a.g.B, p0);
+      const int64_t rem = p0 - (tail_b ? pl.pre[tail_b - 1] : 0);
+      tail_tb = (int)(rem / pl.nblk[tail_b]);
+      tail_jb = (int)(rem - (int64_t)tail_tb * pl.nblk[tail_b]);
+    }
+    load(a);
+  }
+  __device__ void sequence(const AttnArgs& a, int b) {
+    const TreeGeo s = tree_geo(a, b);
+    tiles = s.tiles;
+    ctx = s.ctx;
+    tg.blk = s.blk;
+    tg.b = b;
+    tg.rows_b = (int64_t)(s.blk.L - s.ctx) * a.g.H;
+  }
+  __device__ void tile(const AttnArgs& a, int from, int64_t most) {
+    tg.row0 = (int64_t)tb * TM;
+    tg.grow0 = (int64_t)tg.b * a.n_q * a.g.H + tg.row0;
+    jb = from;
+    je = (int64_t)(tg.blk.nblk - from) < most ? tg.blk.nblk : from + (int)most;
+  }
+  // the segment of round r, or the tail's first
+  __device__ void load(const AttnArgs& a) {
+    if (r < R) {
+      const int2 e = rounds[r];
+      sequence(a, e.x);
+      tb = e.y;
+      tile(a, 0, tg.blk.nblk);
+    } else if (left > 0) {
+      sequence(a, tail_b);
+      tb = tail_tb;
+      tile(a, tail_jb, left);
+    }
+  }
+  __device__ bool valid() const { return r < R || left > 0; }
+  __device__ int nb() const { return je - jb; }
+  __device__ int done_by(int w) const { return w ? nbase[1] : nbase[0]; }
+  __device__ bool partial() const { return jb > 0 || je < tg.blk.nblk; }
+  __device__ void next(const AttnArgs& a) {
+    const int n = nb();
+    gbase += n;
+    nbase[0] += (n + 1) >> 1;
+    nbase[1] += n >> 1;
+    ++k;
+    if (r < R) {
+      ++r;
+      load(a);
+      return;
+    }
+    slot |= 1;
+    left -= n;
+    if (left <= 0) return;
+    if (++tb >= tiles) {
+      tb = 0;
+      int b = tg.b;
+      do {
+        sequence(a, ++b);                      // left > 0: a later sequence has tiles
+      } while (tiles == 0);
+    }
+    tile(a, 0, left);
+  }
+};
+
+// Costs of the two schedules in key blocks: a cluster's blocks plus SEG_COST per segment it walks
+// (the switch: Q reload, output epilogue, pipeline refill), plus COMBINE_COST when tiles are
+// split (the merge).  Measured on B200 (video chunk, long window and decode shapes).
+constexpr int64_t SEG_COST = 7, COMBINE_COST = 16;
+
+// Exclusive sum of v over the CTA's NT threads (every thread calls it).
+template <int NT>
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(FULL, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  __syncthreads();
+  return before + x - v;
+}
+
+// Plan of cluster c of G: its rounds (list, returned count) and its tail [p0, p1).  Every thread of
+// the CTA takes part.
+template <int NT>
+__device__ __forceinline__ int tree_plan(const AttnArgs& a, const TreeSched& sc, TreePlan& pl,
+                                         TreeScratch& x, int2* list, int G, int c, int64_t& p0,
+                                         int64_t& p1) {
+  const int t = threadIdx.x, B = a.g.B;
+  const int per = (B + NT - 1) / NT;
+  if (t == 0) {
+    x.cost[0] = x.cost[1] = x.keys = 0ull;
+    x.rounds = INT32_MAX;
+  }
+  int64_t blocks = 0;
+  int tiles = 0;
+  unsigned long long keys = 0;
+  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
+    const TreeGeo s = tree_geo(a, b);
+    blocks += (int64_t)s.tiles * s.blk.nblk;
+    tiles += s.tiles;
+    if (s.tiles > 0) keys += s.blk.nblk;
+    pl.pre[b] = blocks;
+    pl.tpre[b] = tiles;
+    pl.nblk[b] = s.blk.nblk;
+  }
+  const int64_t ob = cta_scan<NT>(blocks, x.sums[0]);
+  const int ot = (int)cta_scan<NT>(tiles, x.sums[1]);
+  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
+    pl.pre[b] += ob;
+    pl.tpre[b] += ot;
+  }
+  if (keys) atomicAdd(&x.keys, keys);
+  __syncthreads();
+  const int64_t W = pl.pre[B - 1], T = pl.tpre[B - 1];
+  p0 = p1 = 0;
+  if (W == 0) return 0;
+  // thread u < G: cluster u's share, and the blocks of its first rounds
+  const int64_t share = t < G ? W * (t + 1) / G - W * t / G : 0;
+  auto round_blocks = [&](int u, int r) { return pl.nblk[tree_find(pl.tpre, B, (int64_t)r * G + u)]; };
+  const bool waves = (int64_t)x.keys > sc.l2_blocks && a.tiles_per_batch > 2;
+  const int most = (int)(T / G < TREE_MAXR ? T / G : TREE_MAXR);
+  if (waves && t < G) {
+    int r = 0;
+    for (int64_t d = 0; r < most; ++r) {
+      d += round_blocks(t, r);
+      if (d > share) break;
+    }
+    atomicMin(&x.rounds, r);
+  }
+  __syncthreads();
+  const int R = waves ? x.rounds : 0;
+  int64_t head = 0;
+  if (t < G)
+    for (int r = 0; r < R; ++r) head += round_blocks(t, r);
+  const int64_t rest = share - head;           // the tail's blocks
+  const int64_t before = cta_scan<NT>(rest, x.sums[0]);
+  // the rounds took the first R G tiles; the tails share the rest of the line
+  const int64_t done = (int64_t)R * G;
+  int64_t line = 0;
+  if (done > 0) {
+    const int b = tree_find(pl.tpre, B, done - 1);
+    line = (b ? pl.pre[b - 1] : 0) + (done - (b ? pl.tpre[b - 1] : 0)) * pl.nblk[b];
+  }
+  if (t < G) x.start[t] = line + before;
+  if (t == 0) x.start[G] = W;
+  __syncthreads();
+  // cuts on tile boundaries: the first one at or past the cut
+  auto up = [&](int64_t p) {
+    const int b = tree_find(pl.pre, B, p);
+    if (p >= pl.pre[b]) return pl.pre[b];      // p == W
+    const int64_t s = b ? pl.pre[b - 1] : 0, n = pl.nblk[b];
+    return s + (p - s + n - 1) / n * n;
+  };
+  if (sc.split && t < G) {
+    auto tile_at = [&](int64_t p) {
+      const int b = tree_find(pl.pre, B, p);
+      return (b ? pl.tpre[b - 1] : 0) + (p - (b ? pl.pre[b - 1] : 0)) / pl.nblk[b];
+    };
+    auto charge = [&](unsigned long long* into, int64_t s, int64_t e) {
+      const int64_t segs = R + (e > s ? tile_at(e - 1) - tile_at(s) + 1 : 0);
+      atomicMax(into, (unsigned long long)(head + (e - s) + SEG_COST * segs));
+    };
+    charge(&x.cost[0], x.start[t], x.start[t + 1]);
+    charge(&x.cost[1], up(x.start[t]), up(x.start[t + 1]));
+  }
+  __syncthreads();
+  p0 = x.start[c];
+  p1 = x.start[c + 1];
+  if (!sc.split || x.cost[0] + COMBINE_COST >= x.cost[1]) {
+    p0 = up(p0);
+    p1 = up(p1);
+  }
+  for (int r = t; r < R; r += NT) {
+    const int64_t tile = (int64_t)r * G + c;
+    const int b = tree_find(pl.tpre, B, tile);
+    list[r] = make_int2(b, (int)(tile - (b ? pl.tpre[b - 1] : 0)));
+  }
+  return R;
+}
+
+template <bool TREE> struct SchedOf { using S = Sched; using Walk = SegWalk; };
+template <> struct SchedOf<true> { using S = TreeSched; using Walk = TreeWalk; };
 
 __device__ __forceinline__ void rescale_row(uint32_t taddr, float f) {
 #pragma unroll 1
@@ -287,12 +545,47 @@ __device__ __forceinline__ uint4 dq8_int2(uint32_t w, uint32_t s2) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int V>
+// Bits c = 0 .. 63 of a key block of a draft tree: whether node i sees the block's key c.  The
+// first `nctx` keys are context, then come nodes k0, k0 + 1, ...; `valid` keys in all.
+__device__ __forceinline__ uint64_t tree_bits(const AttnArgs& a, int64_t b, int64_t i, int nctx,
+                                              int64_t k0, int valid) {
+  uint64_t bits = nctx >= 64 ? ~0ull : (1ull << nctx) - 1ull;
+  const int n = valid - nctx;                  // nodes among the keys
+  if (n <= 0) return bits;
+  uint64_t nodes = 0;
+  if (a.tree == nullptr) {
+    const int64_t m = i - k0 + 1;              // a chain: nodes k0 .. i
+    nodes = m <= 0 ? 0ull : (m >= 64 ? ~0ull : (1ull << m) - 1ull);
+    nodes &= n >= 64 ? ~0ull : (1ull << n) - 1ull;
+  } else {
+    const uint8_t* row = a.tree + (b * a.n_q + i) * a.n_q + k0;
+#pragma unroll 8
+    for (int e = 0; e < n; ++e) nodes |= (uint64_t)(row[e] != 0) << e;
+  }
+  return bits | nodes << nctx;                 // nctx < 64 here
+}
+
+// Non-finite bf16 values of a 16-byte vector -> 0.
+__device__ __forceinline__ uint4 finite8(uint4 v) {
+  auto fix = [](uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+  };
+  return make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
+}
+
+// TREE: the draft-tree form of a variant (mla_attend_tree).  The walk over ragged windows is
+// planned on the device, rows are masked by the tree in the blocks that hold nodes, and the node
+// rows of such a block are made finite before the PV product: a hidden row's weight is 0, but
+// 0 * NaN would still reach every row of the tile.  (A node that does see a NaN row gets it
+// through its scores.)
+template <int V, bool TREE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmKR,
                   const __grid_constant__ CUtensorMap tmQR, const __grid_constant__ CUtensorMap tmSC,
                   const __grid_constant__ CUtensorMap tmSR, const __grid_constant__ AttnArgs a,
-                  const __grid_constant__ Sched sc) {
+                  const __grid_constant__ typename SchedOf<TREE>::S sc) {
   using LY = Lay<V>;
   constexpr int NST = LY::NST, NSTR = LY::NSTR;
   constexpr int BN = LY::BNK, BOX_BYTES = LY::BOXB, RBOX_BYTES = LY::RBB;
@@ -357,8 +650,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
   grid_dep_wait();                               // the previous kernel's outputs are visible
   grid_dep_launch();
 
-  SegWalk sw;
-  sw.begin(sc, a, blockIdx.x >> 1);
+  using Walk = typename SchedOf<TREE>::Walk;
+  Walk sw;
+  if constexpr (TREE) {
+    // the plan's arrays lie where the K/V ring will be and its scratch where Q's RoPE part will
+    // (no peer writes into either); the list of rounds stays
+    TreePlan& pl = *reinterpret_cast<TreePlan*>(sm + OFF_KV);
+    TreeScratch& x = *reinterpret_cast<TreeScratch*>(sm + OFF_QR);
+    int2* list = reinterpret_cast<int2*>(sm + LY::OFF_ROUNDS);
+    static_assert(sizeof(TreePlan) <= LY::NST * LY::LATB && sizeof(TreeScratch) <= LY::QRB,
+                  "the plan fits the K/V ring, its scratch Q's RoPE part");
+    int64_t p0, p1;
+    const int c = (int)(blockIdx.x >> 1);
+    const int R = tree_plan<LY::NT>(a, sc, pl, x, list, (int)(gridDim.x >> 1), c, p0, p1);
+    __syncthreads();                // the list is complete
+    sw.begin(a, pl, list, R, p0, p1, c);
+    if (tid == 0 && rank == 0 && a.cuts)
+      a.cuts[c] = make_int4(sw.tail_b, sw.tail_tb, sw.tail_jb, 0);
+    fence_proxy_async_smem();      // the arrays are read before TMA writes over them
+    __syncthreads();
+  } else {
+    sw.begin(sc, a, blockIdx.x >> 1);
+  }
 
   if (LY::PACKED && (warp == 8 || warp == 11)) {
     // ------------------------------------------------------------ dequantising producers
@@ -371,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     const int cb = a.cbits;                       // 4 or 2; RoPE codes are 4 bits
     const int chalf = HALF * cb / 8;              // content bytes of a row for this CTA
     const bool issuer = warp == 8 && lane == 0;
-    SegWalk iw = sw;                              // the issuer's walk, NSG blocks ahead
+    Walk iw = sw;                                 // the issuer's walk, NSG blocks ahead
     int ij = iw.valid() ? iw.jb : 0, issued = 0;
     auto issue_next = [&]() -> bool {
       if (!iw.valid()) return true;
@@ -676,13 +989,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       const int64_t r_in_b = tg.row0 + t;
       const bool row_valid = r_in_b < tg.rows_b;
       const int64_t grow = tg.grow0 + t;
-      const int64_t k_end_row =
-          key_end(G, a.q_first, a.k_first + a.n_keys, row_valid ? r_in_b / G.H : tg.i_last);
+      int64_t k_end_row = 0, node = 0;
+      if constexpr (TREE)
+        node = row_valid ? r_in_b / G.H : 0;
+      else
+        k_end_row = key_end(G, a.q_first, a.k_first + a.n_keys, row_valid ? r_in_b / G.H : tg.i_last);
       const int n = sw.nb();
       {
         // the next segment's Q rows (this CTA's latent half, this warpgroup's half of it)
         // into L2 now, so that their load into TMEM at the segment's end is short
-        SegWalk nx = sw;
+        Walk nx = sw;
         nx.next(a);
         if (nx.valid() && nx.tg.row0 + t < nx.tg.rows_b) {
           const char* qrow = reinterpret_cast<const char*>(
@@ -766,6 +1082,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           }
         }
 
+        // a block with draft nodes: which of its keys this row sees, and finite node rows
+        int nctx = BN;                                 // context keys of the block
+        uint64_t sees = ~0ull;
+        if constexpr (TREE) {
+          const int64_t c64 = (int64_t)sw.ctx - g0;
+          nctx = c64 >= valid ? valid : (c64 < 0 ? 0 : (int)c64);
+          if (nctx < BN) {
+            sees = tree_bits(a, tg.b, node, nctx, c64 < 0 ? -c64 : 0, valid);
+            if (t < valid && t >= nctx) {
+              uint8_t* st = sm + OFF_KV + ((sw.gbase + jl) % NST) * BOX_BYTES + t * 128;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
+#pragma unroll
+                for (int w = 0; w < 8; ++w) p[w] = finite8(p[w]);
+              }
+            }
+          }
+        }
+
         // full scores: add the peer's partial
         if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], xc & 1, abort, a.err, 0x203,
                                                  (t << 16) | j))) {
@@ -842,11 +1178,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         }
 
         // masked raw maximum (scores are scaled inside the exponent)
-        const int64_t lim64 = k_end_row - g0;
-        const int lim = lim64 < valid ? (lim64 < 0 ? 0 : (int)lim64) : valid;
-        if (lim < BN) {
+        if constexpr (TREE) {
+          if (nctx < BN) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+            for (int c = 0; c < BN; ++c) s[c] = (sees >> c & 1) ? s[c] : -INFINITY;
+          }
+        } else {
+          const int64_t lim64 = k_end_row - g0;
+          const int lim = lim64 < valid ? (lim64 < 0 ? 0 : (int)lim64) : valid;
+          if (lim < BN) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+          }
         }
         float rm[8];
 #pragma unroll
@@ -927,7 +1270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       // the next segment's Q may enter TMEM once this segment's score MMAs are done
       const uint32_t kph = sw.k & 1;
       {
-        SegWalk nx = sw;
+        Walk nx = sw;
         nx.next(a);
         if (nx.valid()) {
           if (!__all_sync(FULL, mbar_wait(&bar[B_QKDONE], kph, abort, a.err, 0x301, t))) break;
@@ -949,12 +1292,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       named_bar(3, 2 * TM);
       const float mf = fmaxf(m_last, m_sh[(wg ^ 1) * TM + t]);
       named_bar(3, 2 * TM);
-      m_sh[wg * TM + t] = m_last > -INFINITY ? l * ex2(m_last - mf) : 0.f;
+      // (TREE: a NaN maximum or sum stays NaN)
+      const bool some = TREE ? m_last != -INFINITY : m_last > -INFINITY;
+      m_sh[wg * TM + t] = some ? l * ex2(m_last - mf) : 0.f;
       named_bar(3, 2 * TM);
       const float lt = m_sh[t] + m_sh[TM + t];
       named_bar(3, 2 * TM);                  // both have read: the array is the next segment's
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      const float lse_v = lt > 0.f ? (mf + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
+      const bool any = TREE ? lt != 0.f : lt > 0.f;
+      const float inv = any ? 1.f / lt : 0.f;
+      const float lse_v = any ? (mf + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
       const bool part = sw.partial();
       if (wg == 0 && row_valid) {
         if (part)
@@ -1049,9 +1395,11 @@ int cluster_slots() {
     if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c < 1) c = 0;
     n = c < n ? c : n;
   };
-  probe(attend_kernel<0>, Lay<0>::SMEM, Lay<0>::NT);
-  probe(attend_kernel<1>, Lay<1>::SMEM, Lay<1>::NT);
-  probe(attend_kernel<2>, Lay<2>::SMEM, Lay<2>::NT);
+  probe(attend_kernel<0, false>, Lay<0>::SMEM, Lay<0>::NT);
+  probe(attend_kernel<1, false>, Lay<1>::SMEM, Lay<1>::NT);
+  probe(attend_kernel<2, false>, Lay<2>::SMEM, Lay<2>::NT);
+  probe(attend_kernel<0, true>, Lay<0>::SMEM, Lay<0>::NT);
+  probe(attend_kernel<1, true>, Lay<1>::SMEM, Lay<1>::NT);
   if (!ok) return 0;
   if (n < 1) {
     int sms = 0;
@@ -1089,6 +1437,37 @@ cudaError_t tc_attend(const Geo& g, const void* q_abs, int64_t n_q, int64_t q_fi
                         lse, workspace, workspace_bytes, err, st);
 }
 
+namespace {
+
+// Maps of a bf16 ring and of Q's RoPE part.  K: 64-dim boxes of bn cached rows (the latent
+// boxes, and the wide RoPE boxes); KR: the 32-dim RoPE box of d_R = 64 (64-byte swizzle); QR:
+// one 32-dim box (64-byte swizzle), or 64-dim boxes (wide).
+bool ring_maps(const Geo& g, const void* cache, int bn, CUtensorMap* K, CUtensorMap* KR) {
+  uint64_t d[3] = {(uint64_t)g.row, (uint64_t)g.S, (uint64_t)g.B};
+  uint64_t s[2] = {(uint64_t)g.row * 2, (uint64_t)g.S * g.row * 2};
+  uint32_t b[3] = {64, (uint32_t)bn, 1};
+  uint32_t br[3] = {32, (uint32_t)bn, 1};
+  return make_tmap_bf16(K, cache, 3, d, s, b) && make_tmap_bf16(KR, cache, 3, d, s, br, true);
+}
+bool query_map(const Geo& g, const void* q_abs, int64_t n_q, bool wide, CUtensorMap* QR) {
+  uint64_t d[2] = {(uint64_t)g.row, (uint64_t)g.B * n_q * g.H};
+  uint64_t s[1] = {(uint64_t)g.row * 2};
+  uint32_t b[2] = {wide ? 64u : 32u, TM};
+  return make_tmap_bf16(QR, q_abs, 2, d, s, b, !wide);
+}
+
+// The 16-bit exchange rounds a partial score to within 2^-11 of itself.  Up to XCHG_LOG2 in the
+// exponent's log2 units that error stays below 2^-8 of one such unit (a few tenths of a percent
+// of a softmax weight, like the bf16 rounding of P); rows with larger partials get the exact
+// exchange.  Capped well inside the fp16 range.
+float exchange_threshold(float scale_log2) {
+  constexpr float XCHG_LOG2 = 8.f;
+  const float thr = XCHG_LOG2 / scale_log2;
+  return thr <= 32768.f ? thr : 32768.f;
+}
+
+}  // namespace
+
 cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t q_first,
                            const void* cache, const PackedRing* pk, int64_t k_first,
                            int64_t n_keys, float scale, void* o_lat, float* lse,
@@ -1125,39 +1504,17 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
           !make_tmap_raw(&SR, pk->scale_r, true, 1, d, nullptr, b, 0))
         return cudaErrorInvalidValue;
     }
-  } else {
-    // K: 64-dim boxes of bn cached rows (the latent boxes, and the wide RoPE boxes);
-    // KR: the 32-dim RoPE box of d_R = 64 (64-byte swizzle)
-    uint64_t d[3] = {(uint64_t)g.row, (uint64_t)g.S, (uint64_t)g.B};
-    uint64_t s[2] = {(uint64_t)g.row * 2, (uint64_t)g.S * g.row * 2};
-    uint32_t b[3] = {64, (uint32_t)bn, 1};
-    if (!make_tmap_bf16(&K, cache, 3, d, s, b)) return cudaErrorInvalidValue;
-    uint32_t br[3] = {32, (uint32_t)bn, 1};
-    if (!make_tmap_bf16(&KR, cache, 3, d, s, br, true)) return cudaErrorInvalidValue;
+  } else if (!ring_maps(g, cache, bn, &K, &KR)) {
+    return cudaErrorInvalidValue;
   }
-  {
-    // Q's RoPE part: one 32-dim box (64-byte swizzle), or 64-dim boxes (wide)
-    uint64_t d[2] = {(uint64_t)g.row, (uint64_t)g.B * n_q * g.H};
-    uint64_t s[1] = {(uint64_t)g.row * 2};
-    uint32_t b[2] = {variant == 1 ? 64u : 32u, TM};
-    if (!make_tmap_bf16(&QR, q_abs, 2, d, s, b, variant != 1)) return cudaErrorInvalidValue;
-  }
+  if (!query_map(g, q_abs, n_q, variant == 1, &QR)) return cudaErrorInvalidValue;
   const int ncl = cluster_slots();
   if (ncl == 0) return cudaErrorInvalidDevice;
   AttnArgs a{};
   a.g = g;
   a.n_q = n_q; a.q_first = q_first; a.k_first = k_first; a.n_keys = n_keys;
   a.scale_log2 = scale * 1.4426950408889634f;
-  {
-    // The 16-bit exchange rounds a partial score to within 2^-11 of itself.  Up to
-    // XCHG_LOG2 in the exponent's log2 units that error stays below 2^-8 of one such unit
-    // (a few tenths of a percent of a softmax weight, like the bf16 rounding of P); rows
-    // with larger partials get the exact exchange.  Capped well inside the fp16 range.
-    constexpr float XCHG_LOG2 = 8.f;
-    float thr = XCHG_LOG2 / a.scale_log2;
-    if (!(thr <= 32768.f)) thr = 32768.f;
-    a.xthr = thr;
-  }
+  a.xthr = exchange_threshold(a.scale_log2);
   a.q_abs = (const bf16*)q_abs;
   a.o_lat = (bf16*)o_lat;
   a.lse = lse;
@@ -1224,11 +1581,7 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
       pre[t + 1] = pre[t] + nbt[t];
     }
     const int64_t W = pre[Tg];
-    // Two candidate schedules, costed in key blocks: a cluster's blocks plus SEG_COST per
-    // segment it walks (the switch: Q reload, output epilogue, pipeline refill), plus
-    // COMBINE_COST when tiles are split (the merge launch).  Both costs were measured on
-    // B200 (video chunk, long window and decode shapes).
-    constexpr int64_t SEG_COST = 7, COMBINE_COST = 16;
+    // Two candidate schedules, costed in key blocks (SEG_COST, COMBINE_COST).
     // schedules below are in group-relative tiles until they are shifted for the launch
     auto cost = [&](const Sched& c, int nc) {
       int64_t worst = 0;
@@ -1316,13 +1669,13 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
   for (const Plan& p : plans) {
     cudaError_t e;
     if (variant == 2)
-      e = launch_dependent(attend_kernel<2>, (unsigned)(2 * p.G), Lay<2>::NT, Lay<2>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<2, false>, (unsigned)(2 * p.G), Lay<2>::NT, Lay<2>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     else if (variant == 1)
-      e = launch_dependent(attend_kernel<1>, (unsigned)(2 * p.G), Lay<1>::NT, Lay<1>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<1, false>, (unsigned)(2 * p.G), Lay<1>::NT, Lay<1>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     else
-      e = launch_dependent(attend_kernel<0>, (unsigned)(2 * p.G), Lay<0>::NT, Lay<0>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<0, false>, (unsigned)(2 * p.G), Lay<0>::NT, Lay<0>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     if (e != cudaSuccess) return e;
     count_launches(1);
@@ -1333,6 +1686,66 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
     }
   }
   return cudaSuccess;
+}
+
+bool tc_attend_tree_supported(const Geo& g) {
+  return tc_attend_supported(g) && g.B <= TREE_MAXB;
+}
+
+size_t tc_attend_tree_workspace(const Geo& g) {
+  return tc_attend_workspace(g) + MAXC * sizeof(int4);
+}
+
+cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                           const int32_t* window, const uint8_t* tree, float scale, void* o_lat,
+                           float* lse, void* workspace, size_t workspace_bytes, unsigned int* err,
+                           cudaStream_t st) {
+  const bool wide = g.Dr == 2 * Lay<1>::RHALF;
+  const int ncl = cluster_slots();
+  if (ncl == 0) return cudaErrorInvalidDevice;
+  AttnArgs a{};
+  a.bn = wide ? Lay<1>::BNK : Lay<0>::BNK;
+  CUtensorMap K{}, KR{}, QR{};
+  if (!ring_maps(g, cache, a.bn, &K, &KR) || !query_map(g, q_abs, n_nodes, wide, &QR))
+    return cudaErrorInvalidValue;
+  a.g = g;
+  a.n_q = n_nodes;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.xthr = exchange_threshold(a.scale_log2);
+  a.q_abs = (const bf16*)q_abs;
+  a.o_lat = (bf16*)o_lat;
+  a.lse = lse;
+  a.tiles_per_batch = (int)((n_nodes * g.H + TM - 1) / TM);
+  a.pf = a.tiles_per_batch <= 2 ? PF_BLOCKS : 0;      // as in tc_attend_ring
+  a.window = window;
+  a.tree = tree;
+  a.err = err;
+  TreeSched sc{workspace && workspace_bytes >= tc_attend_tree_workspace(g) ? 1 : 0, INT64_MAX};
+  {
+    // keys beyond a third of L2 are read again from HBM by every tile that comes to them later
+    int dev = 0, l2 = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) == cudaSuccess && l2 > 0)
+      sc.l2_blocks = l2 / 3 / ((int64_t)a.bn * g.row * 2);
+  }
+  if (sc.split) {
+    a.ws_o = (bf16*)workspace;
+    a.ws_lse = reinterpret_cast<float*>(a.ws_o + (size_t)2 * ncl * TM * g.Dc);
+    a.cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + tc_attend_workspace(g));
+  }
+  cudaError_t e;
+  if (wide)
+    e = launch_dependent(attend_kernel<1, true>, (unsigned)(2 * ncl), Lay<1>::NT, Lay<1>::SMEM, st,
+                         1u, K, KR, QR, CUtensorMap{}, CUtensorMap{}, a, sc);
+  else
+    e = launch_dependent(attend_kernel<0, true>, (unsigned)(2 * ncl), Lay<0>::NT, Lay<0>::SMEM, st,
+                         1u, K, KR, QR, CUtensorMap{}, CUtensorMap{}, a, sc);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  if (!sc.split) return cudaSuccess;
+  e = launch_combine_tree(a, ncl, st);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 }  // namespace mla

@@ -149,6 +149,33 @@ def test_attend_clips_windows(cuda_ok, cfg):
     check_attend(wl, q.values, c.values, windows, see, n, o, lse)
 
 
+@pytest.mark.parametrize("cfg,nodes", [("HEADS", (9, 3, 8, 1, 9, 5, 0, 7)),
+                                       ("HEADS", (64, 60, 64, 33, 64, 1, 64, 64)),
+                                       ("WIDE", (40, 64, 33, 64, 50, 3, 64, 64))])
+def test_attend_in_rounds(cuda_ok, cfg, nodes):
+    """Keys that crowd L2, so that tiles are handed out in rounds: whole tiles give the bits of one
+    call per sequence (whose schedule has no rounds), split tiles one more bf16 rounding."""
+    B, n, S = 8, max(nodes), 8192
+    rows = [8000, 61, 7777, 8128, 5000, 8064, 8000, 6500]
+    wl = T.workload(dict(getattr(T, cfg), n_heads=128), B, S)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    q = torch.randn((B, n, 128, wl.row_width), device=DEV, generator=g).bfloat16()
+    c = torch.randn((B, S, wl.row_width), device=DEV, generator=g).bfloat16()
+    _, see = T.random_tree(np.random.default_rng(4), B, n)
+    tree = tree_dev(see)
+    windows = [(1000 * b, r, m) for b, (r, m) in enumerate(zip(rows, nodes))]
+    o, lse = attend(wl, q, c, windows, tree, n, split=False)
+    one = wl.scaled(batch=1)
+    for b in range(B):
+        ob, lb = attend(one, q[b:b + 1], c[b:b + 1], windows[b:b + 1], tree[b:b + 1], n, split=False)
+        assert torch.equal(ob[0], o[b]) and torch.equal(lb[0], lse[b])
+    os_, ls = attend(wl, q, c, windows, tree, n, split=True)
+    # each piece and the merged row round once more; a merged row is a mean of its pieces
+    scale = o.float().abs().amax(-1, keepdim=True)
+    assert ((os_.float() - o.float()).abs() <= 4 * T.BF16 * scale).all()
+    assert ((ls - lse).abs() <= 2.0 ** -12).all()
+
+
 @pytest.mark.parametrize("cfg", ["MAIN", "WIDE"])
 def test_attend_large_scores(cuda_ok, cfg):
     """Scores of hundreds and partial sums of 10^5 (the exact exchange), one key winning."""
