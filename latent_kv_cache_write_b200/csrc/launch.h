@@ -139,6 +139,13 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
                            float* lse, void* workspace, size_t workspace_bytes, unsigned int* err,
                            cudaStream_t st);
 
+// The attention weight of cached rows (tc_weight.cu; the same shapes).
+bool tc_attend_weight_supported(const Geo& g);
+cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                             const int32_t* window, const uint8_t* tree, float scale,
+                             const float* lse, const float* qw, const float* win, float* wout,
+                             unsigned int* err, cudaStream_t st);
+
 // Draft trees over ragged windows (tree_simt.cu): attention of the nodes, and the attention
 // weight every row of the windows received.
 cudaError_t simt_attend_tree(const Geo& g, bool bf, const void* q_abs, int64_t n_nodes,

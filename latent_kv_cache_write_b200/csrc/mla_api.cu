@@ -481,6 +481,10 @@ mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t 
     return MLA_ERR_ALIGN;
   if (n_nodes == 0) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
+  if (bf && tc_attend_weight_supported(g))
+    return cuda_status(tc_attend_weight(g, q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
+                                        query_weight, weight_in, weight_out, device_error_word(),
+                                        (cudaStream_t)stream));
   return cuda_status(simt_attend_weight(g, bf, q_abs, n_nodes, cache, window, tree, softmax_scale,
                                         lse, query_weight, weight_in, weight_out,
                                         (cudaStream_t)stream));

@@ -220,12 +220,21 @@ struct TreePlan {
   int32_t tpre[TREE_MAXB];                     // tiles likewise
   int32_t nblk[TREE_MAXB];                     // key blocks of each sequence's tiles
 };
+struct TreeSum {
+  int64_t blocks, keys;
+  int32_t tiles, longest;
+};
 struct TreeScratch {                           // shared memory, next to the plan
   int64_t start[MAXC + 1];                     // where each cluster's tail starts
-  int64_t sums[2][16];
-  unsigned long long cost[2], keys;
+  TreeSum warp[16];
   int rounds;
 };
+
+// a / b for a >= 0, b > 0: the 64-bit division is a long subroutine, and the plan stands before
+// every call's first load.
+__device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // The first sequence whose part of a line ends past p.
 template <typename T>
@@ -265,7 +274,7 @@ struct TreeWalk {
     if (left > 0) {
       tail_b = tree_find(pl.pre, a.g.B, p0);
       const int64_t rem = p0 - (tail_b ? pl.pre[tail_b - 1] : 0);
-      tail_tb = (int)(rem / pl.nblk[tail_b]);
+      tail_tb = (int)div_nn(rem, pl.nblk[tail_b]);
       tail_jb = (int)(rem - (int64_t)tail_tb * pl.nblk[tail_b]);
     }
     load(a);
@@ -326,28 +335,9 @@ struct TreeWalk {
   }
 };
 
-// Costs of the two schedules in key blocks: a cluster's blocks plus SEG_COST per segment it walks
-// (the switch: Q reload, output epilogue, pipeline refill), plus COMBINE_COST when tiles are
-// split (the merge).  Measured on B200 (video chunk, long window and decode shapes).
+// Costs in key blocks: of a segment (the switch: Q reload, output epilogue, pipeline refill), and of
+// split tiles (the merge).  Measured on B200 (video chunk, long window and decode shapes).
 constexpr int64_t SEG_COST = 7, COMBINE_COST = 16;
-
-// Exclusive sum of v over the CTA's NT threads (every thread calls it).
-template <int NT>
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(FULL, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int64_t before = 0;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  __syncthreads();
-  return before + x - v;
-}
 
 // Plan of cluster c of G: its rounds (list, returned count) and its tail [p0, p1).  Every thread of
 // the CTA takes part.
@@ -355,88 +345,129 @@ template <int NT>
 __device__ __forceinline__ int tree_plan(const AttnArgs& a, const TreeSched& sc, TreePlan& pl,
                                          TreeScratch& x, int2* list, int G, int c, int64_t& p0,
                                          int64_t& p1) {
-  const int t = threadIdx.x, B = a.g.B;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.g.B;
   const int per = (B + NT - 1) / NT;
-  if (t == 0) {
-    x.cost[0] = x.cost[1] = x.keys = 0ull;
-    x.rounds = INT32_MAX;
-  }
-  int64_t blocks = 0;
-  int tiles = 0;
-  unsigned long long keys = 0;
+  if (t == 0) x.rounds = INT32_MAX;
+  // where each sequence ends in the line: the threads' runs of sequences, then a scan
+  int64_t blocks = 0, keys = 0;
+  int tiles = 0, longest = 0;
   for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
     const TreeGeo s = tree_geo(a, b);
     blocks += (int64_t)s.tiles * s.blk.nblk;
     tiles += s.tiles;
-    if (s.tiles > 0) keys += s.blk.nblk;
+    if (s.tiles > 0) {
+      keys += s.blk.nblk;
+      longest = max(longest, s.blk.nblk);
+    }
     pl.pre[b] = blocks;
     pl.tpre[b] = tiles;
     pl.nblk[b] = s.blk.nblk;
   }
-  const int64_t ob = cta_scan<NT>(blocks, x.sums[0]);
-  const int ot = (int)cta_scan<NT>(tiles, x.sums[1]);
-  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
-    pl.pre[b] += ob;
-    pl.tpre[b] += ot;
+  const int warps = (B + 32 * per - 1) / (32 * per);         // warps that hold sequences
+  if (warp < warps) {
+    int64_t xb = blocks;
+    int xt = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t yb = __shfl_up_sync(FULL, xb, o);
+      const int yt = __shfl_up_sync(FULL, xt, o);
+      if (lane >= o) {
+        xb += yb;
+        xt += yt;
+      }
+      keys += __shfl_xor_sync(FULL, keys, o);
+    }
+    longest = __reduce_max_sync(FULL, longest);
+    if (lane == 31) x.warp[warp] = TreeSum{xb, keys, xt, longest};
+    blocks = xb - blocks;
+    tiles = xt - tiles;
   }
-  if (keys) atomicAdd(&x.keys, keys);
   __syncthreads();
-  const int64_t W = pl.pre[B - 1], T = pl.tpre[B - 1];
+  int64_t W = 0, K = 0;
+  int T = 0, nmax = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) {
+      blocks += W;
+      tiles += T;
+    }
+    const TreeSum v = x.warp[w];
+    W += v.blocks;
+    K += v.keys;
+    T += v.tiles;
+    nmax = max(nmax, v.longest);
+  }
   p0 = p1 = 0;
   if (W == 0) return 0;
-  // thread u < G: cluster u's share, and the blocks of its first rounds
-  const int64_t share = t < G ? W * (t + 1) / G - W * t / G : 0;
-  auto round_blocks = [&](int u, int r) { return pl.nblk[tree_find(pl.tpre, B, (int64_t)r * G + u)]; };
-  const bool waves = (int64_t)x.keys > sc.l2_blocks && a.tiles_per_batch > 2;
-  const int most = (int)(T / G < TREE_MAXR ? T / G : TREE_MAXR);
-  if (waves && t < G) {
-    int r = 0;
-    for (int64_t d = 0; r < most; ++r) {
-      d += round_blocks(t, r);
-      if (d > share) break;
+  if (warps > 1 || per > 1) {
+    for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
+      pl.pre[b] += blocks;
+      pl.tpre[b] += tiles;
     }
-    atomicMin(&x.rounds, r);
+  } else if (t < B) {
+    pl.pre[t] += blocks;
+    pl.tpre[t] += tiles;
   }
   __syncthreads();
-  const int R = waves ? x.rounds : 0;
-  int64_t head = 0;
-  if (t < G)
-    for (int r = 0; r < R; ++r) head += round_blocks(t, r);
-  const int64_t rest = share - head;           // the tail's blocks
-  const int64_t before = cta_scan<NT>(rest, x.sums[0]);
-  // the rounds took the first R G tiles; the tails share the rest of the line
-  const int64_t done = (int64_t)R * G;
-  int64_t line = 0;
-  if (done > 0) {
-    const int b = tree_find(pl.tpre, B, done - 1);
-    line = (b ? pl.pre[b - 1] : 0) + (done - (b ? pl.tpre[b - 1] : 0)) * pl.nblk[b];
+  // equal shares of the line: cluster u's ends at cut(u + 1)
+  const int64_t each = div_nn(W, G);
+  const int odd = (int)(W - each * G);
+  auto cut = [&](int u) { return each * u + (int)((uint32_t)(odd * u) / (uint32_t)G); };
+  int R = 0;
+  p0 = cut(c);
+  p1 = cut(c + 1);
+  if (K > sc.l2_blocks && a.tiles_per_batch > 2) {
+    // thread u < G: how many rounds cluster u's share holds
+    auto round_blocks = [&](int r) { return pl.nblk[tree_find(pl.tpre, B, (int64_t)r * G + t)]; };
+    const int most = T / G < TREE_MAXR ? T / G : TREE_MAXR;
+    const int64_t share = t < G ? cut(t + 1) - cut(t) : 0;
+    if (t < G) {
+      int r = 0;
+      for (int64_t d = 0; r < most; ++r) {
+        d += round_blocks(r);
+        if (d > share) break;
+      }
+      atomicMin(&x.rounds, r);
+    }
+    __syncthreads();
+    R = x.rounds;
+    // the tails share the line from where the rounds' R G tiles end
+    int64_t rest = share;
+    if (t < G)
+      for (int r = 0; r < R; ++r) rest -= round_blocks(r);
+    int64_t xr = rest;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, xr, o);
+      if (lane >= o) xr += y;
+    }
+    __syncthreads();                          // x.warp has been read
+    if (lane == 31) x.warp[warp].blocks = xr;
+    __syncthreads();
+    const int done = R * G;
+    int64_t line = 0;
+    if (done > 0) {
+      const int b = tree_find(pl.tpre, B, done - 1);
+      line = (b ? pl.pre[b - 1] : 0) + (int64_t)(done - (b ? pl.tpre[b - 1] : 0)) * pl.nblk[b];
+    }
+    for (int w = 0; w < warp; ++w) line += x.warp[w].blocks;
+    if (t < G) x.start[t] = line + xr - rest;
+    if (t == 0) x.start[G] = W;
+    __syncthreads();
+    p0 = x.start[c];
+    p1 = x.start[c + 1];
   }
-  if (t < G) x.start[t] = line + before;
-  if (t == 0) x.start[G] = W;
-  __syncthreads();
-  // cuts on tile boundaries: the first one at or past the cut
-  auto up = [&](int64_t p) {
-    const int b = tree_find(pl.pre, B, p);
-    if (p >= pl.pre[b]) return pl.pre[b];      // p == W
-    const int64_t s = b ? pl.pre[b - 1] : 0, n = pl.nblk[b];
-    return s + (p - s + n - 1) / n * n;
-  };
-  if (sc.split && t < G) {
-    auto tile_at = [&](int64_t p) {
+  // Split tiles, or cut on tile boundaries?  Whole tiles take as long as the longest one, or a share
+  // plus what rounding up to tiles adds (for sequences of one length (ceil(T / G) - T / G) tiles);
+  // split ones take a share, one segment more and the merge.
+  const float share = (float)W / (float)G, up_tiles = (float)((T + G - 1) / G) - (float)T / (float)G;
+  const float whole = fmaxf((float)nmax, share + up_tiles * (float)nmax);
+  if (!sc.split || whole <= share + (float)(SEG_COST + COMBINE_COST)) {
+    auto up = [&](int64_t p) {                // the first boundary at or past p
       const int b = tree_find(pl.pre, B, p);
-      return (b ? pl.tpre[b - 1] : 0) + (p - (b ? pl.pre[b - 1] : 0)) / pl.nblk[b];
+      if (p >= pl.pre[b]) return pl.pre[b];   // p == W
+      const int64_t s = b ? pl.pre[b - 1] : 0, n = pl.nblk[b];
+      return s + div_nn(p - s + n - 1, n) * n;
     };
-    auto charge = [&](unsigned long long* into, int64_t s, int64_t e) {
-      const int64_t segs = R + (e > s ? tile_at(e - 1) - tile_at(s) + 1 : 0);
-      atomicMax(into, (unsigned long long)(head + (e - s) + SEG_COST * segs));
-    };
-    charge(&x.cost[0], x.start[t], x.start[t + 1]);
-    charge(&x.cost[1], up(x.start[t]), up(x.start[t + 1]));
-  }
-  __syncthreads();
-  p0 = x.start[c];
-  p1 = x.start[c + 1];
-  if (!sc.split || x.cost[0] + COMBINE_COST >= x.cost[1]) {
     p0 = up(p0);
     p1 = up(p1);
   }

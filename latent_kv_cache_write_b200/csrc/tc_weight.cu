@@ -1,0 +1,512 @@
+// The attention weight every cached row received, on tcgen05 tensor cores (bf16, d_c = 512,
+// d_R = 64 or 512): w(j) += sum over (node, head) rows r of g(r) exp(s(r, j) - lse(r)).
+//
+// With the log-sum-exps known this is a product S^T = K . Q^T whose epilogue is one exponential
+// and one multiply-add per score, summed along the rows.  Keys are the M side (TMEM lanes), rows the
+// N side (columns), so a thread owns a key and its sum never leaves the thread.  Nothing of S is
+// stored; the sums of a key are joined in one place, without atomics, so the order is fixed.
+//
+// A CTA pair (cta_group::2) takes 256 keys at a time, 128 per CTA, and 256 rows per MMA, of which
+// each CTA loads half: a lone CTA would need 128 rows x 64 dims for every 4 MMAs of M = N = 128,
+// 64 B/clk, and an SM's TMA loads deliver about 44.
+//   RES_K: the keys' tile (9 boxes of 128 rows x 64 dims, 144 KB) stays in shared memory while the
+//          rows stream past it in 4 stages.  MMA-bound: 4608 clk per 256 x 256 x 576 tile.
+//   RES_Q: at most 128 rows per sequence (single tokens, small trees): the rows stay and the keys
+//          stream, read once from HBM, which bounds it.
+//   STREAM: d_R = 512 with more rows: 256 KB of keys do not fit, both operands stream.
+//
+// Warp roles (320 threads): warps 0-3 and 4-7 take alternate accumulators (256 columns each, the
+// two fill tensor memory), warp 8 loads (each CTA its own halves; the bytes of both complete on
+// the even CTA's barriers), warp 9 of the even CTA issues the MMAs.
+#include "attend_common.cuh"
+#include "launch.h"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+#include <mutex>
+
+namespace mla {
+namespace {
+
+using namespace tc;
+using namespace attn;
+
+enum { RES_K = 0, RES_Q = 1, STREAM = 2 };
+
+constexpr int WT = 320;                        // threads
+constexpr int KEYS = 128;                      // keys per CTA
+constexpr int KBOX = KEYS * 64 * 2;            // box of keys: 128 rows x 64 dims
+constexpr int WMAXB = 6144;                    // sequences the plan's array holds
+constexpr unsigned FULL = 0xffffffffu;
+
+// NSL: 64-dim slices of a row (9 or 16).  NT: rows of a tile (N of the MMA), half from each CTA.
+template <int NSL, int MODE>
+struct WLay {
+  static constexpr int NT = MODE == RES_Q ? 128 : 256;
+  static constexpr int QBOX = NT / 2 * 64 * 2;
+  static constexpr int RBOX = MODE == RES_K ? KBOX : (MODE == RES_Q ? QBOX : 0);
+  static constexpr int NRES = MODE == STREAM ? 0 : NSL;               // resident boxes
+  static constexpr int SBOX = MODE == RES_K ? QBOX : (MODE == RES_Q ? KBOX : KBOX + QBOX);
+  static constexpr int NST = MODE == RES_K ? 4 : (MODE == RES_Q ? (NSL == 9 ? 8 : 5) : 6);
+  static constexpr int OFF_RES = 0;
+  static constexpr int OFF_ST = NRES * RBOX;
+  static constexpr int OFF_ROW = OFF_ST + NST * SBOX;      // (lse, weight) of rows [2][2][256]
+  static constexpr int OFF_SUM = OFF_ROW + 4 * 256 * 8;    // sums handed between warpgroups [128]
+  static constexpr int OFF_BAR = OFF_SUM + 128 * 4;
+  static constexpr int B_SF = 0;                           // stage loaded, both CTAs   [NST]
+  static constexpr int B_SE = B_SF + NST;                  // stage free                [NST]
+  static constexpr int B_RF = B_SE + NST;                  // resident box loaded       [NRES]
+  static constexpr int B_RE = B_RF + NRES;                 // resident box free         [NRES]
+  static constexpr int B_AF = B_RE + NRES;                 // accumulator complete      [2]
+  static constexpr int B_AE = B_AF + 2;                    // accumulator read, 8 warps [2]
+  static constexpr int NBAR = B_AE + 2;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // TMEM slot, abort flag, plan's sums
+  static constexpr int SMEM = OFF_MISC + 16 + 16 * 8 + 1024;
+  static_assert(SMEM <= 227 * 1024, "dynamic shared memory of one CTA");
+  static_assert(OFF_ST % 1024 == 0 && OFF_ROW % 1024 == 0 && RBOX % 1024 == 0 && SBOX % 1024 == 0,
+                "swizzled boxes start on their alignment");
+  static_assert(WMAXB * 8 <= OFF_ROW, "the plan's array fits where the operands will be");
+};
+
+struct WeightArgs {
+  AttnArgs a;                                  // g, n_q, q_abs, window, tree, bn, err
+  float c2;                                    // softmax scale in log2 units
+  const float* lse;
+  const float* qw;
+  const float* win;
+  float* out;
+};
+
+// Units (256 keys of a sequence) one pair walks, in order.
+struct UnitWalk {
+  int64_t pos, end;                            // position in the line of tiles, and its end
+  int b, u, units, tiles, nt;
+  TreeGeo s;
+  int64_t rows, qrow0;                         // (node, head) rows of the sequence, its first row
+
+  __device__ void sequence(const AttnArgs& a, int seq) {
+    b = seq;
+    s = tree_geo(a, b);
+    rows = (int64_t)(s.blk.L - s.ctx) * a.g.H;
+    units = (s.blk.nblk + 1) / 2;
+    tiles = (int)((rows + nt - 1) / nt);
+    qrow0 = (int64_t)b * a.n_q * a.g.H;
+  }
+  __device__ bool valid() const { return pos < end; }
+  __device__ void next(const AttnArgs& a) {
+    pos += tiles;
+    if (pos >= end) return;
+    if (++u >= units) {
+      u = 0;
+      do {
+        sequence(a, b + 1);                    // pos < end: a later sequence has tiles
+      } while (tiles == 0);
+    }
+  }
+  // this CTA's key block of the unit: first slot, first logical row, keys (0: none)
+  __device__ void keys(uint32_t rank, int64_t S, int64_t& slot0, int64_t& j0, int& valid) const {
+    const int j = 2 * u + (int)rank;
+    if (j < s.blk.nblk) {
+      s.blk.get(j, slot0, j0, valid);
+    } else {
+      slot0 = S;                               // outside the tensor: the box is filled with zeros
+      j0 = 0;
+      valid = 0;
+    }
+  }
+};
+
+// The walk of pair c of P: the tiles of all units (sequence after sequence) make one line, and a
+// pair takes the units that start in its equal share of it.
+template <int NT>
+__device__ __forceinline__ void plan_units(const AttnArgs& a, int64_t* pre, int64_t* sums, int P,
+                                           int c, UnitWalk& w) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.g.B;
+  const int per = (B + WT - 1) / WT;
+  w.nt = NT;
+  int64_t n = 0;
+  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
+    w.sequence(a, b);
+    n += (int64_t)w.units * w.tiles;
+    pre[b] = n;
+  }
+  int64_t x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(FULL, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int64_t before = x - n, W = 0;
+  const int warps = (B + 32 * per - 1) / (32 * per);
+  for (int k = 0; k < warps; ++k) {
+    if (k == warp) before += W;
+    W += sums[k];
+  }
+  for (int b = t * per; b < (t + 1) * per && b < B; ++b) pre[b] += before;
+  __syncthreads();
+  const int64_t each = W / P;
+  const int odd = (int)(W - each * P);
+  auto cut = [&](int k) { return each * k + (int)((uint32_t)(odd * k) / (uint32_t)P); };
+  const int64_t p0 = cut(c), p1 = cut(c + 1);
+  w.pos = w.end = 0;
+  if (p0 >= p1) return;
+  int lo = 0, hi = B - 1;                      // the sequence that holds p0
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] > p0) hi = mid; else lo = mid + 1;
+  }
+  w.sequence(a, lo);
+  const int64_t start = lo ? pre[lo - 1] : 0;
+  w.u = (int)((p0 - start + w.tiles - 1) / w.tiles);         // the first unit at or past p0
+  w.pos = start + (int64_t)w.u * w.tiles;
+  w.end = p1;
+  if (w.pos < w.end && w.u >= w.units) {       // it is the next sequence's first
+    w.u = 0;
+    do {
+      w.sequence(a, w.b + 1);
+    } while (w.tiles == 0);
+  }
+}
+
+template <int NSL, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
+    attend_weight_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ WeightArgs p) {
+  using LY = WLay<NSL, MODE>;
+  constexpr int NT = LY::NT, NST = LY::NST, NRES = LY::NRES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + LY::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + LY::OFF_MISC + 4);
+  const uint32_t rank = cluster_ctarank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const AttnArgs& a = p.a;
+
+  if (tid == 0) {
+    for (int q = 0; q < LY::B_AE; ++q) mbar_init(&bar[q], 1);
+    for (int q = 0; q < 2; ++q) mbar_init(&bar[LY::B_AE + q], 8);
+    *abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmQ);
+  }
+  if (warp == 9) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                              // the pair's barriers exist before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();                             // the previous kernel's outputs are visible
+  grid_dep_launch();
+
+  UnitWalk w;
+  plan_units<NT>(a, reinterpret_cast<int64_t*>(sm), reinterpret_cast<int64_t*>(sm + LY::OFF_MISC + 16),
+                 (int)(gridDim.x >> 1), (int)(blockIdx.x >> 1), w);
+  fence_proxy_async_smem();                    // the array is read before TMA writes over it
+  __syncthreads();
+  // (a pair's loads complete on the even CTA's barriers, but go to each CTA's own memory)
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      const uint32_t even = mapa(smem_u32(bar), 0);
+      uint32_t it = 0, un = 0;                 // stages filled, resident tiles filled
+      int res_b = -1;
+      bool ok = true;
+      for (; ok && w.valid(); w.next(a)) {
+        int64_t slot0, j0;
+        int valid;
+        w.keys(rank, a.g.S, slot0, j0, valid);
+        // resident boxes of the unit (RES_Q: of the sequence), each as soon as its last use is done
+        const bool fill = MODE == RES_K || (MODE == RES_Q && w.b != res_b);
+        auto resident = [&](int i) {
+          if (!mbar_wait(&bar[LY::B_RE + i], (un & 1) ^ 1, abort, a.err, 0x31, i)) return false;
+          if (rank == 0) mbar_expect_tx(&bar[LY::B_RF + i], 2 * LY::RBOX);
+          const uint32_t full = even + (LY::B_RF + i) * 8;
+          if (MODE == RES_K)
+            tma_load_3d_pair(sm + LY::OFF_RES + i * LY::RBOX, &tmK, full, i * 64, (int32_t)slot0, w.b);
+          else
+            tma_load_2d_pair(sm + LY::OFF_RES + i * LY::RBOX, &tmQ, full, i * 64,
+                             (int32_t)(w.qrow0 + rank * (NT / 2)));
+          return true;
+        };
+        for (int q = 0; ok && q < w.tiles; ++q) {
+          const int64_t row = w.qrow0 + (int64_t)q * NT + rank * (NT / 2);
+          for (int i = 0; ok && i < NSL; ++i, ++it) {
+            if (fill && q == 0) ok = resident(i);
+            if (!ok) break;
+            const int s = it % NST;
+            ok = mbar_wait(&bar[LY::B_SE + s], ((it / NST) & 1) ^ 1, abort, a.err, 0x32, it);
+            if (!ok) break;
+            if (rank == 0) mbar_expect_tx(&bar[LY::B_SF + s], 2 * LY::SBOX);
+            const uint32_t full = even + (LY::B_SF + s) * 8;
+            uint8_t* st = sm + LY::OFF_ST + s * LY::SBOX;
+            if (MODE != RES_Q)
+              tma_load_2d_pair(st, &tmQ, full, i * 64, (int32_t)row);
+            if (MODE != RES_K)
+              tma_load_3d_pair(st + (MODE == STREAM ? LY::QBOX : 0), &tmK, full, i * 64,
+                               (int32_t)slot0, w.b);
+          }
+        }
+        if (fill) {
+          ++un;
+          res_b = w.b;
+        }
+      }
+      // the MMAs' last arrivals on this CTA's barriers land before it may exit
+      for (uint32_t k = it > NST ? it - NST : 0; ok && k < it; ++k)
+        ok = mbar_wait(&bar[LY::B_SE + k % NST], (k / NST) & 1, abort, a.err, 0x37, k);
+      for (int i = 0; ok && un > 0 && i < NRES; ++i)
+        ok = mbar_wait(&bar[LY::B_RE + i], (un - 1) & 1, abort, a.err, 0x38, i);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0 && rank == 0) {
+      const uint32_t id = idesc_bf16(256, NT, false, false);
+      uint32_t it = 0, un = 0, tc = 0;
+      int res_b = -1;
+      bool ok = true;
+      while (ok && w.valid()) {
+        const bool fill = MODE == RES_K || (MODE == RES_Q && w.b != res_b);
+        const int b = w.b, tiles = w.tiles;
+        w.next(a);                             // the next unit tells whether the boxes are done with
+        const bool last = MODE == RES_K || !w.valid() || w.b != b;
+        for (int q = 0; ok && q < tiles; ++q, ++tc) {
+          const int acc = tc & 1;
+          ok = mbar_wait_cluster(&bar[LY::B_AE + acc], ((tc >> 1) & 1) ^ 1, abort, a.err, 0x33, tc);
+          if (!ok) break;
+          tc_fence_after();
+          for (int i = 0; i < NSL; ++i, ++it) {
+            const int s = it % NST;
+            if (fill && q == 0)
+              ok = mbar_wait_cluster(&bar[LY::B_RF + i], un & 1, abort, a.err, 0x34, i);
+            if (ok)
+              ok = mbar_wait_cluster(&bar[LY::B_SF + s], (it / NST) & 1, abort, a.err, 0x35, it);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(sm + LY::OFF_ST + s * LY::SBOX);
+            const uint32_t rs = smem_u32(sm + LY::OFF_RES + i * LY::RBOX);
+            const uint32_t kk = MODE == RES_K ? rs : (MODE == RES_Q ? st : st + LY::QBOX);
+            const uint32_t qq = MODE == RES_Q ? rs : st;
+            const uint64_t da = desc_sw128(kk, 16, 1024), db = desc_sw128(qq, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)        // 16-dim steps: +32 bytes inside the swizzle atom
+              mma_ss_pair(tmem + acc * 256, da + 2 * k, db + 2 * k, id, (i | k) ? 1u : 0u);
+            mma_commit_pair(&bar[LY::B_SE + s]);
+            if (NRES > 0 && last && q == tiles - 1) mma_commit_pair(&bar[LY::B_RE + i]);
+          }
+          if (ok) mma_commit_pair(&bar[LY::B_AF + acc]);
+        }
+        if (fill) {
+          ++un;
+          res_b = b;
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue warpgroups
+    const int wg = warp >> 2, t = tid & 127;   // accumulator, key = TMEM lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t drained = mapa(smem_u32(&bar[LY::B_AE + wg]), 0);
+    float2* rowbuf = reinterpret_cast<float2*>(sm + LY::OFF_ROW) + wg * 512;
+    float* handed = reinterpret_cast<float*>(sm + LY::OFF_SUM);
+    const int H = a.g.H;
+    uint32_t tc = 0, mine = 0;                 // tiles of the pair, tiles this warpgroup has taken
+    // sequences without nodes have no tiles: their totals pass through
+    if (p.win != p.out)
+      for (int b = blockIdx.x; b < a.g.B; b += gridDim.x) {
+        const Window v = load_window(a.window, b, a.g.S, a.n_q);
+        if (v.nodes > 0) continue;
+        for (int j = tid; j < v.rows; j += 256) {
+          const int64_t at = (int64_t)b * a.g.S + v.slot(j, a.g.S);
+          p.out[at] = p.win ? p.win[at] : 0.f;
+        }
+      }
+    // After an expired wait the warps still walk to the end (each further wait gives up at once):
+    // the warpgroups meet at named barriers.
+    bool ok = true;
+    for (; w.valid(); w.next(a)) {
+      int64_t slot0, j0;
+      int valid;
+      w.keys(rank, a.g.S, slot0, j0, valid);
+      const bool nodes = j0 + valid > w.s.ctx;         // the block holds draft nodes
+      const int64_t node = j0 + t - w.s.ctx;           // this key's node (negative: context)
+      const uint8_t* tree =
+          a.tree ? a.tree + (int64_t)w.b * a.n_q * a.n_q + (node > 0 ? node : 0) : nullptr;
+      auto sees = [&](int64_t i) {                     // whether node i sees this key
+        return node < 0 || t >= valid || (tree ? tree[i * a.n_q] != 0 : node <= i);
+      };
+      float total = 0.f;
+      bool took = false;
+      for (int q = 0; q < w.tiles; ++q, ++tc) {
+        if ((int)(tc & 1) != wg) continue;
+        took = true;
+        const int64_t r0 = (int64_t)q * NT;
+        const int n = w.rows - r0 < NT ? (int)(w.rows - r0) : NT;        // rows of the tile
+        // log-sum-exps (log2 units) and weights of the tile's rows; a row that adds nothing has
+        // an infinite one, so that its exponentials are 0
+        float2* rb = rowbuf + (mine & 1) * 256;
+        for (int e = t; e < NT; e += 128) {
+          float2 v = make_float2(INFINITY, 0.f);
+          if (e < n) {
+            const float l = p.lse[w.qrow0 + r0 + e];
+            const float g = p.qw ? p.qw[(int64_t)w.b * a.n_q + (uint32_t)(r0 + e) / (uint32_t)H] : 1.f;
+            if (g != 0.f && l != -INFINITY) v = make_float2(l * 1.4426950408889634f, g);
+          }
+          rb[e] = v;
+        }
+        named_bar(1 + wg, 128);
+        ok = __all_sync(FULL, ok && mbar_wait_cluster(&bar[LY::B_AF + wg], mine & 1, abort, a.err,
+                                                      0x36, (t << 16) | mine));
+        ++mine;
+        tc_fence_after();
+        const uint32_t acc = tmem + lane_base + wg * 256;
+        const float4* rv = reinterpret_cast<const float4*>(rb);
+#pragma unroll 1
+        for (int c0 = 0; c0 < NT; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc + c0, v);
+          tmem_wait_ld();
+          if (c0 + 32 == NT) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(drained);
+          }
+          if (!ok || c0 >= n) continue;
+          // the nodes of these 32 rows, where they matter
+          const uint32_t row = (uint32_t)(r0 + c0);
+          const uint32_t i0 = nodes ? row / (uint32_t)H : 0, i1 = nodes ? (row + 31) / (uint32_t)H : 0;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          if (c0 + 32 <= n && i0 == i1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float4 x = rv[c0 / 2 + e];         // two rows' (lse, weight)
+              const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), p.c2, -x.x));
+              const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), p.c2, -x.z));
+              sum[(2 * e) & 3] = fmaf(p0, x.y, sum[(2 * e) & 3]);
+              sum[(2 * e + 1) & 3] = fmaf(p1, x.w, sum[(2 * e + 1) & 3]);
+            }
+            const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (!nodes || sees(i0)) total += s;
+          } else {
+            // rows past the last, or rows of several nodes next to draft keys: one by one
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 x = rb[c0 + e];
+              const float pe = ex2(fmaf(__uint_as_float(v[e]), p.c2, -x.x));
+              const bool in = c0 + e < n && (!nodes || sees((row + e) / (uint32_t)H));
+              if (in) sum[e & 3] = fmaf(pe, x.y, sum[e & 3]);
+            }
+            total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+        }
+      }
+      const int64_t at = (int64_t)w.b * a.g.S + slot0 + t;
+      if (w.tiles == 1) {
+        // one warpgroup had the unit to itself
+        if (took && ok && t < valid)
+          p.out[at] = (p.win && node < 0 ? p.win[at] : 0.f) + total;
+      } else {
+        // the sum of the even tiles plus that of the odd ones
+        if (wg == 1) handed[t] = total;
+        named_bar(3, 256);
+        if (wg == 0 && ok && t < valid)
+          p.out[at] = (p.win && node < 0 ? p.win[at] : 0.f) + (total + handed[t]);
+        named_bar(3, 256);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                              // no remote access into this CTA is pending
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int NSL, int MODE>
+cudaError_t launch_weight(const CUtensorMap& K, const CUtensorMap& Q, const WeightArgs& p,
+                          cudaStream_t st) {
+  using LY = WLay<NSL, MODE>;
+  static std::mutex mu;
+  static int pairs[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n;
+  {
+    // the shared-memory opt-in and the pairs that can be resident at once, per device
+    std::lock_guard<std::mutex> lock(mu);
+    n = dev < 64 ? pairs[dev] : 0;
+    if (n == 0) {
+      e = cudaFuncSetAttribute(attend_weight_kernel<NSL, MODE>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * MAXC);
+      cfg.blockDim = dim3(WT);
+      cfg.dynamicSmemBytes = LY::SMEM;
+      e = cudaOccupancyMaxActiveClusters(&n, attend_weight_kernel<NSL, MODE>, &cfg);
+      if (e != cudaSuccess) return e;
+      n = n < 1 ? 1 : (n > MAXC ? MAXC : n);
+      if (dev < 64) pairs[dev] = n;
+    }
+  }
+  e = launch_dependent(attend_weight_kernel<NSL, MODE>, (unsigned)(2 * n), WT, LY::SMEM, st, 1u, K,
+                       Q, p);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+bool tc_attend_weight_supported(const Geo& g) {
+  return g.Dc == 512 && (g.Dr == 64 || g.Dr == 512) && g.B <= WMAXB;
+}
+
+cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                             const int32_t* window, const uint8_t* tree, float scale,
+                             const float* lse, const float* qw, const float* win, float* wout,
+                             unsigned int* err, cudaStream_t st) {
+  WeightArgs p{};
+  p.a.g = g;
+  p.a.n_q = n_nodes;
+  p.a.bn = KEYS;
+  p.a.window = window;
+  p.a.tree = tree;
+  p.a.err = err;
+  p.c2 = scale * 1.4426950408889634f;
+  p.lse = lse;
+  p.qw = qw;
+  p.win = win;
+  p.out = wout;
+  const bool few = n_nodes * g.H <= 128;       // one tile of 128 rows per sequence
+  CUtensorMap K, Q;
+  {
+    uint64_t d[3] = {(uint64_t)g.row, (uint64_t)g.S, (uint64_t)g.B};
+    uint64_t s[2] = {(uint64_t)g.row * 2, (uint64_t)g.S * g.row * 2};
+    uint32_t b[3] = {64, KEYS, 1};
+    if (!make_tmap_bf16(&K, cache, 3, d, s, b)) return cudaErrorInvalidValue;
+  }
+  {
+    uint64_t d[2] = {(uint64_t)g.row, (uint64_t)g.B * n_nodes * g.H};
+    uint64_t s[1] = {(uint64_t)g.row * 2};
+    uint32_t b[2] = {64, few ? 64u : 128u};
+    if (!make_tmap_bf16(&Q, q_abs, 2, d, s, b)) return cudaErrorInvalidValue;
+  }
+  if (g.Dr == 64)
+    return few ? launch_weight<9, RES_Q>(K, Q, p, st) : launch_weight<9, RES_K>(K, Q, p, st);
+  return few ? launch_weight<16, RES_Q>(K, Q, p, st) : launch_weight<16, STREAM>(K, Q, p, st);
+}
+
+}  // namespace mla
