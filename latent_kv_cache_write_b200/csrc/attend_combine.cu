@@ -139,11 +139,12 @@ __global__ void __launch_bounds__(256)
                              cl.piece0[i + 1] - p0, [&](int p) { return p0 + p; });
 }
 
-// Draft trees: the clusters' cuts are known on the device only.  Cut i (the start of cluster i)
-// splits a tile when it lies inside it; the first such cut of a tile stands for the tile, whose
-// pieces are the segment of cluster i - 1 that reached the cut and the first segments of the
-// clusters that start inside it.  Every block lists the split tiles for itself (at most MAXC cuts)
-// and the grid takes their rows in turn.
+// Draft trees: the clusters' cuts are known on the device only.  cut[i] is where the range of the
+// i-th cluster that has one starts (sequence, tile, block, cluster).  It splits a tile when it lies
+// inside it; the first such cut of a tile stands for the tile, whose pieces are the segment of the
+// cluster before that reached the cut and the first segments of the clusters that start inside it.
+// Every block lists the split tiles for itself (at most MAXC cuts) and the grid takes their rows in
+// turn.
 template <int CSPLIT>
 __device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws_lse, float* red,
                                               const int4* cut, const int* first,
@@ -158,10 +159,10 @@ __device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws
     const Window w = load_window(a.window, c.x, a.g.S, a.n_q);
     const int64_t row = (int64_t)c.y * TM + r;
     // the segment before the cut is its cluster's first when that cluster starts this tile
-    const int s0 = 2 * (i - 1) + (before.x == c.x && before.y == c.y ? 0 : 1);
+    const int s0 = 2 * before.w + (before.x == c.x && before.y == c.y ? 0 : 1);
     combine_row<CSPLIT, true>(a, ws_lse, red, rr, part, lane, r, row < (int64_t)w.nodes * a.g.H,
                               (int64_t)c.x * a.n_q * a.g.H + row, pieces[e],
-                              [&](int p) { return p == 0 ? s0 : 2 * (i + p - 1); });
+                              [&](int p) { return p == 0 ? s0 : 2 * cut[i + p - 1].w; });
     if (CSPLIT > 1) __syncthreads();               // `red` is the next row's
   }
 }
@@ -174,19 +175,24 @@ __global__ void __launch_bounds__(256)
   __shared__ int n_sh, most_sh;
   tc::grid_dep_wait();                             // the attention's partials are visible
   tc::grid_dep_launch();
-  for (int i = threadIdx.x; i < clusters; i += blockDim.x) cut[i] = a.cuts[i];
-  __syncthreads();
   if (threadIdx.x < 32) {
-    int n = 0, most = 0;
+    int n = 0, most = 0, ranges = 0;
     for (int i0 = 0; i0 < clusters; i0 += 32) {
+      const int4 c = i0 + (int)threadIdx.x < clusters ? a.cuts[i0 + threadIdx.x] : make_int4(-1, 0, 0, 0);
+      const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
+      if (c.x >= 0) cut[ranges + __popc(m & ((1u << threadIdx.x) - 1u))] = c;
+      ranges += __popc(m);
+    }
+    __syncwarp();
+    for (int i0 = 0; i0 < ranges; i0 += 32) {
       const int i = i0 + threadIdx.x;
       // a cut inside a tile has a block > 0; the tile's first one stands for it
-      bool is = i > 0 && i < clusters && cut[i].z > 0;
+      bool is = i > 0 && i < ranges && cut[i].z > 0;
       if (is) is = !(cut[i - 1].z > 0 && cut[i - 1].x == cut[i].x && cut[i - 1].y == cut[i].y);
       const unsigned m = __ballot_sync(0xffffffffu, is);
       if (is) {
         int k = i + 1;
-        while (k < clusters && cut[k].z > 0 && cut[k].x == cut[i].x && cut[k].y == cut[i].y) ++k;
+        while (k < ranges && cut[k].z > 0 && cut[k].x == cut[i].x && cut[k].y == cut[i].y) ++k;
         const int e = n + __popc(m & ((1u << threadIdx.x) - 1u));
         first[e] = i;
         pieces[e] = k - i + 1;

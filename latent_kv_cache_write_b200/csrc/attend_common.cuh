@@ -35,7 +35,8 @@ struct AttnArgs {
   // draft trees: ragged windows (null otherwise), and which node sees which
   const int32_t* window;    // [B][3]
   const uint8_t* tree;      // [B][n_q][n_q] bytes, or null (a chain)
-  int4* cuts;               // where each cluster starts: (sequence, tile, block), [MAXC]
+  int4* cuts;               // where each cluster's range starts: (sequence or -1: none, tile,
+                            // block, cluster), [MAXC]
   unsigned int* err;
 };
 
@@ -100,6 +101,12 @@ __host__ __device__ inline TileGeo tile_geo(const Geo& G, int64_t n_q, int64_t q
   k.p1 = k_first % G.S;
   lay_blocks(k, G.S, bn);
   return t;
+}
+
+// a / b for a >= 0, b > 0: the 64-bit division is a long subroutine, and the plan stands before
+// every call's first load.
+__device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Draft trees: a sequence's tiles of 128 (node, head) rows, and the key blocks (context, then

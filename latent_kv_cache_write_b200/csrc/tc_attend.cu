@@ -230,12 +230,6 @@ struct TreeScratch {                           // shared memory, next to the pla
   int rounds;
 };
 
-// a / b for a >= 0, b > 0: the 64-bit division is a long subroutine, and the plan stands before
-// every call's first load.
-__device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // The first sequence whose part of a line ends past p.
 template <typename T>
 __device__ __forceinline__ int tree_find(const T* pre, int B, int64_t p) {
@@ -697,7 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     __syncthreads();                // the list is complete
     sw.begin(a, pl, list, R, p0, p1, c);
     if (tid == 0 && rank == 0 && a.cuts)
-      a.cuts[c] = make_int4(sw.tail_b, sw.tail_tb, sw.tail_jb, 0);
+      a.cuts[c] = make_int4(sw.tail_b, sw.tail_tb, sw.tail_jb, c);
     fence_proxy_async_smem();      // the arrays are read before TMA writes over them
     __syncthreads();
   } else {

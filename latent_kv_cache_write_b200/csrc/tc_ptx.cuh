@@ -406,13 +406,13 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a, uint64_
       : "memory");
 }
 
-// Arrive on the mbarrier at this offset in both CTAs of the pair (ranks 0 and 1 of the cluster)
-// once every pair MMA issued so far by this thread completes.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// Arrive on the mbarrier at this offset in both CTAs of the pair (`both`: the mask of their cluster
+// ranks) once every pair MMA issued so far by this thread completes.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t both) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(both)
       : "memory");
 }
 
@@ -433,6 +433,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_even), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Plain store into another CTA's shared memory (visible there after a cluster barrier).
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 // Arrive (release, cluster scope) on a barrier given by its shared::cluster address.

@@ -5,6 +5,7 @@
 // and one multiply-add per score, summed along the rows.  Keys are the M side (TMEM lanes), rows the
 // N side (columns), so a thread owns a key and its sum never leaves the thread.  Nothing of S is
 // stored; the sums of a key are joined in one place, without atomics, so the order is fixed.
+// Groups of 128 rows whose query weights are all 0 (rejected nodes) are left out.
 //
 // A CTA pair (cta_group::2) takes 256 keys at a time, 128 per CTA, and 256 rows per MMA, of which
 // each CTA loads half: a lone CTA would need 128 rows x 64 dims for every 4 MMAs of M = N = 128,
@@ -15,6 +16,10 @@
 //          stream, read once from HBM, which bounds it.
 //   STREAM: d_R = 512 with more rows: 256 KB of keys do not fit, both operands stream.
 //
+// A cluster has one to four pairs.  It takes whole units (256 keys), and its pairs share the tiles of
+// its units evenly: a unit that two or more of them share is summed by the first, which the others
+// send their sums through distributed shared memory at the end.
+//
 // Warp roles (320 threads): warps 0-3 and 4-7 take alternate accumulators (256 columns each, the
 // two fill tensor memory), warp 8 loads (each CTA its own halves; the bytes of both complete on
 // the even CTA's barriers), warp 9 of the even CTA issues the MMAs.
@@ -22,6 +27,8 @@
 #include "launch.h"
 #include "tc_ptx.cuh"
 #include "tmap.h"
+
+#include <stdlib.h>
 
 #include <mutex>
 
@@ -37,6 +44,7 @@ constexpr int WT = 320;                        // threads
 constexpr int KEYS = 128;                      // keys per CTA
 constexpr int KBOX = KEYS * 64 * 2;            // box of keys: 128 rows x 64 dims
 constexpr int WMAXB = 6144;                    // sequences the plan's array holds
+constexpr int MAXCP = 4;                       // pairs per cluster
 constexpr unsigned FULL = 0xffffffffu;
 
 // NSL: 64-dim slices of a row (9 or 16).  NT: rows of a tile (N of the MMA), half from each CTA.
@@ -52,7 +60,8 @@ struct WLay {
   static constexpr int OFF_ST = NRES * RBOX;
   static constexpr int OFF_ROW = OFF_ST + NST * SBOX;      // (lse, weight) of rows [2][2][256]
   static constexpr int OFF_SUM = OFF_ROW + 4 * 256 * 8;    // sums handed between warpgroups [128]
-  static constexpr int OFF_BAR = OFF_SUM + 128 * 4;
+  static constexpr int OFF_PART = OFF_SUM + 128 * 4;       // sums of the cluster's other pairs
+  static constexpr int OFF_BAR = OFF_PART + MAXCP * 128 * 4;
   static constexpr int B_SF = 0;                           // stage loaded, both CTAs   [NST]
   static constexpr int B_SE = B_SF + NST;                  // stage free                [NST]
   static constexpr int B_RF = B_SE + NST;                  // resident box loaded       [NRES]
@@ -77,35 +86,81 @@ struct WeightArgs {
   float* out;
 };
 
-// Units (256 keys of a sequence) one pair walks, in order.
+// The row groups (128 rows) of a sequence that add to the weights, and the tiles they make.
+struct Groups {
+  uint64_t set;                                // bit g: group g (masked), else unused
+  bool masked;                                 // up to 64 groups and query weights: listed in `set`
+  int tiles;
+};
+__device__ __forceinline__ Groups row_groups(const WeightArgs& p, int64_t b, int64_t rows, int nt) {
+  Groups r;
+  const int64_t H = p.a.g.H;
+  r.masked = p.qw != nullptr && rows <= 64 * 128;
+  r.set = 0;
+  if (!r.masked) {
+    r.tiles = (int)((rows + nt - 1) / nt);
+    return r;
+  }
+  const float* qw = p.qw + b * p.a.n_q;
+  const int nodes = (int)((uint32_t)rows / (uint32_t)H);
+#pragma unroll 4
+  for (int i = 0; i < nodes; ++i)
+    if (qw[i] != 0.f) {                        // node i's rows lie in groups g0 .. g1
+      const int g0 = (int)((int64_t)i * H >> 7), g1 = (int)(((int64_t)(i + 1) * H - 1) >> 7);
+      r.set |= (g1 >= 63 ? ~0ull : (1ull << (g1 + 1)) - 1ull) & ~((1ull << g0) - 1ull);
+    }
+  r.tiles = (__popcll(r.set) + nt / 128 - 1) / (nt / 128);
+  return r;
+}
+
+// The pieces of units (256 keys of a sequence) one pair walks, in order: tiles [qb, qe) of each.
 struct UnitWalk {
   int64_t pos, end;                            // position in the line of tiles, and its end
-  int b, u, units, tiles, nt;
+  int b, u, units, qb, qe, nt;
   TreeGeo s;
+  Groups g;
   int64_t rows, qrow0;                         // (node, head) rows of the sequence, its first row
 
-  __device__ void sequence(const AttnArgs& a, int seq) {
+  __device__ void sequence(const WeightArgs& p, int seq) {
     b = seq;
-    s = tree_geo(a, b);
-    rows = (int64_t)(s.blk.L - s.ctx) * a.g.H;
+    s = tree_geo(p.a, b);
+    rows = (int64_t)(s.blk.L - s.ctx) * p.a.g.H;
     units = (s.blk.nblk + 1) / 2;
-    tiles = (int)((rows + nt - 1) / nt);
-    qrow0 = (int64_t)b * a.n_q * a.g.H;
+    g = row_groups(p, b, rows, nt);
+    qrow0 = (int64_t)b * p.a.n_q * p.a.g.H;
+  }
+  __device__ void piece(int from) {
+    qb = from;
+    qe = (int64_t)(g.tiles - from) < end - pos ? g.tiles : from + (int)(end - pos);
+  }
+  // at position `at` < end of the line; pre: where each sequence ends in it
+  __device__ void begin(const WeightArgs& p, const int64_t* pre, int64_t at) {
+    int lo = 0, hi = p.a.g.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] > at) hi = mid; else lo = mid + 1;
+    }
+    sequence(p, lo);
+    const int64_t rem = at - (lo ? pre[lo - 1] : 0);
+    pos = at;
+    u = (int)div_nn(rem, g.tiles);
+    piece((int)(rem - (int64_t)u * g.tiles));
   }
   __device__ bool valid() const { return pos < end; }
-  __device__ void next(const AttnArgs& a) {
-    pos += tiles;
+  __device__ void next(const WeightArgs& p) {
+    pos += qe - qb;
     if (pos >= end) return;
     if (++u >= units) {
       u = 0;
       do {
-        sequence(a, b + 1);                    // pos < end: a later sequence has tiles
-      } while (tiles == 0);
+        sequence(p, b + 1);                    // pos < end: a later sequence has tiles
+      } while (g.tiles == 0);
     }
+    piece(0);
   }
   // this CTA's key block of the unit: first slot, first logical row, keys (0: none)
-  __device__ void keys(uint32_t rank, int64_t S, int64_t& slot0, int64_t& j0, int& valid) const {
-    const int j = 2 * u + (int)rank;
+  __device__ void keys(uint32_t side, int64_t S, int64_t& slot0, int64_t& j0, int& valid) const {
+    const int j = 2 * u + (int)side;
     if (j < s.blk.nblk) {
       s.blk.get(j, slot0, j0, valid);
     } else {
@@ -116,18 +171,40 @@ struct UnitWalk {
   }
 };
 
-// The walk of pair c of P: the tiles of all units (sequence after sequence) make one line, and a
-// pair takes the units that start in its equal share of it.
+// The groups of a tile, taken off in order.
+struct GroupCursor {
+  uint64_t left;
+  int k;
+  __device__ void begin(const Groups& g, int tile, int per_tile) {
+    left = g.set;
+    k = tile * per_tile;
+    if (g.masked)
+      for (int i = 0; i < k; ++i) left &= left - 1;
+  }
+  // the next group, or -1 (masked sets may end inside a tile)
+  __device__ int take(const Groups& g) {
+    if (!g.masked) return k++;
+    if (left == 0) return -1;
+    const int r = __ffsll((long long)left) - 1;
+    left &= left - 1;
+    return r;
+  }
+};
+
+// The tiles of all units, sequence after sequence, make one line of W positions.  Cluster c of C
+// takes the units that start in its equal share of it, [s0, s1); pair k of CP an equal part of
+// those positions.
 template <int NT>
-__device__ __forceinline__ void plan_units(const AttnArgs& a, int64_t* pre, int64_t* sums, int P,
-                                           int c, UnitWalk& w) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.g.B;
+__device__ __forceinline__ void plan_units(const WeightArgs& p, int64_t* pre, int64_t* sums, int C,
+                                           int c, UnitWalk& w, int64_t& s0, int64_t& s1) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = p.a.g.B;
   const int per = (B + WT - 1) / WT;
   w.nt = NT;
+  w.pos = w.end = 0;
   int64_t n = 0;
   for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
-    w.sequence(a, b);
-    n += (int64_t)w.units * w.tiles;
+    w.sequence(p, b);
+    n += (int64_t)w.units * w.g.tiles;
     pre[b] = n;
   }
   int64_t x = n;
@@ -146,35 +223,31 @@ __device__ __forceinline__ void plan_units(const AttnArgs& a, int64_t* pre, int6
   }
   for (int b = t * per; b < (t + 1) * per && b < B; ++b) pre[b] += before;
   __syncthreads();
-  const int64_t each = W / P;
-  const int odd = (int)(W - each * P);
-  auto cut = [&](int k) { return each * k + (int)((uint32_t)(odd * k) / (uint32_t)P); };
-  const int64_t p0 = cut(c), p1 = cut(c + 1);
-  w.pos = w.end = 0;
-  if (p0 >= p1) return;
-  int lo = 0, hi = B - 1;                      // the sequence that holds p0
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] > p0) hi = mid; else lo = mid + 1;
-  }
-  w.sequence(a, lo);
-  const int64_t start = lo ? pre[lo - 1] : 0;
-  w.u = (int)((p0 - start + w.tiles - 1) / w.tiles);         // the first unit at or past p0
-  w.pos = start + (int64_t)w.u * w.tiles;
-  w.end = p1;
-  if (w.pos < w.end && w.u >= w.units) {       // it is the next sequence's first
-    w.u = 0;
-    do {
-      w.sequence(a, w.b + 1);
-    } while (w.tiles == 0);
-  }
+  const int64_t each = div_nn(W, C);
+  const int odd = (int)(W - each * C);
+  // the first unit that starts at or past cluster k's share of the line
+  auto start = [&](int k) {
+    const int64_t at = each * k + (int)((uint32_t)(odd * k) / (uint32_t)C);
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] > at) hi = mid; else lo = mid + 1;
+    }
+    if (at >= pre[lo]) return at;              // the line's end
+    const int64_t s = lo ? pre[lo - 1] : 0;
+    const TreeGeo g = tree_geo(p.a, lo);
+    const int64_t tiles = div_nn(pre[lo] - s, (g.blk.nblk + 1) / 2);
+    return s + div_nn(at - s + tiles - 1, tiles) * tiles;
+  };
+  s0 = start(c);
+  s1 = start(c + 1);
 }
 
 template <int NSL, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
+__global__ void __launch_bounds__(WT, 1)
     attend_weight_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmQ,
-                         const __grid_constant__ WeightArgs p) {
+                         const __grid_constant__ WeightArgs p, int CP) {
   using LY = WLay<NSL, MODE>;
   constexpr int NT = LY::NT, NST = LY::NST, NRES = LY::NRES;
   extern __shared__ uint8_t smem_raw[];
@@ -183,7 +256,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + LY::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + LY::OFF_MISC + 4);
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, leader = crank & ~1u;
+  const int pair = (int)(crank >> 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const AttnArgs& a = p.a;
 
@@ -208,20 +282,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
   grid_dep_launch();
 
   UnitWalk w;
-  plan_units<NT>(a, reinterpret_cast<int64_t*>(sm), reinterpret_cast<int64_t*>(sm + LY::OFF_MISC + 16),
-                 (int)(gridDim.x >> 1), (int)(blockIdx.x >> 1), w);
+  int64_t* pre = reinterpret_cast<int64_t*>(sm);
+  int64_t s0, s1;                              // the cluster's positions
+  plan_units<NT>(p, pre, reinterpret_cast<int64_t*>(sm + LY::OFF_MISC + 16),
+                 (int)gridDim.x / (2 * CP), (int)blockIdx.x / (2 * CP), w, s0, s1);
+  // a pair's part of them starts at part(pair); RES_Q has one tile per unit, and no units to share
+  auto part = [&](int k) { return s0 + div_nn((s1 - s0) * k, CP); };
+  if (part(pair) < part(pair + 1)) {           // (else the walk is empty)
+    w.end = part(pair + 1);
+    w.begin(p, pre, part(pair));
+  }
   fence_proxy_async_smem();                    // the array is read before TMA writes over it
   __syncthreads();
   // (a pair's loads complete on the even CTA's barriers, but go to each CTA's own memory)
+  float kept = 0.f, kept_base = 0.f;           // a unit this pair began and others went on with
+  int64_t kept_at = -1, kept_end = 0;
 
   if (warp == 8) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      const uint32_t even = mapa(smem_u32(bar), 0);
+      const uint32_t even = mapa(smem_u32(bar), leader);
       uint32_t it = 0, un = 0;                 // stages filled, resident tiles filled
       int res_b = -1;
       bool ok = true;
-      for (; ok && w.valid(); w.next(a)) {
+      for (; ok && w.valid(); w.next(p)) {
         int64_t slot0, j0;
         int valid;
         w.keys(rank, a.g.S, slot0, j0, valid);
@@ -238,10 +322,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
                              (int32_t)(w.qrow0 + rank * (NT / 2)));
           return true;
         };
-        for (int q = 0; ok && q < w.tiles; ++q) {
-          const int64_t row = w.qrow0 + (int64_t)q * NT + rank * (NT / 2);
+        GroupCursor gc;
+        gc.begin(w.g, w.qb, NT / 128);
+        for (int q = w.qb; ok && q < w.qe; ++q) {
+          // this CTA's half of the tile: a group of 128 rows (a missing second one loads any rows)
+          int64_t row = w.qrow0;
+          if (MODE != RES_Q) {
+            const int g0 = gc.take(w.g), g1 = gc.take(w.g);
+            const int g = rank == 0 ? g0 : g1;
+            row += (int64_t)(g < 0 ? 0 : g) * 128;
+          }
           for (int i = 0; ok && i < NSL; ++i, ++it) {
-            if (fill && q == 0) ok = resident(i);
+            if (fill && q == w.qb) ok = resident(i);
             if (!ok) break;
             const int s = it % NST;
             ok = mbar_wait(&bar[LY::B_SE + s], ((it / NST) & 1) ^ 1, abort, a.err, 0x32, it);
@@ -271,13 +363,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
       const uint32_t id = idesc_bf16(256, NT, false, false);
+      const uint16_t both = (uint16_t)(3u << leader);
       uint32_t it = 0, un = 0, tc = 0;
       int res_b = -1;
       bool ok = true;
       while (ok && w.valid()) {
         const bool fill = MODE == RES_K || (MODE == RES_Q && w.b != res_b);
-        const int b = w.b, tiles = w.tiles;
-        w.next(a);                             // the next unit tells whether the boxes are done with
+        const int b = w.b, tiles = w.qe - w.qb;
+        w.next(p);                             // the next unit tells whether the boxes are done with
         const bool last = MODE == RES_K || !w.valid() || w.b != b;
         for (int q = 0; ok && q < tiles; ++q, ++tc) {
           const int acc = tc & 1;
@@ -300,10 +393,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)        // 16-dim steps: +32 bytes inside the swizzle atom
               mma_ss_pair(tmem + acc * 256, da + 2 * k, db + 2 * k, id, (i | k) ? 1u : 0u);
-            mma_commit_pair(&bar[LY::B_SE + s]);
-            if (NRES > 0 && last && q == tiles - 1) mma_commit_pair(&bar[LY::B_RE + i]);
+            mma_commit_pair(&bar[LY::B_SE + s], both);
+            if (NRES > 0 && last && q == tiles - 1) mma_commit_pair(&bar[LY::B_RE + i], both);
           }
-          if (ok) mma_commit_pair(&bar[LY::B_AF + acc]);
+          if (ok) mma_commit_pair(&bar[LY::B_AF + acc], both);
         }
         if (fill) {
           ++un;
@@ -315,25 +408,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
     // ---------------------------------------------------------------- epilogue warpgroups
     const int wg = warp >> 2, t = tid & 127;   // accumulator, key = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t drained = mapa(smem_u32(&bar[LY::B_AE + wg]), 0);
+    const uint32_t drained = mapa(smem_u32(&bar[LY::B_AE + wg]), leader);
     float2* rowbuf = reinterpret_cast<float2*>(sm + LY::OFF_ROW) + wg * 512;
     float* handed = reinterpret_cast<float*>(sm + LY::OFF_SUM);
-    const int H = a.g.H;
+    const uint32_t H = (uint32_t)a.g.H;
     uint32_t tc = 0, mine = 0;                 // tiles of the pair, tiles this warpgroup has taken
-    // sequences without nodes have no tiles: their totals pass through
-    if (p.win != p.out)
-      for (int b = blockIdx.x; b < a.g.B; b += gridDim.x) {
-        const Window v = load_window(a.window, b, a.g.S, a.n_q);
-        if (v.nodes > 0) continue;
-        for (int j = tid; j < v.rows; j += 256) {
-          const int64_t at = (int64_t)b * a.g.S + v.slot(j, a.g.S);
-          p.out[at] = p.win ? p.win[at] : 0.f;
-        }
+    // sequences that add nothing have no tiles: their totals pass through
+    for (int b = blockIdx.x; b < a.g.B; b += gridDim.x) {
+      const Window v = load_window(a.window, b, a.g.S, a.n_q);
+      if (v.len() == 0 || row_groups(p, b, (int64_t)v.nodes * H, NT).tiles > 0) continue;
+      for (int j = tid; j < v.len(); j += 256) {
+        const int64_t at = (int64_t)b * a.g.S + v.slot(j, a.g.S);
+        p.out[at] = j < v.rows && p.win ? p.win[at] : 0.f;
       }
+    }
     // After an expired wait the warps still walk to the end (each further wait gives up at once):
     // the warpgroups meet at named barriers.
     bool ok = true;
-    for (; w.valid(); w.next(a)) {
+    for (; w.valid(); w.next(p)) {
       int64_t slot0, j0;
       int valid;
       w.keys(rank, a.g.S, slot0, j0, valid);
@@ -346,22 +438,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
       };
       float total = 0.f;
       bool took = false;
-      for (int q = 0; q < w.tiles; ++q, ++tc) {
+      GroupCursor gc;
+      gc.begin(w.g, w.qb, NT / 128);
+      for (int q = w.qb; q < w.qe; ++q, ++tc) {
+        // the tile's groups of 128 columns: first row and rows of each (0: nothing there)
+        uint32_t row[NT / 128];
+        int n[NT / 128];
+#pragma unroll
+        for (int h = 0; h < NT / 128; ++h) {
+          const int g = gc.take(w.g);
+          row[h] = (uint32_t)(g < 0 ? 0 : g) * 128u;
+          const int64_t left = g < 0 ? 0 : w.rows - (int64_t)row[h];
+          n[h] = left < 0 ? 0 : (left < 128 ? (int)left : 128);
+        }
         if ((int)(tc & 1) != wg) continue;
         took = true;
-        const int64_t r0 = (int64_t)q * NT;
-        const int n = w.rows - r0 < NT ? (int)(w.rows - r0) : NT;        // rows of the tile
         // log-sum-exps (log2 units) and weights of the tile's rows; a row that adds nothing has
         // an infinite one, so that its exponentials are 0
         float2* rb = rowbuf + (mine & 1) * 256;
-        for (int e = t; e < NT; e += 128) {
+#pragma unroll
+        for (int h = 0; h < NT / 128; ++h) {
           float2 v = make_float2(INFINITY, 0.f);
-          if (e < n) {
-            const float l = p.lse[w.qrow0 + r0 + e];
-            const float g = p.qw ? p.qw[(int64_t)w.b * a.n_q + (uint32_t)(r0 + e) / (uint32_t)H] : 1.f;
+          if (t < n[h]) {
+            const float l = p.lse[w.qrow0 + row[h] + t];
+            const float g = p.qw ? p.qw[(int64_t)w.b * a.n_q + (row[h] + t) / H] : 1.f;
             if (g != 0.f && l != -INFINITY) v = make_float2(l * 1.4426950408889634f, g);
           }
-          rb[e] = v;
+          rb[h * 128 + t] = v;
         }
         named_bar(1 + wg, 128);
         ok = __all_sync(FULL, ok && mbar_wait_cluster(&bar[LY::B_AF + wg], mine & 1, abort, a.err,
@@ -369,7 +472,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
         ++mine;
         tc_fence_after();
         const uint32_t acc = tmem + lane_base + wg * 256;
-        const float4* rv = reinterpret_cast<const float4*>(rb);
 #pragma unroll 1
         for (int c0 = 0; c0 < NT; c0 += 32) {
           uint32_t v[32];
@@ -380,15 +482,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(drained);
           }
-          if (!ok || c0 >= n) continue;
-          // the nodes of these 32 rows, where they matter
-          const uint32_t row = (uint32_t)(r0 + c0);
-          const uint32_t i0 = nodes ? row / (uint32_t)H : 0, i1 = nodes ? (row + 31) / (uint32_t)H : 0;
+          // rows of these 32 columns that exist, the first one, and (where it matters) their nodes
+          const bool second = NT > 128 && c0 >= 128;
+          const int live = (second ? n[NT / 128 - 1] : n[0]) - (c0 & 127);
+          if (!ok || live <= 0) continue;
+          const uint32_t r0 = (second ? row[NT / 128 - 1] : row[0]) + (c0 & 127);
+          const uint32_t i0 = nodes ? r0 / H : 0, i1 = nodes ? (r0 + 31) / H : 0;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          if (c0 + 32 <= n && i0 == i1) {
+          if (live >= 32 && i0 == i1) {
+            const float4* rv = reinterpret_cast<const float4*>(rb + c0);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float4 x = rv[c0 / 2 + e];         // two rows' (lse, weight)
+              const float4 x = rv[e];                  // two rows' (lse, weight)
               const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), p.c2, -x.x));
               const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), p.c2, -x.z));
               sum[(2 * e) & 3] = fmaf(p0, x.y, sum[(2 * e) & 3]);
@@ -402,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
             for (int e = 0; e < 32; ++e) {
               const float2 x = rb[c0 + e];
               const float pe = ex2(fmaf(__uint_as_float(v[e]), p.c2, -x.x));
-              const bool in = c0 + e < n && (!nodes || sees((row + e) / (uint32_t)H));
+              const bool in = e < live && (!nodes || sees((r0 + e) / H));
               if (in) sum[e & 3] = fmaf(pe, x.y, sum[e & 3]);
             }
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -410,60 +515,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WT, 1)
         }
       }
       const int64_t at = (int64_t)w.b * a.g.S + slot0 + t;
-      if (w.tiles == 1) {
-        // one warpgroup had the unit to itself
-        if (took && ok && t < valid)
+      if (MODE == RES_Q) {
+        // one warpgroup has the unit to itself
+        if (took && ok && t < valid) p.out[at] = (p.win && node < 0 ? p.win[at] : 0.f) + total;
+        continue;
+      }
+      // the sum of the even tiles plus that of the odd ones
+      if (wg == 1) handed[t] = total;
+      named_bar(3, 256);
+      total += handed[t];
+      named_bar(3, 256);
+      if (wg == 0) {
+        if (w.qb > 0) {
+          // another pair started this unit: it is the last one whose part starts at or before it
+          int k = pair - 1;
+          while (k > 0 && part(k) > w.pos - w.qb) --k;
+          st_cluster_f32(mapa(smem_u32(sm + LY::OFF_PART + (pair * 128 + t) * 4), 2 * k + rank), total);
+        } else if (w.qe < w.g.tiles) {
+          // other pairs go on with it: kept until their sums are here
+          kept = total;
+          kept_end = w.pos + w.g.tiles;
+          kept_at = t < valid && ok ? at : -1;
+          kept_base = p.win && node < 0 && t < valid ? p.win[at] : 0.f;
+        } else if (ok && t < valid) {
           p.out[at] = (p.win && node < 0 ? p.win[at] : 0.f) + total;
-      } else {
-        // the sum of the even tiles plus that of the odd ones
-        if (wg == 1) handed[t] = total;
-        named_bar(3, 256);
-        if (wg == 0 && ok && t < valid)
-          p.out[at] = (p.win && node < 0 ? p.win[at] : 0.f) + (total + handed[t]);
-        named_bar(3, 256);
+        }
       }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                              // no remote access into this CTA is pending
+  cluster_sync();                              // the pairs' sums are here; no remote access is pending
+  if (kept_at >= 0) {
+    const float* others = reinterpret_cast<const float*>(sm + LY::OFF_PART) + tid;
+    for (int k = pair + 1; k < CP && part(k) < kept_end; ++k)
+      if (part(k) < part(k + 1)) kept += others[k * 128];
+    p.out[kept_at] = kept_base + kept;
+  }
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
 }
 
+// Clusters of cp pairs that can be resident at once on the current device (0: error).
 template <int NSL, int MODE>
-cudaError_t launch_weight(const CUtensorMap& K, const CUtensorMap& Q, const WeightArgs& p,
-                          cudaStream_t st) {
+int weight_clusters(int cp) {
   using LY = WLay<NSL, MODE>;
   static std::mutex mu;
-  static int pairs[64] = {0};
+  static int cached[64][MAXCP + 1] = {};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  int n;
-  {
-    // the shared-memory opt-in and the pairs that can be resident at once, per device
-    std::lock_guard<std::mutex> lock(mu);
-    n = dev < 64 ? pairs[dev] : 0;
-    if (n == 0) {
-      e = cudaFuncSetAttribute(attend_weight_kernel<NSL, MODE>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
-      if (e != cudaSuccess) return e;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * MAXC);
-      cfg.blockDim = dim3(WT);
-      cfg.dynamicSmemBytes = LY::SMEM;
-      e = cudaOccupancyMaxActiveClusters(&n, attend_weight_kernel<NSL, MODE>, &cfg);
-      if (e != cudaSuccess) return e;
-      n = n < 1 ? 1 : (n > MAXC ? MAXC : n);
-      if (dev < 64) pairs[dev] = n;
-    }
-  }
-  e = launch_dependent(attend_weight_kernel<NSL, MODE>, (unsigned)(2 * n), WT, LY::SMEM, st, 1u, K,
-                       Q, p);
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && cached[dev][cp] > 0) return cached[dev][cp];
+  // also opts the kernel in to its shared memory, once per device
+  if (cudaFuncSetAttribute(attend_weight_kernel<NSL, MODE>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * MAXC);
+  cfg.blockDim = dim3(WT);
+  cfg.dynamicSmemBytes = LY::SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2 * cp;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, attend_weight_kernel<NSL, MODE>, &cfg) != cudaSuccess)
+    return 0;
+  n = n < 1 ? 1 : (n > MAXC ? MAXC : n);
+  if (dev < 64) cached[dev][cp] = n;
+  return n;
+}
+
+template <int NSL, int MODE>
+cudaError_t launch_weight(const CUtensorMap& K, const CUtensorMap& Q, const WeightArgs& p, int cp,
+                          cudaStream_t st) {
+  const int n = weight_clusters<NSL, MODE>(cp);
+  if (n == 0) return cudaErrorInvalidDevice;
+  const cudaError_t e =
+      launch_dependent(attend_weight_kernel<NSL, MODE>, (unsigned)(2 * cp * n), WT,
+                       WLay<NSL, MODE>::SMEM, st, (unsigned)(2 * cp), K, Q, p, cp);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -504,9 +639,11 @@ cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, c
     uint32_t b[2] = {64, few ? 64u : 128u};
     if (!make_tmap_bf16(&Q, q_abs, 2, d, s, b)) return cudaErrorInvalidValue;
   }
+  static const int cps = getenv("WCP") ? atoi(getenv("WCP")) : 2;
+  const int cp = cps;
   if (g.Dr == 64)
-    return few ? launch_weight<9, RES_Q>(K, Q, p, st) : launch_weight<9, RES_K>(K, Q, p, st);
-  return few ? launch_weight<16, RES_Q>(K, Q, p, st) : launch_weight<16, STREAM>(K, Q, p, st);
+    return few ? launch_weight<9, RES_Q>(K, Q, p, 1, st) : launch_weight<9, RES_K>(K, Q, p, cp, st);
+  return few ? launch_weight<16, RES_Q>(K, Q, p, 1, st) : launch_weight<16, STREAM>(K, Q, p, cp, st);
 }
 
 }  // namespace mla

@@ -79,6 +79,9 @@ CASES = [
     ("MAIN", 70, 200, [(190, 130, 70), (0, 0, 70), (4, 31, 65), (1, 5, 1), (0, 200, 9)]),
     ("HEADS", 3, 520, [(500, 517, 3), (0, 0, 2), (10, 447, 3)]),
     ("HEADS", 1, 700, [(600, 699, 1), (0, 2, 1), (0, 2, 0)]),
+    # fewer key blocks than clusters, cut inside tiles
+    ("HEADS", 1, 2700, [(2600, 2600, 1)]),
+    ("HEADS", 2, 3000, [(5, 2990, 2), (0, 1500, 1)]),
     ("VIDEO", 20, 150, [(140, 97, 20), (2, 0, 13), (0, 128, 20)]),
     ("WIDE", 9, 150, [(140, 97, 9), (2, 0, 5), (0, 64, 9)]),
 ]
