@@ -1145,6 +1145,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           }
         }
         ++xc;
+        // (a thread's `need` takes in its last load, and shared loads return in order: the barrier
+        // below is reached with the buffer read)
         // The decision: a word per warpgroup and block (four in turn, each cleared two blocks
         // before its next use) collects the rows' flags across the barrier that also
         // marks the buffer as read.  Both CTAs see the same pairs of flags.
@@ -1157,9 +1159,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         if (exact) {
           // Rounds two and three: undo the fp16 addend (s then holds this CTA's partial to
           // within one float32 rounding) and swap exact fp32 partials, keys 0-31 then 32-63.
+          // A buffer is handed back once every thread HAS its values: a barrier alone does not wait
+          // for loads in flight, and the peer's next stores do not queue behind them.  The barriers
+          // below therefore carry a predicate of every vector that was loaded.
+          uint32_t seen = 0u;
 #pragma unroll
-          for (int q = 0; q < BN / 8; ++q) sub_f16x8(my_x[q * TM], s + 8 * q);
-          named_bar(1 + wg, TM);                 // the buffer is read again before hand-back
+          for (int q = 0; q < BN / 8; ++q) {
+            const uint4 x = my_x[q * TM];
+            seen |= x.x;
+            sub_f16x8(x, s + 8 * q);
+          }
+          named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);   // read again, before the hand-back
           if (t == 0) {
             mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
             mbar_arrive_cluster_relaxed(peer_xe);
@@ -1184,13 +1194,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
 #pragma unroll
             for (int q = 0; q < BN / 8; ++q) {
               const uint4 x = my_x[q * TM];
+              seen |= x.x;
               s[32 * h + 4 * q] += __uint_as_float(x.x);
               s[32 * h + 4 * q + 1] += __uint_as_float(x.y);
               s[32 * h + 4 * q + 2] += __uint_as_float(x.z);
               s[32 * h + 4 * q + 3] += __uint_as_float(x.w);
             }
             ++xc;
-            named_bar(1 + wg, TM);
+            named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);
             if (h == 0 && t == 0) mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);   // round three
             // with merged buffers the last round's buffer is handed back by the PV commit
             if (!LY::MERGED || h == 0) {
