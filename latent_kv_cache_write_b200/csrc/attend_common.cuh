@@ -69,14 +69,6 @@ struct TileGeo {
   Blocks blk;
 };
 
-// A key range of L logical rows from ring slot p1, in at most two contiguous slot runs.
-__host__ __device__ inline void lay_blocks(Blocks& k, int64_t S, int bn) {
-  k.n1 = k.L < S - k.p1 ? k.L : S - k.p1;
-  k.bn = bn;
-  k.nb1 = (int)((k.n1 + bn - 1) / bn);
-  k.nblk = k.nb1 + (int)((k.L - k.n1 + bn - 1) / bn);
-}
-
 // one past the last key query i sees (frame-block-causal, clipped to the key window)
 __host__ __device__ inline int64_t key_end(const Geo& G, int64_t q_first, int64_t k_lim,
                                            int64_t i) {
@@ -99,14 +91,11 @@ __host__ __device__ inline TileGeo tile_geo(const Geo& G, int64_t n_q, int64_t q
   k.k_first = k_first;
   k.L = key_end(G, q_first, k_first + n_keys, t.i_last) - k_first;
   k.p1 = k_first % G.S;
-  lay_blocks(k, G.S, bn);
+  k.n1 = k.L < G.S - k.p1 ? k.L : G.S - k.p1;
+  k.bn = bn;
+  k.nb1 = (int)((k.n1 + bn - 1) / bn);
+  k.nblk = k.nb1 + (int)((k.L - k.n1 + bn - 1) / bn);
   return t;
-}
-
-// a / b for a >= 0, b > 0: the 64-bit division is a long subroutine, and the plan stands before
-// every call's first load.
-__device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Draft trees: a sequence's tiles of 128 (node, head) rows, and the key blocks (context, then
@@ -117,16 +106,80 @@ struct TreeGeo {
   Blocks blk;
 };
 
-__device__ __forceinline__ TreeGeo tree_geo(const AttnArgs& a, int64_t b) {
-  const Window w = load_window(a.window, b, a.g.S, a.n_q);
+// BN keys per block (a power of two).  Everything fits 32 bits: rows and slots are below 2^31.
+template <int BN>
+__device__ __forceinline__ TreeGeo tree_geo(const AttnArgs& a, const Window& w) {
   TreeGeo t;
   t.ctx = w.rows;
-  t.tiles = (int)(((int64_t)w.nodes * a.g.H + TM - 1) / TM);
+  t.tiles = (int)(((uint32_t)w.nodes * (uint32_t)a.g.H + (TM - 1)) / TM);
+  const uint32_t L = (uint32_t)w.len(), run = (uint32_t)a.g.S - (uint32_t)w.first;
+  const uint32_t n1 = L < run ? L : run;
   t.blk.k_first = 0;                       // global tokens become logical rows
   t.blk.p1 = w.first;
-  t.blk.L = w.len();
-  lay_blocks(t.blk, a.g.S, a.bn);
+  t.blk.L = L;
+  t.blk.n1 = n1;
+  t.blk.bn = BN;
+  t.blk.nb1 = (int)((n1 + (BN - 1)) / BN);
+  t.blk.nblk = t.blk.nb1 + (int)((L - n1 + (BN - 1)) / BN);
   return t;
+}
+template <int BN>
+__device__ __forceinline__ TreeGeo tree_geo(const AttnArgs& a, int64_t b) {
+  return tree_geo<BN>(a, load_window(a.window, b, a.g.S, a.n_q));
+}
+
+// A line of work: every sequence takes tiles x blocks positions of it, one after the other (sizes
+// are checked by the host: the line is shorter than 2^31).  The functions below are
+// warp-collective and every warp of every CTA calls them for itself before its first load, so
+// they keep to registers and to little code: lane l looks at sequence l, l + 32, ...
+struct Span {
+  uint32_t tiles, blocks;
+};
+struct Spot {
+  int b;                    // the sequence
+  uint32_t start, off;      // where its positions start, and the position inside them
+  Span s;
+};
+
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {     // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// The sequences that hold positions p[0] .. p[N - 1], each below the line's length; span(b) gives a
+// sequence's sizes and `mine` is span(lane) (B > 0; zero sizes past the last sequence).
+template <int N, typename F>
+__device__ __forceinline__ void line_find(int B, const F& span, Span mine, const uint32_t (&p)[N],
+                                          Spot (&at)[N]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t before = 0;
+  unsigned found = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const uint32_t n = mine.tiles * mine.blocks, end = before + warp_scan(n);
+    bool all = true;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const unsigned past = __ballot_sync(0xffffffffu, end > p[k]);
+      if (past && !(found >> k & 1)) {
+        found |= 1u << k;
+        const int l = __ffs(past) - 1;
+        at[k].b = b0 + l;
+        at[k].start = __shfl_sync(0xffffffffu, end - n, l);
+        at[k].off = p[k] - at[k].start;
+        at[k].s.tiles = __shfl_sync(0xffffffffu, mine.tiles, l);
+        at[k].s.blocks = __shfl_sync(0xffffffffu, mine.blocks, l);
+      }
+      all = all && past;
+    }
+    if (all || b0 + 32 >= B) return;           // (the latter only as a bound)
+    before = __shfl_sync(0xffffffffu, end, 31);
+    mine = b0 + 32 + lane < B ? span(b0 + 32 + lane) : Span{0, 0};
+  }
 }
 
 // Split tiles to merge: tile[i] has the partial segments in workspace slots

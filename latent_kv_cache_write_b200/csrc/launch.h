@@ -130,9 +130,9 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
                            void* workspace, size_t workspace_bytes, unsigned int* err,
                            cudaStream_t st);
 
-// The attention of draft nodes (bf16, d_c = 512, d_R = 64 or 512, at most 6144 sequences).  Its
+// The attention of draft nodes (bf16, d_c = 512, d_R = 64 or 512).  Its
 // workspace may be null: tiles then stay whole.
-bool tc_attend_tree_supported(const Geo& g);
+bool tc_attend_tree_supported(const Geo& g, int64_t n_nodes);
 size_t tc_attend_tree_workspace(const Geo& g);
 cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
                            const int32_t* window, const uint8_t* tree, float scale, void* o_lat,
@@ -140,7 +140,7 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
                            cudaStream_t st);
 
 // The attention weight of cached rows (tc_weight.cu; the same shapes).
-bool tc_attend_weight_supported(const Geo& g);
+bool tc_attend_weight_supported(const Geo& g, int64_t n_nodes);
 cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
                              const int32_t* window, const uint8_t* tree, float scale,
                              const float* lse, const float* qw, const float* win, float* wout,

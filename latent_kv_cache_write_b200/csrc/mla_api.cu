@@ -439,10 +439,9 @@ mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const v
 }
 
 size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes) {
-  (void)n_nodes;
   Geo g;
   if (check_shape(shape, &g) != MLA_OK) return 0;
-  if (shape->dtype == MLA_BF16 && tc_attend_tree_supported(g)) return tc_attend_tree_workspace(g);
+  if (shape->dtype == MLA_BF16 && tc_attend_tree_supported(g, n_nodes)) return tc_attend_tree_workspace(g);
   return 0;
 }
 
@@ -461,7 +460,7 @@ mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_
   if (workspace && !aligned16(workspace)) return MLA_ERR_ALIGN;
   if (n_nodes == 0) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
-  if (bf && tc_attend_tree_supported(g))
+  if (bf && tc_attend_tree_supported(g, n_nodes))
     return cuda_status(tc_attend_tree(g, q_abs, n_nodes, cache, window, tree, softmax_scale, o_lat,
                                       lse, workspace, workspace_bytes, device_error_word(),
                                       (cudaStream_t)stream));
@@ -481,7 +480,7 @@ mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t 
     return MLA_ERR_ALIGN;
   if (n_nodes == 0) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
-  if (bf && tc_attend_weight_supported(g))
+  if (bf && tc_attend_weight_supported(g, n_nodes))
     return cuda_status(tc_attend_weight(g, q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
                                         query_weight, weight_in, weight_out, device_error_word(),
                                         (cudaStream_t)stream));

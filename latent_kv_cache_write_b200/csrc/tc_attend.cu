@@ -208,31 +208,26 @@ struct SegWalk {
 // (sc.l2_blocks); otherwise R = 0 and a cluster's share is one range.
 struct TreeSched {
   int split;                // tiles may be split (there is a workspace)
-  int64_t l2_blocks;        // key blocks beyond which tiles go in rounds
+  uint32_t l2_blocks;       // key blocks beyond which tiles go in rounds
 };
 
-constexpr int TREE_MAXB = 6144;                // sequences the plan's arrays hold
+constexpr int TREE_MAXB = 8192;                // sequences the plan's arrays hold
 constexpr int TREE_MAXR = 32;                  // rounds
 // The plan's arrays (shared memory, where the K/V ring will be), and what stays of it: the
 // sequence and tile of each round.
-struct TreePlan {
-  int64_t pre[TREE_MAXB];                      // blocks of the line up to each sequence's end
-  int32_t tpre[TREE_MAXB];                     // tiles likewise
-  int32_t nblk[TREE_MAXB];                     // key blocks of each sequence's tiles
-};
-struct TreeSum {
-  int64_t blocks, keys;
-  int32_t tiles, longest;
+struct TreePlan {                              // only for rounds
+  uint32_t pre[TREE_MAXB];                     // blocks of the line up to each sequence's end
+  uint32_t tpre[TREE_MAXB];                    // tiles likewise
+  uint32_t nblk[TREE_MAXB];                    // key blocks of each sequence's tiles
 };
 struct TreeScratch {                           // shared memory, next to the plan
-  int64_t start[MAXC + 1];                     // where each cluster's tail starts
-  TreeSum warp[16];
+  uint32_t start[MAXC + 1];                    // where each cluster's tail starts
+  uint32_t warp[16][2];
   int rounds;
 };
 
 // The first sequence whose part of a line ends past p.
-template <typename T>
-__device__ __forceinline__ int tree_find(const T* pre, int B, int64_t p) {
+__device__ __forceinline__ int tree_find(const uint32_t* pre, int B, uint32_t p) {
   int lo = 0, hi = B - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -244,7 +239,7 @@ __device__ __forceinline__ int tree_find(const T* pre, int B, int64_t p) {
 // The segments of one cluster's share, as SegWalk.  A cluster has at most two partial segments,
 // the first and the last of its tail: workspace slots 2 c and 2 c + 1.
 struct TreeWalk {
-  int64_t left;             // blocks of the tail from its current segment on
+  int left;                 // blocks of the tail from its current segment on
   int r, R;                 // round, rounds
   const int2* rounds;       // (sequence, tile) of each round
   int tail_b, tail_tb, tail_jb;
@@ -253,8 +248,9 @@ struct TreeWalk {
   int k, gbase, nbase[2], slot;
   TileGeo tg;
 
-  __device__ void begin(const AttnArgs& a, const TreePlan& pl, const int2* list, int n_rounds,
-                        int64_t p0, int64_t p1, int c) {
+  // the tail: n blocks from block `off` of sequence b's tiles on
+  __device__ void begin(const AttnArgs& a, const int2* list, int n_rounds, int b, uint32_t off,
+                        uint32_t nblk, uint32_t n, int c) {
     k = 0;
     gbase = 0;
     nbase[0] = nbase[1] = 0;
@@ -262,30 +258,29 @@ struct TreeWalk {
     r = 0;
     R = n_rounds;
     rounds = list;
-    left = p1 - p0;
+    left = n;
     tail_b = tail_tb = -1;
     tail_jb = 0;
-    if (left > 0) {
-      tail_b = tree_find(pl.pre, a.g.B, p0);
-      const int64_t rem = p0 - (tail_b ? pl.pre[tail_b - 1] : 0);
-      tail_tb = (int)div_nn(rem, pl.nblk[tail_b]);
-      tail_jb = (int)(rem - (int64_t)tail_tb * pl.nblk[tail_b]);
+    if (n > 0) {
+      tail_b = b;
+      tail_tb = (int)(off / nblk);
+      tail_jb = (int)(off - (uint32_t)tail_tb * nblk);
     }
     load(a);
   }
   __device__ void sequence(const AttnArgs& a, int b) {
-    const TreeGeo s = tree_geo(a, b);
+    const TreeGeo s = tree_geo<64>(a, b);
     tiles = s.tiles;
     ctx = s.ctx;
     tg.blk = s.blk;
     tg.b = b;
     tg.rows_b = (int64_t)(s.blk.L - s.ctx) * a.g.H;
   }
-  __device__ void tile(const AttnArgs& a, int from, int64_t most) {
+  __device__ void tile(const AttnArgs& a, int from, int most) {
     tg.row0 = (int64_t)tb * TM;
     tg.grow0 = (int64_t)tg.b * a.n_q * a.g.H + tg.row0;
     jb = from;
-    je = (int64_t)(tg.blk.nblk - from) < most ? tg.blk.nblk : from + (int)most;
+    je = tg.blk.nblk - from < most ? tg.blk.nblk : from + most;
   }
   // the segment of round r, or the tail's first
   __device__ void load(const AttnArgs& a) {
@@ -331,146 +326,152 @@ struct TreeWalk {
 
 // Costs in key blocks: of a segment (the switch: Q reload, output epilogue, pipeline refill), and of
 // split tiles (the merge).  Measured on B200 (video chunk, long window and decode shapes).
-constexpr int64_t SEG_COST = 7, COMBINE_COST = 16;
+constexpr int SEG_COST = 7, COMBINE_COST = 16;
 
-// Plan of cluster c of G: its rounds (list, returned count) and its tail [p0, p1).  Every thread of
-// the CTA takes part.
-template <int NT>
-__device__ __forceinline__ int tree_plan(const AttnArgs& a, const TreeSched& sc, TreePlan& pl,
-                                         TreeScratch& x, int2* list, int G, int c, int64_t& p0,
-                                         int64_t& p1) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.g.B;
+// Where cluster u's equal share of a line of W positions starts.
+__device__ __forceinline__ uint32_t line_cut(uint32_t W, uint32_t G, uint32_t u) {
+  const uint32_t each = W / G, odd = W - each * G;
+  return each * u + odd * u / G;
+}
+
+// Rounds: how many every cluster takes (returned, with cluster c's in `list`), and where the tails
+// start (x.start).  Every thread of the CTA takes part; span: a sequence's tiles and key blocks.
+template <int NT, typename F>
+__device__ __forceinline__ int tree_rounds(const F& span, TreePlan& pl, TreeScratch& x, int2* list,
+                                           int B, uint32_t W, uint32_t T, int G, int c) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int per = (B + NT - 1) / NT;
   if (t == 0) x.rounds = INT32_MAX;
   // where each sequence ends in the line: the threads' runs of sequences, then a scan
-  int64_t blocks = 0, keys = 0;
-  int tiles = 0, longest = 0;
+  uint32_t blocks = 0, tiles = 0;
   for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
-    const TreeGeo s = tree_geo(a, b);
-    blocks += (int64_t)s.tiles * s.blk.nblk;
+    const Span s = span(b);
+    blocks += s.tiles * s.blocks;
     tiles += s.tiles;
-    if (s.tiles > 0) {
-      keys += s.blk.nblk;
-      longest = max(longest, s.blk.nblk);
-    }
     pl.pre[b] = blocks;
     pl.tpre[b] = tiles;
-    pl.nblk[b] = s.blk.nblk;
+    pl.nblk[b] = s.blocks;
   }
-  const int warps = (B + 32 * per - 1) / (32 * per);         // warps that hold sequences
-  if (warp < warps) {
-    int64_t xb = blocks;
-    int xt = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t yb = __shfl_up_sync(FULL, xb, o);
-      const int yt = __shfl_up_sync(FULL, xt, o);
-      if (lane >= o) {
-        xb += yb;
-        xt += yt;
-      }
-      keys += __shfl_xor_sync(FULL, keys, o);
-    }
-    longest = __reduce_max_sync(FULL, longest);
-    if (lane == 31) x.warp[warp] = TreeSum{xb, keys, xt, longest};
-    blocks = xb - blocks;
-    tiles = xt - tiles;
+  const uint32_t xb = warp_scan(blocks), xt = warp_scan(tiles);
+  if (lane == 31) {
+    x.warp[warp][0] = xb;
+    x.warp[warp][1] = xt;
   }
   __syncthreads();
-  int64_t W = 0, K = 0;
-  int T = 0, nmax = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w == warp) {
-      blocks += W;
-      tiles += T;
-    }
-    const TreeSum v = x.warp[w];
-    W += v.blocks;
-    K += v.keys;
-    T += v.tiles;
-    nmax = max(nmax, v.longest);
+  blocks = xb - blocks;
+  tiles = xt - tiles;
+  for (int w = 0; w < warp; ++w) {
+    blocks += x.warp[w][0];
+    tiles += x.warp[w][1];
   }
-  p0 = p1 = 0;
-  if (W == 0) return 0;
-  if (warps > 1 || per > 1) {
-    for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
-      pl.pre[b] += blocks;
-      pl.tpre[b] += tiles;
-    }
-  } else if (t < B) {
-    pl.pre[t] += blocks;
-    pl.tpre[t] += tiles;
+  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
+    pl.pre[b] += blocks;
+    pl.tpre[b] += tiles;
   }
   __syncthreads();
-  // equal shares of the line: cluster u's ends at cut(u + 1)
-  const int64_t each = div_nn(W, G);
-  const int odd = (int)(W - each * G);
-  auto cut = [&](int u) { return each * u + (int)((uint32_t)(odd * u) / (uint32_t)G); };
-  int R = 0;
-  p0 = cut(c);
-  p1 = cut(c + 1);
-  if (K > sc.l2_blocks && a.tiles_per_batch > 2) {
-    // thread u < G: how many rounds cluster u's share holds
-    auto round_blocks = [&](int r) { return pl.nblk[tree_find(pl.tpre, B, (int64_t)r * G + t)]; };
-    const int most = T / G < TREE_MAXR ? T / G : TREE_MAXR;
-    const int64_t share = t < G ? cut(t + 1) - cut(t) : 0;
-    if (t < G) {
-      int r = 0;
-      for (int64_t d = 0; r < most; ++r) {
-        d += round_blocks(r);
-        if (d > share) break;
-      }
-      atomicMin(&x.rounds, r);
+  // thread u < G: how many rounds cluster u's share holds
+  auto round_blocks = [&](int r) { return pl.nblk[tree_find(pl.tpre, B, (uint32_t)(r * G + t))]; };
+  const uint32_t share = t < G ? line_cut(W, G, t + 1) - line_cut(W, G, t) : 0;
+  if (t < G) {
+    const int most = T / G < (uint32_t)TREE_MAXR ? (int)(T / G) : TREE_MAXR;
+    int r = 0;
+    for (uint32_t d = 0; r < most; ++r) {
+      d += round_blocks(r);
+      if (d > share) break;
     }
-    __syncthreads();
-    R = x.rounds;
-    // the tails share the line from where the rounds' R G tiles end
-    int64_t rest = share;
-    if (t < G)
-      for (int r = 0; r < R; ++r) rest -= round_blocks(r);
-    int64_t xr = rest;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(FULL, xr, o);
-      if (lane >= o) xr += y;
-    }
-    __syncthreads();                          // x.warp has been read
-    if (lane == 31) x.warp[warp].blocks = xr;
-    __syncthreads();
-    const int done = R * G;
-    int64_t line = 0;
-    if (done > 0) {
-      const int b = tree_find(pl.tpre, B, done - 1);
-      line = (b ? pl.pre[b - 1] : 0) + (int64_t)(done - (b ? pl.tpre[b - 1] : 0)) * pl.nblk[b];
-    }
-    for (int w = 0; w < warp; ++w) line += x.warp[w].blocks;
-    if (t < G) x.start[t] = line + xr - rest;
-    if (t == 0) x.start[G] = W;
-    __syncthreads();
-    p0 = x.start[c];
-    p1 = x.start[c + 1];
+    atomicMin(&x.rounds, r);
   }
-  // Split tiles, or cut on tile boundaries?  Whole tiles take as long as the longest one, or a share
-  // plus what rounding up to tiles adds (for sequences of one length (ceil(T / G) - T / G) tiles);
-  // split ones take a share, one segment more and the merge.
-  const float share = (float)W / (float)G, up_tiles = (float)((T + G - 1) / G) - (float)T / (float)G;
-  const float whole = fmaxf((float)nmax, share + up_tiles * (float)nmax);
-  if (!sc.split || whole <= share + (float)(SEG_COST + COMBINE_COST)) {
-    auto up = [&](int64_t p) {                // the first boundary at or past p
-      const int b = tree_find(pl.pre, B, p);
-      if (p >= pl.pre[b]) return pl.pre[b];   // p == W
-      const int64_t s = b ? pl.pre[b - 1] : 0, n = pl.nblk[b];
-      return s + div_nn(p - s + n - 1, n) * n;
-    };
-    p0 = up(p0);
-    p1 = up(p1);
+  __syncthreads();
+  const int R = x.rounds;
+  // the tails share the line from where the rounds' R G tiles end
+  uint32_t rest = share;
+  if (t < G)
+    for (int r = 0; r < R; ++r) rest -= round_blocks(r);
+  const uint32_t xr = warp_scan(rest);
+  if (lane == 31) x.warp[warp][0] = xr;
+  __syncthreads();
+  const uint32_t done = (uint32_t)(R * G);
+  uint32_t line = 0;
+  if (done > 0) {
+    const int b = tree_find(pl.tpre, B, done - 1);
+    line = (b ? pl.pre[b - 1] : 0) + (done - (b ? pl.tpre[b - 1] : 0)) * pl.nblk[b];
   }
+  for (int w = 0; w < warp; ++w) line += x.warp[w][0];
+  if (t < G) x.start[t] = line + xr - rest;
+  if (t == 0) x.start[G] = W;
   for (int r = t; r < R; r += NT) {
-    const int64_t tile = (int64_t)r * G + c;
+    const uint32_t tile = (uint32_t)(r * G + c);
     const int b = tree_find(pl.tpre, B, tile);
     list[r] = make_int2(b, (int)(tile - (b ? pl.tpre[b - 1] : 0)));
   }
+  __syncthreads();
   return R;
+}
+
+// Plan of cluster c of G, and its walk.  Every thread of the CTA takes part.
+template <int NT>
+__device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc, TreePlan& pl,
+                                          TreeScratch& x, int2* list, int G, int c, TreeWalk& sw) {
+  const int lane = threadIdx.x & 31, B = a.g.B;
+  auto span = [&](int b) {
+    const TreeGeo s = tree_geo<64>(a, b);
+    return Span{(uint32_t)s.tiles, (uint32_t)s.blk.nblk};
+  };
+  const Span mine = lane < B ? span(lane) : Span{0, 0};
+  uint32_t W = 0, T = 0, K = 0, nmax = 0;      // blocks, tiles, key blocks, the longest tile
+  for (int b = lane; b - lane < B; b += 32) {
+    const Span s = b == lane ? mine : (b < B ? span(b) : Span{0, 0});
+    W += s.tiles * s.blocks;
+    T += s.tiles;
+    if (s.tiles > 0) {
+      K += s.blocks;
+      nmax = max(nmax, s.blocks);
+    }
+  }
+  W = __reduce_add_sync(FULL, W);
+  T = __reduce_add_sync(FULL, T);
+  K = __reduce_add_sync(FULL, K);
+  nmax = __reduce_max_sync(FULL, nmax);
+  uint32_t p0 = 0, p1 = 0;                     // the tail's ends in the line
+  int R = 0;
+  Spot at[2] = {{0, 0, 0, mine}, {0, 0, 0, mine}};
+  if (W > 0) {
+    p0 = line_cut(W, G, c);
+    p1 = line_cut(W, G, c + 1);
+    if (K > sc.l2_blocks && a.tiles_per_batch > 2 && B <= TREE_MAXB) {
+      R = tree_rounds<NT>(span, pl, x, list, B, W, T, G, c);
+      p0 = x.start[c];
+      p1 = x.start[c + 1];
+      fence_proxy_async_smem();                // the arrays are read before TMA writes over them
+      __syncthreads();
+    }
+    // Split tiles, or cut on tile boundaries?  Whole tiles take as long as the longest one, or a
+    // share plus what rounding up to tiles adds (for sequences of one length (ceil(T / G) - T / G)
+    // tiles); split ones take a share, one segment more and the merge.
+    const float share = (float)W / (float)G;
+    const float up = ((float)((T + G - 1) / G) - (float)T / (float)G) * (float)nmax;
+    const bool whole = !sc.split || fmaxf((float)nmax, share + up) <= share + SEG_COST + COMBINE_COST;
+    if (p0 < p1) {
+      // (an end at W has no sequence: the last position's stands for it)
+      const uint32_t q[2] = {p0, p1 < W ? p1 : W - 1};
+      line_find(B, span, mine, q, at);
+      if (whole) {                             // the first boundaries at or past the cuts
+        const uint32_t n0 = (at[0].off + at[0].s.blocks - 1) / at[0].s.blocks * at[0].s.blocks;
+        const uint32_t n1 = (at[1].off + at[1].s.blocks - 1) / at[1].s.blocks * at[1].s.blocks;
+        p0 += n0 - at[0].off;
+        at[0].off = n0;
+        if (p1 < W) p1 += n1 - at[1].off;
+        // (which may be the start of the next sequence that has tiles)
+        if (p0 < p1 && n0 >= at[0].s.tiles * at[0].s.blocks) {
+          const uint32_t q0[1] = {p0};
+          Spot s[1];
+          line_find(B, span, mine, q0, s);
+          at[0] = s[0];
+        }
+      }
+    }
+  }
+  sw.begin(a, list, R, at[0].b, at[0].off, at[0].s.blocks, p0 < p1 ? p1 - p0 : 0u, c);
 }
 
 template <bool TREE> struct SchedOf { using S = Sched; using Walk = SegWalk; };
@@ -512,23 +513,54 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64]) {
     for (int c = 0; c < 32; ++c) s[32 * h + c] = __uint_as_float(v[h][c]);
 }
 
+// Four lanes (rows) that hold four 16-byte chunks each trade them: lane k of the four ends with
+// chunk k of each row, x[j] from the four's row j; applied again it gives the rows back.  Row-wise
+// accesses then go out as 64 contiguous bytes per four lanes instead of 16 per lane: a warp's access
+// touches 8 lines, not 32, and the load/store unit takes a line per clock.
+__device__ __forceinline__ void quad_transpose(uint4 (&x)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool hi = lane & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      // the pair (i, i + d): the low lane sends its upper chunk for the high lane's lower one
+      const uint4 send = hi ? x[i] : x[i + d];
+      uint4 got;
+      got.x = __shfl_xor_sync(FULL, send.x, d);
+      got.y = __shfl_xor_sync(FULL, send.y, d);
+      got.z = __shfl_xor_sync(FULL, send.z, d);
+      got.w = __shfl_xor_sync(FULL, send.w, d);
+      if (hi) x[i] = got; else x[i + d] = got;
+    }
+  }
+}
+
 // Q latent half of row `grow` -> TMEM columns from `tq` (A operand of the score MMA),
 // bf16 pairs per column; each warpgroup loads half of the row.  All 16 vector loads are
 // issued before the first TMEM store, so their latencies overlap.
 __device__ __forceinline__ void load_q(const AttnArgs& a, uint32_t tq, int64_t grow,
                                        bool row_ok, uint32_t rank, int wg) {
-  const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + grow * a.g.row + rank * HALF +
+  // chunk k (this lane's place among four) of the rows of the four lanes: 16 loads in flight
+  const int k = threadIdx.x & 3;
+  const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (grow - k) * a.g.row + rank * HALF +
                                                     wg * (HALF / 2));
-  uint4 x[16];
+  const unsigned live = __ballot_sync(FULL, row_ok) >> (threadIdx.x & 28);
+  uint4 x[4][4];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) x[q] = row_ok ? src[q] : make_uint4(0, 0, 0, 0);
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[c][j] = (live >> j & 1) ? src[j * (a.g.row / 8) + 4 * c + k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int c = 0; c < HALF / 64; ++c) {
+    quad_transpose(x[c]);
     uint32_t v[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      v[4 * q] = x[4 * c + q].x; v[4 * q + 1] = x[4 * c + q].y;
-      v[4 * q + 2] = x[4 * c + q].z; v[4 * q + 3] = x[4 * c + q].w;
+      v[4 * q] = x[c][q].x; v[4 * q + 1] = x[c][q].y;
+      v[4 * q + 2] = x[c][q].z; v[4 * q + 3] = x[c][q].w;
     }
     tmem_st16(tq + wg * (HALF / 4) + c * 16, v);
   }
@@ -678,22 +710,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
   using Walk = typename SchedOf<TREE>::Walk;
   Walk sw;
   if constexpr (TREE) {
-    // the plan's arrays lie where the K/V ring will be and its scratch where Q's RoPE part will
-    // (no peer writes into either); the list of rounds stays
-    TreePlan& pl = *reinterpret_cast<TreePlan*>(sm + OFF_KV);
-    TreeScratch& x = *reinterpret_cast<TreeScratch*>(sm + OFF_QR);
-    int2* list = reinterpret_cast<int2*>(sm + LY::OFF_ROUNDS);
+    // the arrays of a plan with rounds lie where the K/V ring will be and its scratch where Q's
+    // RoPE part will (no peer writes into either); the list of rounds stays
     static_assert(sizeof(TreePlan) <= LY::NST * LY::LATB && sizeof(TreeScratch) <= LY::QRB,
                   "the plan fits the K/V ring, its scratch Q's RoPE part");
-    int64_t p0, p1;
     const int c = (int)(blockIdx.x >> 1);
-    const int R = tree_plan<LY::NT>(a, sc, pl, x, list, (int)(gridDim.x >> 1), c, p0, p1);
-    __syncthreads();                // the list is complete
-    sw.begin(a, pl, list, R, p0, p1, c);
+    tree_plan<LY::NT>(a, sc, *reinterpret_cast<TreePlan*>(sm + OFF_KV),
+                      *reinterpret_cast<TreeScratch*>(sm + OFF_QR),
+                      reinterpret_cast<int2*>(sm + LY::OFF_ROUNDS), (int)(gridDim.x >> 1), c, sw);
     if (tid == 0 && rank == 0 && a.cuts)
       a.cuts[c] = make_int4(sw.tail_b, sw.tail_tb, sw.tail_jb, c);
-    fence_proxy_async_smem();      // the arrays are read before TMA writes over them
-    __syncthreads();
   } else {
     sw.begin(sc, a, blockIdx.x >> 1);
   }
@@ -1338,6 +1364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       const float inv = any ? 1.f / lt : 0.f;
       const float lse_v = any ? (mf + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
       const bool part = sw.partial();
+      const unsigned live_rows = __ballot_sync(FULL, row_valid) >> (t & 28);
       if (wg == 0 && row_valid) {
         if (part)
           a.ws_lse[((int64_t)sw.slot * 2 + rank) * TM + t] = lse_v;
@@ -1354,31 +1381,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = 0u;
         }
-        if (!row_valid) continue;
-        if (part) {
-          // the normalised partial, rounded to bf16 like a final output (the merge adds the
-          // pieces of a row in fp32)
-          uint4* dst = reinterpret_cast<uint4*>(a.ws_o + ((int64_t)sw.slot * TM + t) * G.Dc +
-                                                rank * HALF + c);
+        // the normalised rows in bf16: a final output, or a partial that the merge adds in fp32
+        uint4 w[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(
-                pack_bf16(__uint_as_float(v[8 * q + 0]) * inv, __uint_as_float(v[8 * q + 1]) * inv),
-                pack_bf16(__uint_as_float(v[8 * q + 2]) * inv, __uint_as_float(v[8 * q + 3]) * inv),
-                pack_bf16(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv),
-                pack_bf16(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
-        } else {
-          bf16* dst = a.o_lat + grow * G.Dc + rank * HALF + c;
+        for (int q = 0; q < 4; ++q)
+          w[q] = make_uint4(
+              pack_bf16(__uint_as_float(v[8 * q + 0]) * inv, __uint_as_float(v[8 * q + 1]) * inv),
+              pack_bf16(__uint_as_float(v[8 * q + 2]) * inv, __uint_as_float(v[8 * q + 3]) * inv),
+              pack_bf16(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv),
+              pack_bf16(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
+        quad_transpose(w);
+        const int k = t & 3;
+        bf16* dst = (part ? a.ws_o + ((int64_t)sw.slot * TM + (t - k)) * G.Dc
+                          : a.o_lat + (grow - k) * G.Dc) + rank * HALF + c + 8 * k;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4 w;
-            w.x = pack_bf16(__uint_as_float(v[8 * q + 0]) * inv, __uint_as_float(v[8 * q + 1]) * inv);
-            w.y = pack_bf16(__uint_as_float(v[8 * q + 2]) * inv, __uint_as_float(v[8 * q + 3]) * inv);
-            w.z = pack_bf16(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv);
-            w.w = pack_bf16(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv);
-            reinterpret_cast<uint4*>(dst)[q] = w;
-          }
-        }
+        for (int j = 0; j < 4; ++j)
+          if (live_rows >> j & 1) *reinterpret_cast<uint4*>(dst + j * G.Dc) = w[j];
       }
       tc_fence_before();
       mbar_arrive(&bar[B_OFREE]);
@@ -1724,8 +1742,10 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
   return cudaSuccess;
 }
 
-bool tc_attend_tree_supported(const Geo& g) {
-  return tc_attend_supported(g) && g.B <= TREE_MAXB;
+bool tc_attend_tree_supported(const Geo& g, int64_t n_nodes) {
+  // the line of key blocks (at most one block more per run of slots) is counted in 31 bits
+  const int64_t tiles = (n_nodes * g.H + TM - 1) / TM, blocks = g.S / Lay<0>::BNK + 3;
+  return tc_attend_supported(g) && (double)g.B * tiles * blocks < 2147483648.0;
 }
 
 size_t tc_attend_tree_workspace(const Geo& g) {
@@ -1756,13 +1776,13 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   a.window = window;
   a.tree = tree;
   a.err = err;
-  TreeSched sc{workspace && workspace_bytes >= tc_attend_tree_workspace(g) ? 1 : 0, INT64_MAX};
+  TreeSched sc{workspace && workspace_bytes >= tc_attend_tree_workspace(g) ? 1 : 0, UINT32_MAX};
   {
     // keys beyond a third of L2 are read again from HBM by every tile that comes to them later
     int dev = 0, l2 = 0;
     if (cudaGetDevice(&dev) == cudaSuccess &&
         cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) == cudaSuccess && l2 > 0)
-      sc.l2_blocks = l2 / 3 / ((int64_t)a.bn * g.row * 2);
+      sc.l2_blocks = (uint32_t)(l2 / 3 / ((int64_t)a.bn * g.row * 2));
   }
   if (sc.split) {
     a.ws_o = (bf16*)workspace;

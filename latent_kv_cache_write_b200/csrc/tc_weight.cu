@@ -43,7 +43,6 @@ enum { RES_K = 0, RES_Q = 1, STREAM = 2 };
 constexpr int WT = 320;                        // threads
 constexpr int KEYS = 128;                      // keys per CTA
 constexpr int KBOX = KEYS * 64 * 2;            // box of keys: 128 rows x 64 dims
-constexpr int WMAXB = 6144;                    // sequences the plan's array holds
 constexpr int MAXCP = 4;                       // pairs per cluster
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -69,12 +68,11 @@ struct WLay {
   static constexpr int B_AF = B_RE + NRES;                 // accumulator complete      [2]
   static constexpr int B_AE = B_AF + 2;                    // accumulator read, 8 warps [2]
   static constexpr int NBAR = B_AE + 2;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // TMEM slot, abort flag, plan's sums
-  static constexpr int SMEM = OFF_MISC + 16 + 16 * 8 + 1024;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // TMEM slot, abort flag
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "dynamic shared memory of one CTA");
   static_assert(OFF_ST % 1024 == 0 && OFF_ROW % 1024 == 0 && RBOX % 1024 == 0 && SBOX % 1024 == 0,
                 "swizzled boxes start on their alignment");
-  static_assert(WMAXB * 8 <= OFF_ROW, "the plan's array fits where the operands will be");
 };
 
 struct WeightArgs {
@@ -94,7 +92,6 @@ struct Groups {
 };
 __device__ __forceinline__ Groups row_groups(const WeightArgs& p, int64_t b, int64_t rows, int nt) {
   Groups r;
-  const int64_t H = p.a.g.H;
   r.masked = p.qw != nullptr && rows <= 64 * 128;
   r.set = 0;
   if (!r.masked) {
@@ -102,20 +99,18 @@ __device__ __forceinline__ Groups row_groups(const WeightArgs& p, int64_t b, int
     return r;
   }
   const float* qw = p.qw + b * p.a.n_q;
-  const int nodes = (int)((uint32_t)rows / (uint32_t)H);
+  const uint32_t H = (uint32_t)p.a.g.H, nodes = (uint32_t)rows / H;
 #pragma unroll 4
-  for (int i = 0; i < nodes; ++i)
-    if (qw[i] != 0.f) {                        // node i's rows lie in groups g0 .. g1
-      const int g0 = (int)((int64_t)i * H >> 7), g1 = (int)(((int64_t)(i + 1) * H - 1) >> 7);
-      r.set |= (g1 >= 63 ? ~0ull : (1ull << (g1 + 1)) - 1ull) & ~((1ull << g0) - 1ull);
-    }
+  for (uint32_t i = 0; i < nodes; ++i)
+    if (qw[i] != 0.f)                          // node i's rows lie in groups i H / 128 .. ((i + 1) H - 1) / 128
+      r.set |= ((2ull << (((i + 1) * H - 1) >> 7)) - 1ull) & ~((1ull << (i * H >> 7)) - 1ull);
   r.tiles = (__popcll(r.set) + nt / 128 - 1) / (nt / 128);
   return r;
 }
 
 // The pieces of units (256 keys of a sequence) one pair walks, in order: tiles [qb, qe) of each.
 struct UnitWalk {
-  int64_t pos, end;                            // position in the line of tiles, and its end
+  uint32_t pos, end;                           // position in the line of tiles, and its end
   int b, u, units, qb, qe, nt;
   TreeGeo s;
   Groups g;
@@ -123,7 +118,7 @@ struct UnitWalk {
 
   __device__ void sequence(const WeightArgs& p, int seq) {
     b = seq;
-    s = tree_geo(p.a, b);
+    s = tree_geo<KEYS>(p.a, b);
     rows = (int64_t)(s.blk.L - s.ctx) * p.a.g.H;
     units = (s.blk.nblk + 1) / 2;
     g = row_groups(p, b, rows, nt);
@@ -131,20 +126,14 @@ struct UnitWalk {
   }
   __device__ void piece(int from) {
     qb = from;
-    qe = (int64_t)(g.tiles - from) < end - pos ? g.tiles : from + (int)(end - pos);
+    qe = (uint32_t)(g.tiles - from) < end - pos ? g.tiles : from + (int)(end - pos);
   }
-  // at position `at` < end of the line; pre: where each sequence ends in it
-  __device__ void begin(const WeightArgs& p, const int64_t* pre, int64_t at) {
-    int lo = 0, hi = p.a.g.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] > at) hi = mid; else lo = mid + 1;
-    }
-    sequence(p, lo);
-    const int64_t rem = at - (lo ? pre[lo - 1] : 0);
+  // from position `at`, offset `off` of sequence seq's
+  __device__ void begin(const WeightArgs& p, int seq, uint32_t at, uint32_t off) {
+    sequence(p, seq);
     pos = at;
-    u = (int)div_nn(rem, g.tiles);
-    piece((int)(rem - (int64_t)u * g.tiles));
+    u = (int)(off / (uint32_t)g.tiles);
+    piece((int)(off - (uint32_t)(u * g.tiles)));
   }
   __device__ bool valid() const { return pos < end; }
   __device__ void next(const WeightArgs& p) {
@@ -191,56 +180,55 @@ struct GroupCursor {
   }
 };
 
+// Part k of CP of the positions [s0, s1).
+__device__ __forceinline__ uint32_t line_part(uint32_t s0, uint32_t s1, int k, int CP) {
+  const uint32_t n = s1 - s0, each = n / (uint32_t)CP, odd = n - each * (uint32_t)CP;
+  return s0 + each * (uint32_t)k + odd * (uint32_t)k / (uint32_t)CP;
+}
+
 // The tiles of all units, sequence after sequence, make one line of W positions.  Cluster c of C
 // takes the units that start in its equal share of it, [s0, s1); pair k of CP an equal part of
-// those positions.
+// those positions.  Warp-collective.
 template <int NT>
-__device__ __forceinline__ void plan_units(const WeightArgs& p, int64_t* pre, int64_t* sums, int C,
-                                           int c, UnitWalk& w, int64_t& s0, int64_t& s1) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = p.a.g.B;
-  const int per = (B + WT - 1) / WT;
+__device__ __forceinline__ void plan_units(const WeightArgs& p, uint32_t C, uint32_t c, int k,
+                                           int CP, UnitWalk& w, uint32_t& s0, uint32_t& s1) {
+  const int lane = threadIdx.x & 31, B = p.a.g.B;
   w.nt = NT;
   w.pos = w.end = 0;
-  int64_t n = 0;
-  for (int b = t * per; b < (t + 1) * per && b < B; ++b) {
-    w.sequence(p, b);
-    n += (int64_t)w.units * w.g.tiles;
-    pre[b] = n;
-  }
-  int64_t x = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(FULL, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int64_t before = x - n, W = 0;
-  const int warps = (B + 32 * per - 1) / (32 * per);
-  for (int k = 0; k < warps; ++k) {
-    if (k == warp) before += W;
-    W += sums[k];
-  }
-  for (int b = t * per; b < (t + 1) * per && b < B; ++b) pre[b] += before;
-  __syncthreads();
-  const int64_t each = div_nn(W, C);
-  const int odd = (int)(W - each * C);
-  // the first unit that starts at or past cluster k's share of the line
-  auto start = [&](int k) {
-    const int64_t at = each * k + (int)((uint32_t)(odd * k) / (uint32_t)C);
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] > at) hi = mid; else lo = mid + 1;
-    }
-    if (at >= pre[lo]) return at;              // the line's end
-    const int64_t s = lo ? pre[lo - 1] : 0;
-    const TreeGeo g = tree_geo(p.a, lo);
-    const int64_t tiles = div_nn(pre[lo] - s, (g.blk.nblk + 1) / 2);
-    return s + div_nn(at - s + tiles - 1, tiles) * tiles;
+  auto span = [&](int b) {                     // tiles per unit, units
+    const TreeGeo s = tree_geo<KEYS>(p.a, b);
+    const int64_t rows = (int64_t)(s.blk.L - s.ctx) * p.a.g.H;
+    return Span{(uint32_t)row_groups(p, b, rows, NT).tiles, (uint32_t)(s.blk.nblk + 1) / 2};
   };
-  s0 = start(c);
-  s1 = start(c + 1);
+  const Span mine = lane < B ? span(lane) : Span{0, 0};
+  uint32_t W = 0;
+  for (int b = lane; b - lane < B; b += 32) {
+    const Span s = b == lane ? mine : (b < B ? span(b) : Span{0, 0});
+    W += s.tiles * s.blocks;
+  }
+  W = __reduce_add_sync(FULL, W);
+  s0 = s1 = 0;
+  if (W == 0) return;
+  // the shares' ends, moved up to where a unit starts; then where this pair's part lies
+  const uint32_t each = W / C, odd = W - each * C;
+  const uint32_t cut[2] = {each * c + odd * c / C, each * (c + 1) + odd * (c + 1) / C};
+  if (cut[0] >= cut[1]) {                      // (a line shorter than the clusters are many)
+    s0 = s1 = 0;
+    return;
+  }
+  const uint32_t q[2] = {cut[0], cut[1] < W ? cut[1] : W - 1};
+  Spot f[2];
+  line_find(B, span, mine, q, f);
+  auto up = [](const Spot& x) { return (x.off + x.s.tiles - 1) / x.s.tiles * x.s.tiles - x.off; };
+  s0 = cut[0] + up(f[0]);
+  s1 = cut[1] < W ? cut[1] + up(f[1]) : W;
+  const uint32_t p0[1] = {line_part(s0, s1, k, CP)};
+  const uint32_t p1 = line_part(s0, s1, k + 1, CP);
+  if (p0[0] >= p1) return;                     // nothing for this pair
+  Spot g[1];
+  line_find(B, span, mine, p0, g);
+  w.end = p1;
+  w.begin(p, g[0].b, p0[0], g[0].off);
 }
 
 template <int NSL, int MODE>
@@ -282,21 +270,13 @@ __global__ void __launch_bounds__(WT, 1)
   grid_dep_launch();
 
   UnitWalk w;
-  int64_t* pre = reinterpret_cast<int64_t*>(sm);
-  int64_t s0, s1;                              // the cluster's positions
-  plan_units<NT>(p, pre, reinterpret_cast<int64_t*>(sm + LY::OFF_MISC + 16),
-                 (int)gridDim.x / (2 * CP), (int)blockIdx.x / (2 * CP), w, s0, s1);
-  // a pair's part of them starts at part(pair); RES_Q has one tile per unit, and no units to share
-  auto part = [&](int k) { return s0 + div_nn((s1 - s0) * k, CP); };
-  if (part(pair) < part(pair + 1)) {           // (else the walk is empty)
-    w.end = part(pair + 1);
-    w.begin(p, pre, part(pair));
-  }
-  fence_proxy_async_smem();                    // the array is read before TMA writes over it
-  __syncthreads();
+  uint32_t s0, s1;                             // the cluster's positions
+  plan_units<NT>(p, gridDim.x / (2 * CP), blockIdx.x / (2 * CP), pair, CP, w, s0, s1);
+  auto part = [&](int k) { return line_part(s0, s1, k, CP); };
   // (a pair's loads complete on the even CTA's barriers, but go to each CTA's own memory)
   float kept = 0.f, kept_base = 0.f;           // a unit this pair began and others went on with
-  int64_t kept_at = -1, kept_end = 0;
+  int64_t kept_at = -1;
+  uint32_t kept_end = 0;
 
   if (warp == 8) {
     // ---------------------------------------------------------------- TMA producer
@@ -359,9 +339,20 @@ __global__ void __launch_bounds__(WT, 1)
       for (int i = 0; ok && un > 0 && i < NRES; ++i)
         ok = mbar_wait(&bar[LY::B_RE + i], (un - 1) & 1, abort, a.err, 0x38, i);
     }
+  } else if (warp == 9 && rank == 1) {
+    // ---------------------------------------------------------------- pass-through
+    // sequences that add nothing have no tiles: their totals stay, a node's row gets 0
+    for (int b = blockIdx.x >> 1; b < a.g.B; b += gridDim.x >> 1) {
+      const Window v = load_window(a.window, b, a.g.S, a.n_q);
+      if (v.len() == 0 || row_groups(p, b, (int64_t)v.nodes * a.g.H, NT).tiles > 0) continue;
+      for (int j = lane; j < v.len(); j += 32) {
+        const int64_t at = (int64_t)b * a.g.S + v.slot(j, a.g.S);
+        p.out[at] = j < v.rows && p.win ? p.win[at] : 0.f;
+      }
+    }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (lane == 0) {
       const uint32_t id = idesc_bf16(256, NT, false, false);
       const uint16_t both = (uint16_t)(3u << leader);
       uint32_t it = 0, un = 0, tc = 0;
@@ -413,15 +404,6 @@ __global__ void __launch_bounds__(WT, 1)
     float* handed = reinterpret_cast<float*>(sm + LY::OFF_SUM);
     const uint32_t H = (uint32_t)a.g.H;
     uint32_t tc = 0, mine = 0;                 // tiles of the pair, tiles this warpgroup has taken
-    // sequences that add nothing have no tiles: their totals pass through
-    for (int b = blockIdx.x; b < a.g.B; b += gridDim.x) {
-      const Window v = load_window(a.window, b, a.g.S, a.n_q);
-      if (v.len() == 0 || row_groups(p, b, (int64_t)v.nodes * H, NT).tiles > 0) continue;
-      for (int j = tid; j < v.len(); j += 256) {
-        const int64_t at = (int64_t)b * a.g.S + v.slot(j, a.g.S);
-        p.out[at] = j < v.rows && p.win ? p.win[at] : 0.f;
-      }
-    }
     // After an expired wait the warps still walk to the end (each further wait gives up at once):
     // the warpgroups meet at named barriers.
     bool ok = true;
@@ -605,8 +587,11 @@ cudaError_t launch_weight(const CUtensorMap& K, const CUtensorMap& Q, const Weig
 
 }  // namespace
 
-bool tc_attend_weight_supported(const Geo& g) {
-  return g.Dc == 512 && (g.Dr == 64 || g.Dr == 512) && g.B <= WMAXB;
+bool tc_attend_weight_supported(const Geo& g, int64_t n_nodes) {
+  // the line of tiles (of at least 128 rows, 256 keys) is counted in 31 bits
+  const int64_t tiles = (n_nodes * g.H + 127) / 128, units = g.S / 256 + 3;
+  return g.Dc == 512 && (g.Dr == 64 || g.Dr == 512) &&
+         (double)g.B * tiles * units < 2147483648.0;
 }
 
 cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,

@@ -152,6 +152,23 @@ def test_attend_clips_windows(cuda_ok, cfg):
     check_attend(wl, q.values, c.values, windows, see, n, o, lse)
 
 
+@pytest.mark.parametrize("cfg", ["MAIN", "WIDE"])
+def test_attend_repeats(cuda_ok, cfg):
+    """The same call gives the same bits every time, with scores that take the exact exchange (its
+    buffers are handed between the two SMs three times per block)."""
+    n, S, windows = 9, 90, [(0, 70, 9), (80, 64, 9), (5, 20, 3)]
+    wl = T.workload(getattr(T, cfg), 3, S)
+    rng = np.random.default_rng(5)
+    q = T.normal(rng, (3, n, 8, wl.row_width), "bf16", 2.0)
+    c = T.normal(rng, (3, S, wl.row_width), "bf16")
+    qd, cd = P.upload(q), P.upload(c)
+    o, lse = attend(wl, qd, cd, windows, None, n)
+    check_attend(wl, q.values, c.values, windows, None, n, o, lse)
+    for _ in range(200):
+        o2, lse2 = attend(wl, qd, cd, windows, None, n)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("cfg,nodes", [("HEADS", (9, 3, 8, 1, 9, 5, 0, 7)),
                                        ("HEADS", (64, 60, 64, 33, 64, 1, 64, 64)),
                                        ("WIDE", (40, 64, 33, 64, 50, 3, 64, 64))])
