@@ -170,40 +170,54 @@ __device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws
 __global__ void __launch_bounds__(256)
     combine_tree_kernel(const __grid_constant__ AttnArgs a, int clusters) {
   __shared__ float red[8 * 32 * 17];
-  __shared__ int4 cut[MAXC];
+  __shared__ int4 cut[MAXC + 1];
   __shared__ int first[MAXC], pieces[MAXC];
   __shared__ int n_sh, most_sh;
+  const int t = threadIdx.x;
   tc::grid_dep_wait();                             // the attention's partials are visible
   tc::grid_dep_launch();
-  if (threadIdx.x < 32) {
-    int n = 0, most = 0, ranges = 0;
-    for (int i0 = 0; i0 < clusters; i0 += 32) {
-      const int4 c = i0 + (int)threadIdx.x < clusters ? a.cuts[i0 + threadIdx.x] : make_int4(-1, 0, 0, 0);
-      const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
-      if (c.x >= 0) cut[ranges + __popc(m & ((1u << threadIdx.x) - 1u))] = c;
-      ranges += __popc(m);
-    }
-    __syncwarp();
-    for (int i0 = 0; i0 < ranges; i0 += 32) {
-      const int i = i0 + threadIdx.x;
-      // a cut inside a tile has a block > 0; the tile's first one stands for it
-      bool is = i > 0 && i < ranges && cut[i].z > 0;
-      if (is) is = !(cut[i - 1].z > 0 && cut[i - 1].x == cut[i].x && cut[i - 1].y == cut[i].y);
-      const unsigned m = __ballot_sync(0xffffffffu, is);
-      if (is) {
-        int k = i + 1;
-        while (k < ranges && cut[k].z > 0 && cut[k].x == cut[i].x && cut[k].y == cut[i].y) ++k;
-        const int e = n + __popc(m & ((1u << threadIdx.x) - 1u));
-        first[e] = i;
-        pieces[e] = k - i + 1;
-        most = max(most, k - i + 1);
+  if (t < 32) {
+    // the cuts of the clusters that have a range, four per lane
+    int4 c[MAXC / 32];
+#pragma unroll
+    for (int q = 0; q < MAXC / 32; ++q)
+      c[q] = 32 * q + t < clusters ? a.cuts[32 * q + t] : make_int4(-1, 0, 0, 0);
+    unsigned split = 0;
+#pragma unroll
+    for (int q = 0; q < MAXC / 32; ++q) split |= (unsigned)(c[q].x >= 0 && c[q].z > 0);
+    if (t == 0) n_sh = most_sh = 0;
+    if (__any_sync(0xffffffffu, split)) {
+      int ranges = 0;
+#pragma unroll
+      for (int q = 0; q < MAXC / 32; ++q) {
+        const unsigned m = __ballot_sync(0xffffffffu, c[q].x >= 0);
+        if (c[q].x >= 0) cut[ranges + __popc(m & ((1u << t) - 1u))] = c[q];
+        ranges += __popc(m);
       }
-      n += __popc(m);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (threadIdx.x == 0) {
-      n_sh = n;
-      most_sh = most;
+      if (t == 0) cut[ranges] = make_int4(-1, 0, 0, 0);
+      __syncwarp();
+      int n = 0, most = 0;
+      for (int i0 = 0; i0 < ranges; i0 += 32) {
+        const int i = i0 + t;
+        // a cut inside a tile has a block > 0; the tile's first one stands for it
+        bool is = i > 0 && i < ranges && cut[i].z > 0;
+        if (is) is = !(cut[i - 1].z > 0 && cut[i - 1].x == cut[i].x && cut[i - 1].y == cut[i].y);
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        if (is) {
+          int k = i + 1;
+          while (cut[k].z > 0 && cut[k].x == cut[i].x && cut[k].y == cut[i].y) ++k;
+          const int e = n + __popc(m & ((1u << t) - 1u));
+          first[e] = i;
+          pieces[e] = k - i + 1;
+          most = max(most, k - i + 1);
+        }
+        n += __popc(m);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (t == 0) {
+        n_sh = n;
+        most_sh = most;
+      }
     }
   }
   __syncthreads();
@@ -230,7 +244,8 @@ cudaError_t launch_combine(const AttnArgs& a, const CombineList& cl, cudaStream_
 }
 
 cudaError_t launch_combine_tree(const AttnArgs& a, int clusters, cudaStream_t st) {
-  return launch_dependent(combine_tree_kernel, 148u * 4u, 256, 0, st, 1u, a, clusters);
+  // two blocks per SM: enough loads in flight, and few blocks to start when nothing was split
+  return launch_dependent(combine_tree_kernel, 148u * 2u, 256, 0, st, 1u, a, clusters);
 }
 
 }  // namespace attn

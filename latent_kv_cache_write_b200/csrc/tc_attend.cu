@@ -47,6 +47,8 @@
 
 #include <cuda_fp16.h>
 
+#include <math.h>
+
 #include <mutex>
 #include <vector>
 
@@ -1040,9 +1042,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       const int64_t r_in_b = tg.row0 + t;
       const bool row_valid = r_in_b < tg.rows_b;
       const int64_t grow = tg.grow0 + t;
-      int64_t k_end_row = 0, node = 0;
+      int64_t k_end_row = 0;
+      int node = 0;
       if constexpr (TREE)
-        node = row_valid ? r_in_b / G.H : 0;
+        node = row_valid ? (int)((uint32_t)r_in_b / (uint32_t)G.H) : 0;
       else
         k_end_row = key_end(G, a.q_first, a.k_first + a.n_keys, row_valid ? r_in_b / G.H : tg.i_last);
       const int n = sw.nb();
@@ -1133,22 +1136,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           }
         }
 
-        // a block with draft nodes: which of its keys this row sees, and finite node rows
+        // a block with draft nodes: finite node rows
         int nctx = BN;                                 // context keys of the block
-        uint64_t sees = ~0ull;
         if constexpr (TREE) {
-          const int64_t c64 = (int64_t)sw.ctx - g0;
-          nctx = c64 >= valid ? valid : (c64 < 0 ? 0 : (int)c64);
-          if (nctx < BN) {
-            sees = tree_bits(a, tg.b, node, nctx, c64 < 0 ? -c64 : 0, valid);
-            if (t < valid && t >= nctx) {
-              uint8_t* st = sm + OFF_KV + ((sw.gbase + jl) % NST) * BOX_BYTES + t * 128;
+          nctx = max(min(sw.ctx - (int)g0, valid), 0);
+          if (nctx < BN && t < valid && t >= nctx) {
+            uint8_t* st = sm + OFF_KV + ((sw.gbase + jl) % NST) * BOX_BYTES + t * 128;
 #pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
-                uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
+            for (int q = 0; q < 4; ++q) {
+              uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
 #pragma unroll
-                for (int w = 0; w < 8; ++w) p[w] = finite8(p[w]);
-              }
+              for (int w = 0; w < 8; ++w) p[w] = finite8(p[w]);
             }
           }
         }
@@ -1242,6 +1240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         // masked raw maximum (scores are scaled inside the exponent)
         if constexpr (TREE) {
           if (nctx < BN) {
+            const uint64_t sees = tree_bits(a, tg.b, node, nctx, max((int)g0 - sw.ctx, 0), valid);
 #pragma unroll
             for (int c = 0; c < BN; ++c) s[c] = (sees >> c & 1) ? s[c] : -INFINITY;
           }
@@ -1767,7 +1766,9 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   a.g = g;
   a.n_q = n_nodes;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.xthr = exchange_threshold(a.scale_log2);
+  // fp16's error is the same in a whole binade, so the threshold may go up to the next power of two
+  // under the same bound (2^-8 log2 units): fewer rows take the exact exchange
+  a.xthr = fminf(exp2f(ceilf(log2f(exchange_threshold(a.scale_log2)))), 32768.f);
   a.q_abs = (const bf16*)q_abs;
   a.o_lat = (bf16*)o_lat;
   a.lse = lse;
@@ -1776,7 +1777,11 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   a.window = window;
   a.tree = tree;
   a.err = err;
-  TreeSched sc{workspace && workspace_bytes >= tc_attend_tree_workspace(g) ? 1 : 0, UINT32_MAX};
+  // A tile is only split when that saves more than a segment and the merge cost, so rings whose
+  // longest tile is shorter never need the merge launch.
+  const bool split = workspace && workspace_bytes >= tc_attend_tree_workspace(g) &&
+                     g.S / a.bn + 2 > SEG_COST + COMBINE_COST;
+  TreeSched sc{split ? 1 : 0, UINT32_MAX};
   {
     // keys beyond a third of L2 are read again from HBM by every tile that comes to them later
     int dev = 0, l2 = 0;
