@@ -37,6 +37,7 @@ struct AttnArgs {
   const uint8_t* tree;      // [B][n_q][n_q] bytes, or null (a chain)
   int4* cuts;               // where each cluster's range starts: (sequence or -1: none, tile,
                             // block, cluster), [MAXC]
+  uint32_t zero;            // 0, which the compiler does not know
   unsigned int* err;
 };
 
@@ -100,10 +101,33 @@ __host__ __device__ inline TileGeo tile_geo(const Geo& G, int64_t n_q, int64_t q
 
 // Draft trees: a sequence's tiles of 128 (node, head) rows, and the key blocks (context, then
 // nodes) that each of them walks.
+struct TreeBlocks {          // as Blocks, from logical row 0, in 32 bits (registers are short)
+  int32_t p1, n1, L;
+  int nb1, nblk;
+  template <int BN>
+  __device__ void get(int j, int& slot0, int& g0, int& valid) const {
+    const bool second = j >= nb1;
+    const int r = (second ? j - nb1 : j) * BN;
+    const int v = (second ? L - n1 : n1) - r;
+    slot0 = second ? r : p1 + r;
+    g0 = second ? n1 + r : r;
+    valid = v < BN ? v : BN;
+  }
+  __device__ void get(int j, int64_t& slot0, int64_t& g0, int& valid) const {
+    int s, g;
+    get<64>(j, s, g, valid);
+    slot0 = s;
+    g0 = g;
+  }
+};
 struct TreeGeo {
   int32_t ctx;              // context rows
   int tiles;
-  Blocks blk;
+  TreeBlocks blk;
+};
+struct TreeTile {            // as TileGeo
+  int b, rows_b, row0, grow0;
+  TreeBlocks blk;
 };
 
 // BN keys per block (a power of two).  Everything fits 32 bits: rows and slots are below 2^31.
@@ -114,11 +138,9 @@ __device__ __forceinline__ TreeGeo tree_geo(const AttnArgs& a, const Window& w) 
   t.tiles = (int)(((uint32_t)w.nodes * (uint32_t)a.g.H + (TM - 1)) / TM);
   const uint32_t L = (uint32_t)w.len(), run = (uint32_t)a.g.S - (uint32_t)w.first;
   const uint32_t n1 = L < run ? L : run;
-  t.blk.k_first = 0;                       // global tokens become logical rows
   t.blk.p1 = w.first;
-  t.blk.L = L;
-  t.blk.n1 = n1;
-  t.blk.bn = BN;
+  t.blk.L = (int32_t)L;
+  t.blk.n1 = (int32_t)n1;
   t.blk.nb1 = (int)((n1 + (BN - 1)) / BN);
   t.blk.nblk = t.blk.nb1 + (int)((L - n1 + (BN - 1)) / BN);
   return t;

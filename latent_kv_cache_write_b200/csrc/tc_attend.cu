@@ -47,8 +47,6 @@
 
 #include <cuda_fp16.h>
 
-#include <math.h>
-
 #include <mutex>
 #include <vector>
 
@@ -58,7 +56,7 @@ namespace {
 using namespace tc;
 using namespace attn;
 
-// Three variants of one kernel, chosen per call by the host; all take 64-key blocks.
+// Five variants of one kernel, chosen per call by the host; all take 64-key blocks.
 //   V = 0: d_R = 64: 4 K/V stages, separate exchange and P buffers; a warpgroup hands its
 //          exchange buffer back to the peer as soon as it has read it.
 //   V = 1: d_R = 512 (the wide positional key): each CTA's 256 RoPE dims as four 64-dim
@@ -72,6 +70,13 @@ using namespace attn;
 //          not loaded but written.  TMA brings each block's packed codes and scales into a
 //          3-slot staging ring, and two warps (one key row per lane; 384 threads) write the
 //          dequantised bf16 rows into the stage in the layout the TMA loads would have.
+//   V = 3, 4: draft trees (mla_attend_tree) with d_R = 64, 512: as V = 0 and 1, but the walk over
+//          ragged windows is planned on the device, rows are masked by the tree in the blocks that
+//          hold nodes, and partial scores are exchanged in float32: the log-sum-exp, which other
+//          calls go by, is then one of the scores as they are (with fp16 partials it is some 1e-4
+//          off).  V = 3 sends a block at once, keys 32-63 into the peer's P buffer, which is free
+//          once its PV has read the P of its previous block (the PV's commit says so); V = 4 sends
+//          both halves through the merged buffer.  A warp hands a buffer back for itself.
 // K/V ring, box-major: latent box q (dims 64q..64q+63 of this CTA's half, 128-byte
 // swizzle) of stage s at OFF_KV + (q * NST + s) * BOXB; RoPE box q of RoPE slot r at
 // OFF_KVR + (q * NSTR + r) * RBB (NSTR = NST and r = s except for V = 1).
@@ -79,8 +84,9 @@ using namespace attn;
 // segment; a waiter counts the uses and waits on the parity of the count.
 template <int V>
 struct Lay {
-  static constexpr bool WIDE = V == 1;
+  static constexpr bool WIDE = V == 1 || V == 4;
   static constexpr bool PACKED = V == 2;
+  static constexpr bool TREE = V >= 3;
   static constexpr int NT = PACKED ? 384 : 352;              // threads
   static constexpr int NST = WIDE ? 3 : (PACKED ? 3 : 4);     // latent stages
   static constexpr int NSTR = WIDE ? 1 : NST;                  // RoPE slots
@@ -129,11 +135,13 @@ struct Lay {
   static constexpr int B_KRF = B_KRE + NSTR;    // RoPE slot loaded (wide; TMA)           [NSTR]
   static constexpr int B_SGF = B_KRF + NSTR;   // staging slot loaded (TMA)           [NSG]
   static constexpr int B_SGE = B_SGF + NSG;    // staging slot read (64)               [NSG]
-  static constexpr int NBAR = B_SGE + NSG;
+  static constexpr int B_XP = B_SGE + NSG;      // V = 3, 4: P buffer in the peer free  [2]
+  static constexpr int NBAR = B_XP + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   // draft trees: (sequence, tile) of each round, behind the TMEM slot, abort flag, votes [2][4]
   static constexpr int OFF_ROUNDS = OFF_MISC + 48;
-  static constexpr int SMEM = OFF_ROUNDS + 32 * 8 + 1024;
+  static constexpr int OFF_WALK = OFF_ROUNDS + (TREE ? 32 * 8 : 0);    // softmax walk [3]
+  static constexpr int SMEM = OFF_WALK + (TREE ? 3 * 112 : 0) + 1024;
   static_assert(SMEM <= 227 * 1024, "dynamic shared memory of one CTA");
   static_assert(OFF_SG % 1024 == 0 && OFF_SGR % 128 == 0 && OFF_SGS % 128 == 0 &&
                 OFF_QR % 1024 == 0 && OFF_X % 1024 == 0 && OFF_P % 1024 == 0,
@@ -248,7 +256,7 @@ struct TreeWalk {
   int tb, tiles, jb, je;    // tile of the sequence, its tiles, this segment's blocks
   int ctx;                  // context rows of the sequence
   int k, gbase, nbase[2], slot;
-  TileGeo tg;
+  TreeTile tg;
 
   // the tail: n blocks from block `off` of sequence b's tiles on
   __device__ void begin(const AttnArgs& a, const int2* list, int n_rounds, int b, uint32_t off,
@@ -276,11 +284,11 @@ struct TreeWalk {
     ctx = s.ctx;
     tg.blk = s.blk;
     tg.b = b;
-    tg.rows_b = (int64_t)(s.blk.L - s.ctx) * a.g.H;
+    tg.rows_b = (s.blk.L - s.ctx) * a.g.H;
   }
   __device__ void tile(const AttnArgs& a, int from, int most) {
-    tg.row0 = (int64_t)tb * TM;
-    tg.grow0 = (int64_t)tg.b * a.n_q * a.g.H + tg.row0;
+    tg.row0 = tb * TM;
+    tg.grow0 = tg.b * (int)a.n_q * a.g.H + tg.row0;
     jb = from;
     je = tg.blk.nblk - from < most ? tg.blk.nblk : from + most;
   }
@@ -503,6 +511,33 @@ __device__ __forceinline__ void sub_f16x8(const uint4& x, float* s) {
   }
 }
 
+// Draft trees: 32 of this thread's partial scores to the peer, float32, chunk-major, once `credit`
+// says that the buffer is free; and the peer's added to them (returns an OR of a word of every
+// vector that was loaded).
+__device__ __forceinline__ bool send_scores(const float* s, uint64_t* credit, uint32_t parity,
+                                            uint32_t dst, uint32_t full, volatile int* abort,
+                                            unsigned int* err, uint32_t tag) {
+  if (!__all_sync(FULL, mbar_wait_cluster(credit, parity, abort, err, 0x202, tag))) return false;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    st_async_v4(dst + q * (TM * 16), __float_as_uint(s[4 * q]), __float_as_uint(s[4 * q + 1]),
+                __float_as_uint(s[4 * q + 2]), __float_as_uint(s[4 * q + 3]), full);
+  return true;
+}
+__device__ __forceinline__ uint32_t add_scores(float* s, const uint4* buf) {
+  uint32_t seen = 0u;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint4 x = buf[q * TM];
+    seen |= x.x;
+    s[4 * q] += __uint_as_float(x.x);
+    s[4 * q + 1] += __uint_as_float(x.y);
+    s[4 * q + 2] += __uint_as_float(x.z);
+    s[4 * q + 3] += __uint_as_float(x.w);
+  }
+  return seen;
+}
+
 // This thread's row of a 64-column S buffer (fp32 partial scores) -> s.
 __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64]) {
   uint32_t v[2][32];
@@ -634,18 +669,14 @@ __device__ __forceinline__ uint4 finite8(uint4 v) {
   return make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
 }
 
-// TREE: the draft-tree form of a variant (mla_attend_tree).  The walk over ragged windows is
-// planned on the device, rows are masked by the tree in the blocks that hold nodes, and the node
-// rows of such a block are made finite before the PV product: a hidden row's weight is 0, but
-// 0 * NaN would still reach every row of the tile.  (A node that does see a NaN row gets it
-// through its scores.)
-template <int V, bool TREE>
+template <int V>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmKR,
                   const __grid_constant__ CUtensorMap tmQR, const __grid_constant__ CUtensorMap tmSC,
                   const __grid_constant__ CUtensorMap tmSR, const __grid_constant__ AttnArgs a,
-                  const __grid_constant__ typename SchedOf<TREE>::S sc) {
+                  const __grid_constant__ typename SchedOf<Lay<V>::TREE>::S sc) {
   using LY = Lay<V>;
+  constexpr bool TREE = LY::TREE;
   constexpr int NST = LY::NST, NSTR = LY::NSTR;
   constexpr int BN = LY::BNK, BOX_BYTES = LY::BOXB, RBOX_BYTES = LY::RBB;
   constexpr int STAGE_BYTES = LY::STAGEB, QR_BYTES = LY::QRB, XP_BYTES = LY::XPB;
@@ -689,7 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       mbar_init(&bar[B_SF + q], 1);
       mbar_init(&bar[B_SE + q], 128);
       mbar_init(&bar[B_XF + q], 1);
-      mbar_init(&bar[B_XE + q], 1);
+      mbar_init(&bar[B_XE + q], TREE ? 4 : 1);     // TREE: a warp each
+      mbar_init(&bar[LY::B_XP + q], 1);
       mbar_init(&bar[B_PF + q], 128);
       mbar_init(&bar[B_PE + q], 1);
       mbar_init(&bar[B_M + q], 128);
@@ -1009,7 +1041,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           }
           mma_commit(&bar[B_PE + pb]);
           mma_commit(&bar[B_KVE + s]);
-          if constexpr (LY::MERGED) mma_commit_cluster(&bar[B_XE + pb], (uint16_t)(1u << peer));
+          if constexpr (LY::MERGED || TREE)
+            mma_commit_cluster(&bar[(TREE ? LY::B_XP : B_XE) + pb], (uint16_t)(1u << peer));
         }
         if (ok) mma_commit(&bar[B_SEGDONE]);
       }
@@ -1024,6 +1057,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     const uint32_t peer_xf = mapa(smem_u32(&bar[B_XF + wg]), peer);
     const uint32_t peer_xe = mapa(smem_u32(&bar[B_XE + wg]), peer);
     const uint4* my_x = reinterpret_cast<const uint4*>(sm + OFF_X + wg * XP_BYTES) + t;
+    const uint32_t peer_p = mapa(smem_u32(sm + OFF_P + wg * XP_BYTES), peer) + (uint32_t)t * 16;
+    const uint4* my_p = reinterpret_cast<const uint4*>(sm + OFF_P + wg * XP_BYTES) + t;
     uint8_t* prow = sm + OFF_P + wg * XP_BYTES + t * (BN * 2);   // P row t
     const float c2 = a.scale_log2;
     bool ok = true;
@@ -1031,44 +1066,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
     uint32_t nd = 0;        // blocks this warpgroup has decided the exchange of
     uint32_t* xvote = reinterpret_cast<uint32_t*>(sm + LY::OFF_MISC + 16);
 
+    // Draft trees: the walk is long and the same for all, so it stays in shared memory (the third
+    // segment from here is worked out before the barrier that ends one), and the threads keep what
+    // their blocks need.
+    TreeWalk* wk = reinterpret_cast<TreeWalk*>(sm + LY::OFF_WALK);
+    static_assert(!TREE || sizeof(TreeWalk) <= 112, "three walks fit");
+    if constexpr (TREE) {
+      if (tid == 0) {
+        wk[0] = sw;
+        wk[1] = sw;
+        if (wk[1].valid()) wk[1].next(a);
+      }
+      named_bar(3, 2 * TM);
+    }
     if (sw.valid()) {
       load_q(a, tmem + lane_base + Q_COL, sw.tg.grow0 + t, sw.tg.row0 + t < sw.tg.rows_b, rank,
              wg);
       tc_fence_before();
       mbar_arrive(&bar[B_QREADY]);
     }
-    for (; sw.valid(); sw.next(a)) {
-      const TileGeo& tg = sw.tg;
-      const int64_t r_in_b = tg.row0 + t;
-      const bool row_valid = r_in_b < tg.rows_b;
-      const int64_t grow = tg.grow0 + t;
+    for (int ks = 0;; ++ks) {
+      // this segment's part of the walk
+      const Walk& cw = TREE ? reinterpret_cast<const Walk&>(wk[ks % 3]) : sw;
+      if (!cw.valid()) break;
+      const auto blk = cw.tg.blk;
+      const int jb = cw.jb, n = cw.nb(), gbase = cw.gbase;
+      const int nb_mine = cw.done_by(wg), nb_other = cw.done_by(wg ^ 1);
+      const int ws_slot = cw.partial() ? cw.slot : -1;
+      const int64_t r_in_b = cw.tg.row0 + t;
+      const bool row_valid = r_in_b < cw.tg.rows_b;
+      const int64_t grow = cw.tg.grow0 + t;
       int64_t k_end_row = 0;
-      int node = 0;
-      if constexpr (TREE)
+      int node = 0, ctx = 0, seq_b = 0;
+      if constexpr (TREE) {
         node = row_valid ? (int)((uint32_t)r_in_b / (uint32_t)G.H) : 0;
-      else
-        k_end_row = key_end(G, a.q_first, a.k_first + a.n_keys, row_valid ? r_in_b / G.H : tg.i_last);
-      const int n = sw.nb();
+        ctx = cw.ctx;
+        seq_b = cw.tg.b;
+      } else {
+        k_end_row =
+            key_end(G, a.q_first, a.k_first + a.n_keys, row_valid ? r_in_b / G.H : cw.tg.i_last);
+      }
       {
         // the next segment's Q rows (this CTA's latent half, this warpgroup's half of it)
         // into L2 now, so that their load into TMEM at the segment's end is short
-        Walk nx = sw;
-        nx.next(a);
-        if (nx.valid() && nx.tg.row0 + t < nx.tg.rows_b) {
-          const char* qrow = reinterpret_cast<const char*>(
-              a.q_abs + (nx.tg.grow0 + t) * G.row + rank * HALF + wg * (HALF / 2));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + 128));
+        auto prefetch_q = [&](const Walk& nx) {
+          if (nx.valid() && nx.tg.row0 + t < nx.tg.rows_b) {
+            const char* qrow = reinterpret_cast<const char*>(
+                a.q_abs + (int64_t)(nx.tg.grow0 + t) * G.row + rank * HALF + wg * (HALF / 2));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + 128));
+          }
+        };
+        if constexpr (TREE) {
+          prefetch_q(wk[(ks + 1) % 3]);
+        } else {
+          Walk nx = sw;
+          nx.next(a);
+          prefetch_q(nx);
         }
       }
       float m_last = -INFINITY, l = 0.f;       // this warpgroup's running sum and its max
       for (int jl = wg; jl < n; jl += 2) {
-        const int j = sw.jb + jl;              // block of the tile
-        const int seq = sw.done_by(wg) + (jl >> 1);
+        const int j = jb + jl;                 // block of the tile
+        const int seq = nb_mine + (jl >> 1);
         const uint32_t kph = seq & 1;
         // arm this block's first exchange round: the peer's asynchronous stores complete
         // XP_BYTES of transactions on it (they may land before or after this arrive)
-        if (t == 0) mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
+        if (t == 0) mbar_expect_tx(&bar[B_XF + wg], TREE && !LY::MERGED ? 2 * XP_BYTES : XP_BYTES);
         if (!__all_sync(FULL, mbar_wait(&bar[B_SF + wg], kph, abort, a.err, 0x201, (t << 16) | j))) {
           ok = false;
           break;
@@ -1079,55 +1143,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         tc_fence_before();
         mbar_arrive(&bar[B_SE + wg]);
 
-        // send this CTA's partial scores into the peer's buffer once the peer is done
-        // with it: it has read what was sent in this warpgroup's previous round (and,
-        // with merged buffers, its PV has read the P held there)
-        if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XE + wg], (xc & 1) ^ 1, abort, a.err,
-                                                 0x202, (t << 16) | j))) {
-          ok = false;
-          break;
-        }
-        // The partials go rounded to fp16 (saturating: within 2^-11 of each partial).  A row
-        // with a partial beyond a.xthr in magnitude sets bit 0 of its last 16-byte chunk (the
-        // lowest mantissa bit of key 56), found while the first seven chunks travel; if any
-        // row of either CTA did, both CTAs' warpgroups exchange exact fp32 partials below.
-        bool need;
-        {
-          uint32_t hs[BN / 2];
-#pragma unroll
-          for (int c = 0; c < BN / 2; ++c) hs[c] = f16x2_satfinite(s[2 * c], s[2 * c + 1]);
-#pragma unroll
-          for (int q = 0; q < BN / 8 - 1; ++q)
-            st_async_v4(peer_x + q * (TM * 16), hs[4 * q], hs[4 * q + 1], hs[4 * q + 2],
-                        hs[4 * q + 3], peer_xf);
-          float hi[4], lo[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            hi[c] = fmax3(s[16 * c], s[16 * c + 1], s[16 * c + 2]);
-            lo[c] = fmin3(s[16 * c], s[16 * c + 1], s[16 * c + 2]);
-#pragma unroll
-            for (int e = 3; e < 15; e += 2) {
-              hi[c] = fmax3(hi[c], s[16 * c + e], s[16 * c + e + 1]);
-              lo[c] = fmin3(lo[c], s[16 * c + e], s[16 * c + e + 1]);
-            }
-            hi[c] = fmaxf(hi[c], s[16 * c + 15]);
-            lo[c] = fminf(lo[c], s[16 * c + 15]);
+        bool need = false;
+        if constexpr (TREE) {
+          // exact float32 partials, the half that needs no P buffer first (with merged buffers the
+          // other half follows when the first has been read)
+          if (!send_scores(s, &bar[LY::MERGED ? LY::B_XP + wg : B_XE + wg], (xc & 1) ^ 1, peer_x,
+                           peer_xf, abort, a.err, (t << 16) | j) ||
+              (!LY::MERGED && !send_scores(s + 32, &bar[LY::B_XP + wg], (xc & 1) ^ 1, peer_p, peer_xf,
+                                           abort, a.err, (t << 16) | j))) {
+            ok = false;
+            break;
           }
-          need = fmaxf(fmax3(hi[0], hi[1], fmaxf(hi[2], hi[3])),
-                       -fmin3(lo[0], lo[1], fminf(lo[2], lo[3]))) > a.xthr;
-          constexpr int QL = BN / 8 - 1;
-          st_async_v4(peer_x + QL * (TM * 16), (hs[4 * QL] & ~1u) | (need ? 1u : 0u),
-                      hs[4 * QL + 1], hs[4 * QL + 2], hs[4 * QL + 3], peer_xf);
+        } else {
+          // send this CTA's partial scores into the peer's buffer once the peer is done
+          // with it: it has read what was sent in this warpgroup's previous round (and,
+          // with merged buffers, its PV has read the P held there)
+          if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XE + wg], (xc & 1) ^ 1, abort, a.err,
+                                                   0x202, (t << 16) | j))) {
+            ok = false;
+            break;
+          }
+          // The partials go rounded to fp16 (saturating: within 2^-11 of each partial).  A row
+          // with a partial beyond a.xthr in magnitude sets bit 0 of its last 16-byte chunk (the
+          // lowest mantissa bit of key 56), found while the first seven chunks travel; if any
+          // row of either CTA did, both CTAs' warpgroups exchange exact fp32 partials below.
+          {
+            uint32_t hs[BN / 2];
+#pragma unroll
+            for (int c = 0; c < BN / 2; ++c) hs[c] = f16x2_satfinite(s[2 * c], s[2 * c + 1]);
+#pragma unroll
+            for (int q = 0; q < BN / 8 - 1; ++q)
+              st_async_v4(peer_x + q * (TM * 16), hs[4 * q], hs[4 * q + 1], hs[4 * q + 2],
+                          hs[4 * q + 3], peer_xf);
+            float hi[4], lo[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              hi[c] = fmax3(s[16 * c], s[16 * c + 1], s[16 * c + 2]);
+              lo[c] = fmin3(s[16 * c], s[16 * c + 1], s[16 * c + 2]);
+#pragma unroll
+              for (int e = 3; e < 15; e += 2) {
+                hi[c] = fmax3(hi[c], s[16 * c + e], s[16 * c + e + 1]);
+                lo[c] = fmin3(lo[c], s[16 * c + e], s[16 * c + e + 1]);
+              }
+              hi[c] = fmaxf(hi[c], s[16 * c + 15]);
+              lo[c] = fminf(lo[c], s[16 * c + 15]);
+            }
+            need = fmaxf(fmax3(hi[0], hi[1], fmaxf(hi[2], hi[3])),
+                         -fmin3(lo[0], lo[1], fminf(lo[2], lo[3]))) > a.xthr;
+            constexpr int QL = BN / 8 - 1;
+            st_async_v4(peer_x + QL * (TM * 16), (hs[4 * QL] & ~1u) | (need ? 1u : 0u),
+                        hs[4 * QL + 1], hs[4 * QL + 2], hs[4 * QL + 3], peer_xf);
+          }
         }
 
         int64_t slot0, g0;
         int valid;
-        tg.blk.get(j, slot0, g0, valid);
+        blk.get(j, slot0, g0, valid);
         if (valid < BN && t < BN && t >= valid) {
           // a partial block: zero this CTA's latent rows past the last key so that masked
           // keys contribute exact zeros to P.V whatever the ring holds there (the stage
           // has landed: the score MMAs of this block have completed)
-          uint8_t* st = sm + OFF_KV + ((sw.gbase + jl) % NST) * BOX_BYTES + t * 128;
+          uint8_t* st = sm + OFF_KV + ((gbase + jl) % NST) * BOX_BYTES + t * 128;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
@@ -1136,12 +1212,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           }
         }
 
-        // a block with draft nodes: finite node rows
+        // A block with draft nodes: finite node rows.  A hidden row's weight is 0, but 0 * NaN would
+        // still reach every row of the tile through the PV product (a node that does see a NaN
+        // row gets it through its scores).
         int nctx = BN;                                 // context keys of the block
         if constexpr (TREE) {
-          nctx = max(min(sw.ctx - (int)g0, valid), 0);
+          nctx = max(min(ctx - (int)g0, valid), 0);
           if (nctx < BN && t < valid && t >= nctx) {
-            uint8_t* st = sm + OFF_KV + ((sw.gbase + jl) % NST) * BOX_BYTES + t * 128;
+            uint8_t* st = sm + OFF_KV + ((gbase + jl) % NST) * BOX_BYTES + t * 128;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
@@ -1152,95 +1230,125 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         }
 
         // full scores: add the peer's partial
-        if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], xc & 1, abort, a.err, 0x203,
-                                                 (t << 16) | j))) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int q = 0; q < BN / 8; ++q) {
-          const uint4 x = my_x[q * TM];
-          if (q == BN / 8 - 1) need = need || (x.x & 1u) != 0u;
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[8 * q + 2 * e] = add_f32_f16(s[8 * q + 2 * e], w[e] & 0xFFFFu);
-            s[8 * q + 2 * e + 1] = add_f32_f16(s[8 * q + 2 * e + 1], w[e] >> 16);
+        if constexpr (TREE) {
+          if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], LY::MERGED ? 0 : xc & 1, abort,
+                                                   a.err, 0x203, (t << 16) | j))) {
+            ok = false;
+            break;
           }
-        }
-        ++xc;
-        // (a thread's `need` takes in its last load, and shared loads return in order: the barrier
-        // below is reached with the buffer read)
-        // The decision: a word per warpgroup and block (four in turn, each cleared two blocks
-        // before its next use) collects the rows' flags across the barrier that also
-        // marks the buffer as read.  Both CTAs see the same pairs of flags.
-        volatile uint32_t* vote = xvote + wg * 4;
-        if (need) atomicOr(const_cast<uint32_t*>(&vote[nd & 3]), 1u);
-        named_bar(1 + wg, TM);
-        const bool exact = vote[nd & 3] != 0u;
-        if (t == 0) vote[(nd + 2) & 3] = 0u;
-        ++nd;
-        if (exact) {
-          // Rounds two and three: undo the fp16 addend (s then holds this CTA's partial to
-          // within one float32 rounding) and swap exact fp32 partials, keys 0-31 then 32-63.
-          // A buffer is handed back once every thread HAS its values: a barrier alone does not wait
-          // for loads in flight, and the peer's next stores do not queue behind them.  The barriers
-          // below therefore carry a predicate of every vector that was loaded.
-          uint32_t seen = 0u;
+          // A warp hands the exchange buffer back for itself once it HAS its values: the credit's
+          // address takes in every vector that was loaded (a.zero is 0), since the peer's next
+          // stores do not queue behind loads in flight.
+          const uint32_t seen = add_scores(s, my_x);
+          if (LY::MERGED && t == 0) mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(peer_xe + (seen & a.zero));
+          if constexpr (LY::MERGED) {
+            if (!send_scores(s + 32, &bar[B_XE + wg], xc & 1, peer_x, peer_xf, abort, a.err,
+                             (t << 16) | j) ||
+                !__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], 1, abort, a.err, 0x208,
+                                                    (t << 16) | j))) {
+              ok = false;
+              break;
+            }
+            add_scores(s + 32, my_x);
+          } else {
+            add_scores(s + 32, my_p);
+          }
+          named_bar(1 + wg, TM);                 // P goes where the partials were
+          ++xc;
+        } else {
+          if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], xc & 1, abort, a.err, 0x203,
+                                                   (t << 16) | j))) {
+            ok = false;
+            break;
+          }
 #pragma unroll
           for (int q = 0; q < BN / 8; ++q) {
             const uint4 x = my_x[q * TM];
-            seen |= x.x;
-            sub_f16x8(x, s + 8 * q);
-          }
-          named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);   // read again, before the hand-back
-          if (t == 0) {
-            mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
-            mbar_arrive_cluster_relaxed(peer_xe);
-          }
-          for (int h = 0; ok && h < 2; ++h) {
-            if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XE + wg], (xc & 1) ^ 1, abort, a.err,
-                                                     0x207, (t << 16) | j))) {
-              ok = false;
-              break;
-            }
+            if (q == BN / 8 - 1) need = need || (x.x & 1u) != 0u;
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int q = 0; q < BN / 8; ++q)
-              st_async_v4(peer_x + q * (TM * 16), __float_as_uint(s[32 * h + 4 * q]),
-                          __float_as_uint(s[32 * h + 4 * q + 1]),
-                          __float_as_uint(s[32 * h + 4 * q + 2]),
-                          __float_as_uint(s[32 * h + 4 * q + 3]), peer_xf);
-            if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], xc & 1, abort, a.err, 0x208,
-                                                     (t << 16) | j))) {
-              ok = false;
-              break;
+            for (int e = 0; e < 4; ++e) {
+              s[8 * q + 2 * e] = add_f32_f16(s[8 * q + 2 * e], w[e] & 0xFFFFu);
+              s[8 * q + 2 * e + 1] = add_f32_f16(s[8 * q + 2 * e + 1], w[e] >> 16);
             }
+          }
+          ++xc;
+          // (a thread's `need` takes in its last load, and shared loads return in order: the barrier
+          // below is reached with the buffer read)
+          // The decision: a word per warpgroup and block (four in turn, each cleared two blocks
+          // before its next use) collects the rows' flags across the barrier that also
+          // marks the buffer as read.  Both CTAs see the same pairs of flags.
+          volatile uint32_t* vote = xvote + wg * 4;
+          if (need) atomicOr(const_cast<uint32_t*>(&vote[nd & 3]), 1u);
+          named_bar(1 + wg, TM);
+          const bool exact = vote[nd & 3] != 0u;
+          if (t == 0) vote[(nd + 2) & 3] = 0u;
+          ++nd;
+          if (exact) {
+            // Rounds two and three: undo the fp16 addend (s then holds this CTA's partial to
+            // within one float32 rounding) and swap exact fp32 partials, keys 0-31 then 32-63.
+            // A buffer is handed back once every thread HAS its values: a barrier alone does not wait
+            // for loads in flight, and the peer's next stores do not queue behind them.  The barriers
+            // below therefore carry a predicate of every vector that was loaded.
+            uint32_t seen = 0u;
 #pragma unroll
             for (int q = 0; q < BN / 8; ++q) {
               const uint4 x = my_x[q * TM];
               seen |= x.x;
-              s[32 * h + 4 * q] += __uint_as_float(x.x);
-              s[32 * h + 4 * q + 1] += __uint_as_float(x.y);
-              s[32 * h + 4 * q + 2] += __uint_as_float(x.z);
-              s[32 * h + 4 * q + 3] += __uint_as_float(x.w);
+              sub_f16x8(x, s + 8 * q);
             }
-            ++xc;
-            named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);
-            if (h == 0 && t == 0) mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);   // round three
-            // with merged buffers the last round's buffer is handed back by the PV commit
-            if (!LY::MERGED || h == 0) {
-              if (t == 0) mbar_arrive_cluster_relaxed(peer_xe);
+            named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);   // read again, before the hand-back
+            if (t == 0) {
+              mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
+              mbar_arrive_cluster_relaxed(peer_xe);
             }
+            for (int h = 0; ok && h < 2; ++h) {
+              if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XE + wg], (xc & 1) ^ 1, abort, a.err,
+                                                       0x207, (t << 16) | j))) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int q = 0; q < BN / 8; ++q)
+                st_async_v4(peer_x + q * (TM * 16), __float_as_uint(s[32 * h + 4 * q]),
+                            __float_as_uint(s[32 * h + 4 * q + 1]),
+                            __float_as_uint(s[32 * h + 4 * q + 2]),
+                            __float_as_uint(s[32 * h + 4 * q + 3]), peer_xf);
+              if (!__all_sync(FULL, mbar_wait_cluster(&bar[B_XF + wg], xc & 1, abort, a.err, 0x208,
+                                                       (t << 16) | j))) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int q = 0; q < BN / 8; ++q) {
+                const uint4 x = my_x[q * TM];
+                seen |= x.x;
+                s[32 * h + 4 * q] += __uint_as_float(x.x);
+                s[32 * h + 4 * q + 1] += __uint_as_float(x.y);
+                s[32 * h + 4 * q + 2] += __uint_as_float(x.z);
+                s[32 * h + 4 * q + 3] += __uint_as_float(x.w);
+              }
+              ++xc;
+              named_bar_or(1 + wg, TM, seen == 0xFFFFFFFFu);
+              if (h == 0 && t == 0) mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);   // round three
+              // with merged buffers the last round's buffer is handed back by the PV commit
+              if (!LY::MERGED || h == 0) {
+                if (t == 0) mbar_arrive_cluster_relaxed(peer_xe);
+              }
+            }
+            if (!ok) break;
+          } else if constexpr (!LY::MERGED) {
+            if (t == 0) mbar_arrive_cluster_relaxed(peer_xe);   // hand the buffer back
           }
-          if (!ok) break;
-        } else if constexpr (!LY::MERGED) {
-          if (t == 0) mbar_arrive_cluster_relaxed(peer_xe);   // hand the buffer back
+
         }
 
         // masked raw maximum (scores are scaled inside the exponent)
         if constexpr (TREE) {
           if (nctx < BN) {
-            const uint64_t sees = tree_bits(a, tg.b, node, nctx, max((int)g0 - sw.ctx, 0), valid);
+            const uint64_t sees = tree_bits(a, seq_b, node, nctx, max((int)g0 - ctx, 0), valid);
 #pragma unroll
             for (int c = 0; c < BN; ++c) s[c] = (sees >> c & 1) ? s[c] : -INFINITY;
           }
@@ -1262,7 +1370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         const float mb = rmax * c2;
 
         // running maximum after the previous block (published by the other warpgroup)
-        const int ow = wg ^ 1, oseq = sw.done_by(ow) + ((jl - 1) >> 1);
+        const int ow = wg ^ 1, oseq = nb_other + ((jl - 1) >> 1);
         float m_prev = -INFINITY;
         if (jl > 0) {
           if (!__all_sync(FULL, mbar_wait(&bar[B_M + ow], oseq & 1, abort, a.err, 0x204,
@@ -1308,7 +1416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           tc_fence_after();
           rescale_row(tmem + lane_base + O_COL, fac);
         }
-        if constexpr (!LY::MERGED) {
+        if constexpr (!LY::MERGED && !TREE) {
           if (!__all_sync(FULL, mbar_wait(&bar[B_PE + wg], kph ^ 1, abort, a.err, 0x206,
                                           (t << 16) | j))) {
             ok = false;
@@ -1329,18 +1437,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       if (!__all_sync(FULL, ok)) break;
 
       // the next segment's Q may enter TMEM once this segment's score MMAs are done
-      const uint32_t kph = sw.k & 1;
+      const uint32_t kph = ks & 1;
       {
-        Walk nx = sw;
-        nx.next(a);
-        if (nx.valid()) {
-          if (!__all_sync(FULL, mbar_wait(&bar[B_QKDONE], kph, abort, a.err, 0x301, t))) break;
+        bool done = true;
+        auto next_q = [&](const Walk& nx) {
+          if (!nx.valid()) return;
+          done = __all_sync(FULL, mbar_wait(&bar[B_QKDONE], kph, abort, a.err, 0x301, t));
+          if (!done) return;
           tc_fence_after();
           load_q(a, tmem + lane_base + Q_COL, nx.tg.grow0 + t, nx.tg.row0 + t < nx.tg.rows_b,
                  rank, wg);
           tc_fence_before();
           mbar_arrive(&bar[B_QREADY]);
+        };
+        if constexpr (TREE) {
+          next_q(wk[(ks + 1) % 3]);
+          if (tid == 0) {
+            // every thread has read the slot, its segment's, before the last one's barriers
+            TreeWalk& w2 = wk[(ks + 2) % 3];
+            w2 = wk[(ks + 1) % 3];
+            if (w2.valid()) w2.next(a);
+          }
+          __syncwarp();
+        } else {
+          Walk nx = sw;
+          nx.next(a);
+          next_q(nx);
         }
+        if (!done) break;
       }
 
       // ---------------------------------------------------------- segment epilogue
@@ -1362,11 +1486,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       const bool any = TREE ? lt != 0.f : lt > 0.f;
       const float inv = any ? 1.f / lt : 0.f;
       const float lse_v = any ? (mf + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
-      const bool part = sw.partial();
+      const bool part = ws_slot >= 0;
       const unsigned live_rows = __ballot_sync(FULL, row_valid) >> (t & 28);
       if (wg == 0 && row_valid) {
         if (part)
-          a.ws_lse[((int64_t)sw.slot * 2 + rank) * TM + t] = lse_v;
+          a.ws_lse[((int64_t)ws_slot * 2 + rank) * TM + t] = lse_v;
         else if (a.lse && rank == 0)
           a.lse[grow] = lse_v;
       }
@@ -1391,7 +1515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
               pack_bf16(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
         quad_transpose(w);
         const int k = t & 3;
-        bf16* dst = (part ? a.ws_o + ((int64_t)sw.slot * TM + (t - k)) * G.Dc
+        bf16* dst = (part ? a.ws_o + ((int64_t)ws_slot * TM + (t - k)) * G.Dc
                           : a.o_lat + (grow - k) * G.Dc) + rank * HALF + c + 8 * k;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -1399,12 +1523,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       }
       tc_fence_before();
       mbar_arrive(&bar[B_OFREE]);
+      if constexpr (!TREE) sw.next(a);
     }
     // with merged buffers the peer's last PV commit arrives on this CTA's barrier: let it
     // land before exit
-    if constexpr (LY::MERGED) {
-      if (ok && !sw.valid() && xc > 0)
-        mbar_wait_cluster(&bar[B_XE + wg], (xc - 1) & 1, abort, a.err, 0x402, t);
+    if constexpr (LY::MERGED || TREE) {
+      if (ok && xc > 0)
+        mbar_wait_cluster(&bar[(TREE ? LY::B_XP : B_XE) + wg], (xc - 1) & 1, abort, a.err, 0x402, t);
     }
   }
 
@@ -1448,11 +1573,11 @@ int cluster_slots() {
     if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c < 1) c = 0;
     n = c < n ? c : n;
   };
-  probe(attend_kernel<0, false>, Lay<0>::SMEM, Lay<0>::NT);
-  probe(attend_kernel<1, false>, Lay<1>::SMEM, Lay<1>::NT);
-  probe(attend_kernel<2, false>, Lay<2>::SMEM, Lay<2>::NT);
-  probe(attend_kernel<0, true>, Lay<0>::SMEM, Lay<0>::NT);
-  probe(attend_kernel<1, true>, Lay<1>::SMEM, Lay<1>::NT);
+  probe(attend_kernel<0>, Lay<0>::SMEM, Lay<0>::NT);
+  probe(attend_kernel<1>, Lay<1>::SMEM, Lay<1>::NT);
+  probe(attend_kernel<2>, Lay<2>::SMEM, Lay<2>::NT);
+  probe(attend_kernel<3>, Lay<3>::SMEM, Lay<3>::NT);
+  probe(attend_kernel<4>, Lay<4>::SMEM, Lay<4>::NT);
   if (!ok) return 0;
   if (n < 1) {
     int sms = 0;
@@ -1722,13 +1847,13 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
   for (const Plan& p : plans) {
     cudaError_t e;
     if (variant == 2)
-      e = launch_dependent(attend_kernel<2, false>, (unsigned)(2 * p.G), Lay<2>::NT, Lay<2>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<2>, (unsigned)(2 * p.G), Lay<2>::NT, Lay<2>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     else if (variant == 1)
-      e = launch_dependent(attend_kernel<1, false>, (unsigned)(2 * p.G), Lay<1>::NT, Lay<1>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<1>, (unsigned)(2 * p.G), Lay<1>::NT, Lay<1>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     else
-      e = launch_dependent(attend_kernel<0, false>, (unsigned)(2 * p.G), Lay<0>::NT, Lay<0>::SMEM, st, 1u,
+      e = launch_dependent(attend_kernel<0>, (unsigned)(2 * p.G), Lay<0>::NT, Lay<0>::SMEM, st, 1u,
                            K, KR, QR, SC, SR, a, p.sc);
     if (e != cudaSuccess) return e;
     count_launches(1);
@@ -1766,9 +1891,6 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   a.g = g;
   a.n_q = n_nodes;
   a.scale_log2 = scale * 1.4426950408889634f;
-  // fp16's error is the same in a whole binade, so the threshold may go up to the next power of two
-  // under the same bound (2^-8 log2 units): fewer rows take the exact exchange
-  a.xthr = fminf(exp2f(ceilf(log2f(exchange_threshold(a.scale_log2)))), 32768.f);
   a.q_abs = (const bf16*)q_abs;
   a.o_lat = (bf16*)o_lat;
   a.lse = lse;
@@ -1796,10 +1918,10 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   }
   cudaError_t e;
   if (wide)
-    e = launch_dependent(attend_kernel<1, true>, (unsigned)(2 * ncl), Lay<1>::NT, Lay<1>::SMEM, st,
+    e = launch_dependent(attend_kernel<4>, (unsigned)(2 * ncl), Lay<4>::NT, Lay<4>::SMEM, st,
                          1u, K, KR, QR, CUtensorMap{}, CUtensorMap{}, a, sc);
   else
-    e = launch_dependent(attend_kernel<0, true>, (unsigned)(2 * ncl), Lay<0>::NT, Lay<0>::SMEM, st,
+    e = launch_dependent(attend_kernel<3>, (unsigned)(2 * ncl), Lay<3>::NT, Lay<3>::SMEM, st,
                          1u, K, KR, QR, CUtensorMap{}, CUtensorMap{}, a, sc);
   if (e != cudaSuccess) return e;
   count_launches(1);

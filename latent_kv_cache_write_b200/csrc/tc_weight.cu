@@ -151,7 +151,10 @@ struct UnitWalk {
   __device__ void keys(uint32_t side, int64_t S, int64_t& slot0, int64_t& j0, int& valid) const {
     const int j = 2 * u + (int)side;
     if (j < s.blk.nblk) {
-      s.blk.get(j, slot0, j0, valid);
+      int sl, jl;
+      s.blk.get<KEYS>(j, sl, jl, valid);
+      slot0 = sl;
+      j0 = jl;
     } else {
       slot0 = S;                               // outside the tensor: the box is filled with zeros
       j0 = 0;

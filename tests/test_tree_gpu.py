@@ -49,9 +49,7 @@ def attend(wl, q, cache_t, windows, see, n, split=True, fill=7.0):
     return o, lse
 
 
-def check_attend(wl, qv, cv, windows, see, n, o, lse, fill=7.0, exchanged=None):
-    if exchanged is None:
-        exchanged = wl.d_latent == 512 and wl.dtype == "bf16"
+def check_attend(wl, qv, cv, windows, see, n, o, lse, fill=7.0):
     ref, rl, spread = D.attend_tree(qv, cv, windows, see, SCALE, wl.d_latent)
     got, gl = P.download(o), P.download(lse)
     for b in range(wl.batch):
@@ -60,7 +58,7 @@ def check_attend(wl, qv, cv, windows, see, n, o, lse, fill=7.0, exchanged=None):
         if m == 0:
             continue
         ds = T.score_error(qv[b, :m], np.nan_to_num(cv[b, D.slots(f, r + m, wl.ring_slots)]),
-                           SCALE, exchanged)
+                           SCALE)
         T.check_within(got[b, :m], ref[b, :m],
                        T.attend_tolerance(spread[b, :m], ref[b, :m], r + m, ds, wl.dtype), "o")
         empty = np.isneginf(rl[b, :m])
@@ -245,7 +243,7 @@ def test_attend_weight(cuda_ok, cfg, n, S, windows):
             assert (got[rest] == old[b, rest]).all(), "slots outside the window"
             if not at:
                 continue
-            ds = T.score_error(q.values[b], c.values[b, at], SCALE, False)
+            ds = T.score_error(q.values[b], c.values[b, at], SCALE)
             rel = 2 * ds + 2.0 ** -20 + (m * wl.n_heads + 8) * T.F32 \
                 + 2.0 ** -23 * np.abs(np.where(np.isfinite(lse32[b, :m]), lse32[b, :m], 0)).max(initial=0)
             T.check_within(got[at], ref[b, at], rel * np.abs(ref[b, at]) + 1e-30, "weight")

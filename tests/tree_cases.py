@@ -47,14 +47,13 @@ BF16 = 2.0 ** -8        # half a step of bf16, relative
 F32 = 2.0 ** -24
 
 
-def score_error(q, k, scale, exchanged):
+def score_error(q, k, scale):
     """Bound on a score's absolute error: float32 products and sums over the row's width (each of
     `width` additions rounds a partial sum of at most sum|q||k|; the tensor cores' adders may
-    truncate, 2 F32 instead of F32), plus, where two SMs exchange rounded partials, 2^-8 of the
-    exponent's log2 unit."""
+    truncate, 2 F32 instead of F32)."""
     width = q.shape[-1]
     size = scale * float(np.linalg.norm(q, axis=-1).max() * np.linalg.norm(k, axis=-1).max())
-    return width * 2 * F32 * size + (2.0 ** -8 * np.log(2.0) if exchanged else 0.0)
+    return width * 2 * F32 * size
 
 
 def attend_tolerance(spread, o, n_keys, d_score, dtype):
