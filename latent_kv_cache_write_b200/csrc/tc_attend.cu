@@ -136,7 +136,8 @@ struct Lay {
   static constexpr int B_SGF = B_KRF + NSTR;   // staging slot loaded (TMA)           [NSG]
   static constexpr int B_SGE = B_SGF + NSG;    // staging slot read (64)               [NSG]
   static constexpr int B_XP = B_SGE + NSG;      // V = 3, 4: P buffer in the peer free  [2]
-  static constexpr int NBAR = B_XP + 2;
+  static constexpr int B_XG = B_XP + 2;         // V = 3: second half of the scores landed (tx) [2]
+  static constexpr int NBAR = B_XG + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   // draft trees: (sequence, tile) of each round, behind the TMEM slot, abort flag, votes [2][4]
   static constexpr int OFF_ROUNDS = OFF_MISC + 48;
@@ -722,6 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       mbar_init(&bar[B_XF + q], 1);
       mbar_init(&bar[B_XE + q], TREE ? 4 : 1);     // TREE: a warp each
       mbar_init(&bar[LY::B_XP + q], 1);
+      mbar_init(&bar[LY::B_XG + q], 1);
       mbar_init(&bar[B_PF + q], 128);
       mbar_init(&bar[B_PE + q], 1);
       mbar_init(&bar[B_M + q], 128);
@@ -1132,7 +1134,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         const uint32_t kph = seq & 1;
         // arm this block's first exchange round: the peer's asynchronous stores complete
         // XP_BYTES of transactions on it (they may land before or after this arrive)
-        if (t == 0) mbar_expect_tx(&bar[B_XF + wg], TREE && !LY::MERGED ? 2 * XP_BYTES : XP_BYTES);
+        if (t == 0) {
+          mbar_expect_tx(&bar[B_XF + wg], XP_BYTES);
+          if (TREE && !LY::MERGED) mbar_expect_tx(&bar[LY::B_XG + wg], XP_BYTES);
+        }
         if (!__all_sync(FULL, mbar_wait(&bar[B_SF + wg], kph, abort, a.err, 0x201, (t << 16) | j))) {
           ok = false;
           break;
@@ -1149,8 +1154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
           // other half follows when the first has been read)
           if (!send_scores(s, &bar[LY::MERGED ? LY::B_XP + wg : B_XE + wg], (xc & 1) ^ 1, peer_x,
                            peer_xf, abort, a.err, (t << 16) | j) ||
-              (!LY::MERGED && !send_scores(s + 32, &bar[LY::B_XP + wg], (xc & 1) ^ 1, peer_p, peer_xf,
-                                           abort, a.err, (t << 16) | j))) {
+              (!LY::MERGED && !send_scores(s + 32, &bar[LY::B_XP + wg], (xc & 1) ^ 1, peer_p,
+                                           mapa(smem_u32(&bar[LY::B_XG + wg]), peer), abort, a.err, (t << 16) | j))) {
             ok = false;
             break;
           }
@@ -1253,6 +1258,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
             }
             add_scores(s + 32, my_x);
           } else {
+            if (!__all_sync(FULL, mbar_wait_cluster(&bar[LY::B_XG + wg], xc & 1, abort, a.err, 0x208,
+                                                    (t << 16) | j))) {
+              ok = false;
+              break;
+            }
             add_scores(s + 32, my_p);
           }
           named_bar(1 + wg, TM);                 // P goes where the partials were
