@@ -28,8 +28,6 @@
 #include "tc_ptx.cuh"
 #include "tmap.h"
 
-#include <stdlib.h>
-
 #include <mutex>
 
 namespace mla {
@@ -100,7 +98,7 @@ __device__ __forceinline__ Groups row_groups(const WeightArgs& p, int64_t b, int
   }
   const float* qw = p.qw + b * p.a.n_q;
   const uint32_t H = (uint32_t)p.a.g.H, nodes = (uint32_t)rows / H;
-#pragma unroll 4
+#pragma unroll 8
   for (uint32_t i = 0; i < nodes; ++i)
     if (qw[i] != 0.f)                          // node i's rows lie in groups i H / 128 .. ((i + 1) H - 1) / 128
       r.set |= ((2ull << (((i + 1) * H - 1) >> 7)) - 1ull) & ~((1ull << (i * H >> 7)) - 1ull);
@@ -487,13 +485,22 @@ __global__ void __launch_bounds__(WT, 1)
             const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (!nodes || sees(i0)) total += s;
           } else {
-            // rows past the last, or rows of several nodes next to draft keys: one by one
+            // rows past the last, or rows of several nodes next to draft keys: a bit per row
+            uint32_t in = live >= 32 ? ~0u : (1u << live) - 1u;
+            if (nodes) {
+              uint32_t seen = 0u;
+              for (uint32_t i = i0; i <= i1; ++i) {
+                const int lo = max((int)(i * H) - (int)r0, 0), hi = (int)((i + 1) * H) - (int)r0;
+                const uint32_t run = (hi >= 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+                if (lo < live && sees(i)) seen |= run;
+              }
+              in &= seen;
+            }
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float2 x = rb[c0 + e];
               const float pe = ex2(fmaf(__uint_as_float(v[e]), p.c2, -x.x));
-              const bool in = e < live && (!nodes || sees((r0 + e) / H));
-              if (in) sum[e & 3] = fmaf(pe, x.y, sum[e & 3]);
+              if (in >> e & 1) sum[e & 3] = fmaf(pe, x.y, sum[e & 3]);
             }
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
@@ -627,8 +634,25 @@ cudaError_t tc_attend_weight(const Geo& g, const void* q_abs, int64_t n_nodes, c
     uint32_t b[2] = {64, few ? 64u : 128u};
     if (!make_tmap_bf16(&Q, q_abs, 2, d, s, b)) return cudaErrorInvalidValue;
   }
-  static const int cps = getenv("WCP") ? atoi(getenv("WCP")) : 2;
-  const int cp = cps;
+  // Pairs per cluster: with P clusters, units of up to T tiles take about ceil(units / P) turns of
+  // T / cp tiles and a load of the keys each.  (Counted with full rings; 148 SMs give 74 clusters of
+  // one pair, 37 of two, 17 of four.  Measured, us with 1 / 2 / 4 pairs: 1 sequence of 1000 rows
+  // and 16 nodes, 128 heads 40 / 24 / 16; 1 of 8000 rows, 40 nodes 92 / 53 / 70; 32 of 4000 rows,
+  // 32 nodes 529 / 588 / 636.)
+  int cp = 1;
+  if (!few) {
+    const int64_t units = (int64_t)g.B * ((g.S + 255) / 256), tiles = (n_nodes * g.H + 255) / 256;
+    double best = 1e300;
+    for (int c = 1; c <= MAXCP; c *= 2) {
+      const int n = g.Dr == 64 ? weight_clusters<9, RES_K>(c) : weight_clusters<16, STREAM>(c);
+      if (n == 0) continue;
+      const double turns = (double)((units + n - 1) / n) * (double)((tiles + c - 1) / c + 1);
+      if (turns < best) {
+        best = turns;
+        cp = c;
+      }
+    }
+  }
   if (g.Dr == 64)
     return few ? launch_weight<9, RES_Q>(K, Q, p, 1, st) : launch_weight<9, RES_K>(K, Q, p, cp, st);
   return few ? launch_weight<16, RES_Q>(K, Q, p, 1, st) : launch_weight<16, STREAM>(K, Q, p, cp, st);

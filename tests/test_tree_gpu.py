@@ -82,6 +82,7 @@ CASES = [
     ("HEADS", 2, 3000, [(5, 2990, 2), (0, 1500, 1)]),
     ("VIDEO", 20, 150, [(140, 97, 20), (2, 0, 13), (0, 128, 20)]),
     ("WIDE", 9, 150, [(140, 97, 9), (2, 0, 5), (0, 64, 9)]),
+    ("WIDE", 40, 600, [(190, 530, 40), (0, 0, 33), (5, 64, 7)]),
 ]
 
 
