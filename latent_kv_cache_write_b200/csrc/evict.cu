@@ -9,22 +9,31 @@
 // the first hole).  The order of the rows does not matter to the attention: a cached key carries
 // its rotation, and the position array moves along.
 //
-// Two launches: one block per sequence chooses the rows and lists the moves (latency-bound: a radix
-// selection over the sequence's weights in shared memory, then two block scans), and the whole GPU
-// copies the listed rows (bound by HBM: each moved row is read and written once).
+// A block per sequence chooses the rows and lists the moves: the rows' ranks as 32-bit keys in shared
+// memory (up to KEYS_SH rows; longer contexts recompute them), a radix selection of the budget's
+// threshold, then ballots and scans that keep the rows' order.  It is bound by the latency of its
+// passes (8192 rows: about 10 us).  Where at most MOVE_HERE rows can move (accepted nodes, a full
+// cache that drops a few rows per step) the block also moves them; otherwise a second launch lets the
+// whole GPU copy the listed rows, each read and written once (bound by HBM).
 #include "launch.h"
+#include "tc_ptx.cuh"
 #include "window.cuh"
+
+#include <mutex>
 
 namespace mla {
 namespace {
 
 constexpr int NT = 1024;                    // threads of a planning block
+constexpr int NW = NT / 32;
+constexpr int KEYS_SH = 48 * 1024;          // keys kept in shared memory
+constexpr int MOVE_HERE = 128;              // rows a planning block moves itself
 constexpr unsigned FULL = 0xffffffffu;
 
 // Workspace: counts [B] (padded to 4), then per sequence `cap` destination and `cap` source slots.
 struct Plan {
   int32_t* count;
-  int32_t* move;                            // [B][2][cap]
+  int32_t* slots;                           // [B][2][cap]
   int64_t cap;
 };
 
@@ -35,8 +44,11 @@ struct EvictArgs {
   int32_t n_sink, n_recent;
   const uint8_t* accept;                    // accept: [B, n_nodes]; null for evict
   int32_t* window;
-  const float* weight;
-  const int32_t* position;
+  void* cache;
+  float* weight;
+  int32_t* position;
+  int32_t per_row;                          // vectors of a cached row
+  int32_t key_rows;                         // keys that fit this launch's shared memory
   Plan plan;
 };
 
@@ -46,105 +58,160 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+constexpr uint32_t SAFE = 0xFFFFFFFFu;      // protected rows (+inf is 0xFF800000)
 
-// Exclusive sum over the block's threads of v, and the total.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+// Warp w's count -> the sum over the warps before it; *total: over all.  `sums`: one word per warp.
+__device__ __forceinline__ uint32_t warp_offsets(uint32_t v, uint32_t* sums, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  if (lane == 0) sums[warp] = v;
+  __syncthreads();
+  uint32_t x = sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(FULL, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) warp_sums[warp] = x;
+  *total = __shfl_sync(FULL, x, 31);
+  const uint32_t before = __shfl_sync(FULL, x, warp ? warp - 1 : 0);
   __syncthreads();
-  if (warp == 0) {
-    uint32_t s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(FULL, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  const uint32_t before = warp ? warp_sums[warp - 1] : 0u;
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
+  return warp ? before : 0u;
 }
 
-__global__ void __launch_bounds__(NT) evict_plan_kernel(EvictArgs a) {
+// Rows listed in dst / src of one sequence, by `warps` warps of which this is number w: four rows'
+// vectors in flight per lane.
+template <typename V>
+__device__ __forceinline__ void move_rows(V* rows, int per_row, float* weight, int32_t* position,
+                                          const int32_t* dst, const int32_t* src, int n, int w,
+                                          int warps) {
+  const int lane = threadIdx.x & 31;
+  for (int k0 = 4 * w; k0 < n; k0 += 4 * warps) {
+    const V* from[4];
+    V* to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u < n ? k0 + u : n - 1;       // (the last row again: the same values)
+      from[u] = rows + (int64_t)src[k] * per_row;
+      to[u] = rows + (int64_t)dst[k] * per_row;
+    }
+    for (int c = lane; c < per_row; c += 32) {
+      V v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = from[u][c];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) to[u][c] = v[u];
+    }
+    if (lane < 4 && k0 + lane < n) {
+      const int d = dst[k0 + lane], s = src[k0 + lane];
+      if (weight) weight[d] = weight[s];
+      if (position) position[d] = position[s];
+    }
+  }
+}
+
+template <typename V, bool MOVE>
+__global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t keys_sh[];     // [key_rows]
   __shared__ uint32_t hist[2048];
-  __shared__ uint32_t warp_sums[32];
+  __shared__ uint32_t sums[32];
   __shared__ uint32_t pick[2];              // chosen digit, rows still to take inside it
   __shared__ int newest_sh;
-  const int b = blockIdx.x, t = threadIdx.x;
+  __shared__ uint32_t safe_sh;
+  __shared__ int32_t list[MOVE ? 2 * MOVE_HERE : 1];
+  const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  tc::grid_dep_wait();                      // the previous kernel's outputs are visible
+  tc::grid_dep_launch();
   const Window w = load_window(a.window, b, a.S, a.accept ? a.n_nodes : a.S);
-  const int32_t* pos = a.position + (int64_t)b * a.S;
-  const float* wt = a.weight + (int64_t)b * a.S;
-  int32_t* dst = a.plan.move + (int64_t)b * 2 * a.plan.cap;
-  int32_t* src = dst + a.plan.cap;
+  int32_t* pos = a.position ? a.position + (int64_t)b * a.S : nullptr;
+  float* wt = a.weight ? a.weight + (int64_t)b * a.S : nullptr;
+  int32_t* dst = MOVE ? list : a.plan.slots + (int64_t)b * 2 * a.plan.cap;
+  int32_t* src = dst + (MOVE ? MOVE_HERE : a.plan.cap);
 
-  int64_t base, n, count;                   // logical rows considered, and how many stay
+  const int base = a.accept ? w.rows : 0;   // logical rows considered: base .. base + n - 1
+  const int n = a.accept ? w.nodes : w.rows;
+  int count = 0;                            // how many of them stay
   uint32_t thr = 0, ties = 0;
-  int newest = 0;
-  // evict: does logical row j outrank the threshold, or tie with it
-  auto key = [&](int64_t j) -> uint32_t {
+  const uint8_t* acc = a.accept ? a.accept + (int64_t)b * a.n_nodes : nullptr;
+  const bool held = n <= a.key_rows;        // their keys stay in shared memory
+  int newest = INT32_MIN;
+  auto make_key = [&](int j) -> uint32_t {
     const int64_t s = w.slot(j, a.S);
     const int32_t p = pos[s];
-    if (p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent) return 0xFFFFFFFFu;
+    if (p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent) return SAFE;
     return weight_key(wt[s]);
   };
+  auto key = [&](int j) -> uint32_t { return held ? keys_sh[j] : make_key(j); };
+  auto finish = [&](int rows, int moves) {
+    if (!MOVE) a.plan.count[b] = moves;
+    a.window[3 * b] = w.first;
+    a.window[3 * b + 1] = rows;
+    a.window[3 * b + 2] = 0;
+  };
 
-  if (a.accept) {
-    base = w.rows;
-    n = w.nodes;
-    count = 0;
-  } else {
-    base = 0;
-    n = w.rows;
-    count = a.n_keep;
+  if (!a.accept) {
     if (n <= a.n_keep) {                    // the whole block agrees: nothing leaves
       __syncthreads();
-      if (t == 0) {
-        a.plan.count[b] = 0;
-        a.window[3 * b] = w.first;
-        a.window[3 * b + 1] = w.rows;
-        a.window[3 * b + 2] = 0;
-      }
+      if (t == 0) finish(n, 0);
       return;
     }
-    if (t == 0) newest_sh = INT32_MIN;
+    count = (int)a.n_keep;
+    if (t == 0) {
+      newest_sh = INT32_MIN;
+      safe_sh = 0u;
+    }
     __syncthreads();
     int mx = INT32_MIN;
-    for (int64_t j = t; j < n; j += NT) mx = max(mx, pos[w.slot(j, a.S)]);
+#pragma unroll 4
+    for (int j = t; j < n; j += NT) mx = max(mx, pos[w.slot(j, a.S)]);
     mx = __reduce_max_sync(FULL, mx);
-    if ((t & 31) == 0) atomicMax(&newest_sh, mx);
+    if (lane == 0) atomicMax(&newest_sh, mx);
     __syncthreads();
     newest = newest_sh;
-    // the n_keep-th largest key, 11 + 11 + 10 bits at a time (11 bits take the exponent and two
-    // mantissa bits at once: weights crowd in few exponents)
-    uint32_t prefix = 0, take = (uint32_t)a.n_keep;
-    const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-    if (a.n_keep > 0) {
+    uint32_t safe = 0;
+#pragma unroll 4
+    for (int j = t; j < n; j += NT) {
+      const uint32_t k = make_key(j);
+      if (held) keys_sh[j] = k;
+      safe += k == SAFE;
+    }
+    safe = __reduce_add_sync(FULL, safe);
+    if (lane == 0 && safe) atomicAdd(&safe_sh, safe);
+    __syncthreads();
+    safe = safe_sh;
+    if (count > 0 && safe >= (uint32_t)count) {
+      thr = SAFE;                           // protected rows alone fill the budget
+      ties = (uint32_t)count;
+    } else if (count > 0) {
+      // the largest key such that `take` rows below SAFE reach it, 11 + 11 + 10 bits at a time (11
+      // bits take the exponent and two mantissa bits at once: weights crowd in few exponents)
+      uint32_t prefix = 0, take = (uint32_t)count - safe;
+      const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+#pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
         for (int q = t; q < 2048; q += NT) hist[q] = 0u;
         __syncthreads();
+        const int sh = shift[pass], above = sh + bits[pass];
         const uint32_t mask = (1u << bits[pass]) - 1u;
-        const int above = shift[pass] + bits[pass];
-        for (int64_t j = t; j < n; j += NT) {
+#pragma unroll 4
+        for (int j = t; j < n; j += NT) {
           const uint32_t k = key(j);
-          if (above == 32 || (k >> above) == prefix) atomicAdd(&hist[(k >> shift[pass]) & mask], 1u);
+          if (k != SAFE && (above == 32 || (k >> above) == prefix)) atomicAdd(&hist[(k >> sh) & mask], 1u);
         }
         __syncthreads();
-        // thread t owns digits 2047 - 2t and 2046 - 2t: rows above them by an exclusive scan
-        const uint32_t h0 = hist[2047 - 2 * t], h1 = hist[2046 - 2 * t];
-        uint32_t total;
-        const uint32_t before = block_scan(h0 + h1, warp_sums, &total);
+        // warp v owns digits 2047 - 64 v .. : rows above each by a scan within the warp
+        const int d0 = 2047 - 2 * t;
+        const uint32_t h0 = hist[d0], h1 = hist[d0 - 1];
+        uint32_t x = h0 + h1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(FULL, x, o);
+          if (lane >= o) x += y;
+        }
+        uint32_t all;
+        const uint32_t before =
+            warp_offsets(__shfl_sync(FULL, x, 31), sums, &all) + x - (h0 + h1);
         if (before < take && take <= before + h0 + h1) {
           const bool first = take <= before + h0;
-          pick[0] = (uint32_t)(first ? 2047 - 2 * t : 2046 - 2 * t);
+          pick[0] = (uint32_t)(first ? d0 : d0 - 1);
           pick[1] = take - before - (first ? 0u : h0);
         }
         __syncthreads();
@@ -152,107 +219,140 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(EvictArgs a) {
         take = pick[1];
         __syncthreads();
       }
+      thr = prefix;
+      ties = take;                          // rows at the threshold that stay: the lowest ones
     }
-    thr = prefix;
-    ties = take;                            // rows at the threshold that stay: the lowest ones
   }
 
-  // Each thread takes a run of consecutive rows, so that one scan orders them.
-  const int64_t per = (n + NT - 1) / NT;
-  const int64_t j0 = t * per < n ? t * per : n, j1 = j0 + per < n ? j0 + per : n;
+  // Each warp takes a run of consecutive rows, 32 at a time, so that ballots order them.
+  const int per = ((n + NT - 1) / NT) * 32;
+  const int j0 = min(warp * per, n), j1 = min(j0 + per, n);
   uint32_t tie0 = 0, total;
   if (a.accept) {
-    const uint8_t* acc = a.accept + (int64_t)b * a.n_nodes;
     uint32_t c = 0;
-    for (int64_t j = j0; j < j1; ++j) c += acc[j] != 0;
-    block_scan(c, warp_sums, &total);
-    count = total;
-  } else if (a.n_keep > 0) {
+    for (int j = j0; j < j1; j += 32) c += __popc(__ballot_sync(FULL, j + lane < j1 && acc[j + lane] != 0));
+    warp_offsets(c, sums, &total);
+    count = (int)total;
+  } else if (count > 0) {
     uint32_t c = 0;
-    for (int64_t j = j0; j < j1; ++j) c += key(j) == thr;
-    tie0 = block_scan(c, warp_sums, &total);
+    for (int j = j0; j < j1; j += 32) c += __popc(__ballot_sync(FULL, j + lane < j1 && key(j + lane) == thr));
+    tie0 = warp_offsets(c, sums, &total);
   }
-  auto stays = [&](int64_t j, uint32_t& tie) -> bool {
-    if (a.accept) return a.accept[(int64_t)b * a.n_nodes + j] != 0;
-    if (a.n_keep == 0) return false;
-    const uint32_t k = key(j);
-    if (k == thr) return tie++ < ties;
-    return k > thr;
+  // whether row j (this lane's of the 32 at hand) stays; `tie` counts threshold rows before the 32
+  auto stays = [&](int j, uint32_t& tie) -> bool {
+    const bool in = j < j1;
+    if (a.accept) return in && acc[j] != 0;
+    if (count == 0) return false;
+    const uint32_t k = in ? key(j) : 0u;
+    const unsigned m = __ballot_sync(FULL, in && k == thr);
+    const uint32_t rank = tie + __popc(m & ((1u << lane) - 1u));
+    tie += __popc(m);
+    return in && (k == thr ? rank < ties : k > thr);
   };
-  // holes below count (low half) and staying rows past it (high half): at most 2^15 of each per
-  // thread would be needed to mix them, but the block totals need 32 bits, so two scans
   uint32_t holes = 0, late = 0, tie = tie0;
-  for (int64_t j = j0; j < j1; ++j) {
-    const bool s = stays(j, tie);
-    holes += j < count && !s;
-    late += j >= count && s;
+  for (int j = j0; j < j1; j += 32) {
+    const bool s = stays(j + lane, tie), in = j + lane < j1;
+    holes += __popc(__ballot_sync(FULL, in && j + lane < count && !s));
+    late += __popc(__ballot_sync(FULL, j + lane >= count && s));
   }
   uint32_t n_move, n_late;
-  uint32_t hole = block_scan(holes, warp_sums, &n_move);
-  uint32_t lt = block_scan(late, warp_sums, &n_late);
+  uint32_t hole = warp_offsets(holes, sums, &n_move);
+  uint32_t lt = warp_offsets(late, sums, &n_late);
   tie = tie0;
-  for (int64_t j = j0; j < j1; ++j) {
-    const bool s = stays(j, tie);
-    if (j < count && !s) dst[hole++] = (int32_t)w.slot(base + j, a.S);
-    if (j >= count && s) src[lt++] = (int32_t)w.slot(base + j, a.S);
+  for (int j = j0; j < j1; j += 32) {
+    const bool s = stays(j + lane, tie), in = j + lane < j1;
+    const int32_t slot = in ? (int32_t)w.slot(base + j + lane, a.S) : 0;
+    const bool is_hole = in && j + lane < count && !s, is_late = j + lane >= count && s;
+    const unsigned mh = __ballot_sync(FULL, is_hole), ml = __ballot_sync(FULL, is_late);
+    const unsigned below = (1u << lane) - 1u;
+    if (is_hole) dst[hole + __popc(mh & below)] = slot;
+    if (is_late) src[lt + __popc(ml & below)] = slot;
+    hole += __popc(mh);
+    lt += __popc(ml);
   }
-  if (t == 0) {
-    a.plan.count[b] = (int32_t)n_move;
-    a.window[3 * b] = w.first;
-    a.window[3 * b + 1] = (int32_t)(base + count);
-    a.window[3 * b + 2] = 0;
+  if (MOVE) {
+    __syncthreads();                        // the list is complete
+    move_rows(static_cast<V*>(a.cache) + (int64_t)b * a.S * a.per_row, a.per_row, wt, pos, dst, src,
+              (int)n_move, warp, NW);
   }
+  if (t == 0) finish(base + count, (int)n_move);
 }
 
-// Copy the listed rows: blockIdx.y is the sequence; its blocks' threads take the rows' vectors
-// in turn.
+// Copy the listed rows; blockIdx.y is the sequence.
 template <typename V>
-__global__ void __launch_bounds__(256)
-    evict_move_kernel(int64_t S, int per_row, V* cache, float* weight, int32_t* position,
-                      Plan plan) {
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  tc::grid_dep_wait();                      // the plan is visible
+  tc::grid_dep_launch();
   const int b = blockIdx.y;
-  const int64_t n = plan.count[b];
-  const int32_t* dst = plan.move + (int64_t)b * 2 * plan.cap;
-  const int32_t* src = dst + plan.cap;
-  V* rows = cache + (int64_t)b * S * per_row;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  for (int64_t k = t; k < n; k += step) {
-    const int64_t d = b * S + dst[k], s = b * S + src[k];
-    if (weight) weight[d] = weight[s];
-    if (position) position[d] = position[s];
-  }
-  for (int64_t e = t; e < n * per_row; e += step) {
-    const int64_t k = e / per_row;
-    const int c = (int)(e - k * per_row);
-    rows[(int64_t)dst[k] * per_row + c] = rows[(int64_t)src[k] * per_row + c];
-  }
+  const int32_t* dst = a.plan.slots + (int64_t)b * 2 * a.plan.cap;
+  move_rows(static_cast<V*>(a.cache) + (int64_t)b * a.S * a.per_row, a.per_row,
+            a.weight ? a.weight + (int64_t)b * a.S : nullptr,
+            a.position ? a.position + (int64_t)b * a.S : nullptr, dst, dst + a.plan.cap,
+            a.plan.count[b], (int)(blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32),
+            (int)(gridDim.x * (blockDim.x / 32)));
 }
 
-cudaError_t run(const Geo& g, bool bf, void* cache, float* weight, int32_t* position,
-                const EvictArgs& a, cudaStream_t st) {
-  evict_plan_kernel<<<g.B, NT, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+template <typename V>
+cudaError_t run_as(const Geo& g, EvictArgs a, int64_t most, cudaStream_t st) {
+  if (most <= MOVE_HERE) {
+    // (the few rows' keys fit without opting in to more shared memory)
+    const int rows = a.accept ? 0 : (int)(g.S < 8192 ? g.S : 8192);
+    a.key_rows = rows;
+    cudaError_t e = launch_dependent(evict_plan_kernel<V, true>, (unsigned)g.B, NT,
+                                     (size_t)rows * 4, st, 1u, a);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+  }
+  {
+    // the shared-memory opt-in is per device
+    static std::mutex mu;
+    static uint64_t done = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !(done >> dev & 1)) {
+      e = cudaFuncSetAttribute(evict_plan_kernel<V, false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, KEYS_SH * 4);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) done |= 1ull << dev;
+    }
+  }
+  a.key_rows = a.accept ? 0 : (int)(g.S < KEYS_SH ? g.S : KEYS_SH);
+  cudaError_t e = launch_dependent(evict_plan_kernel<V, false>, (unsigned)g.B, NT,
+                                   (size_t)a.key_rows * 4, st, 1u, a);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  const int bytes = g.row * (bf ? 2 : 4);
-  const int x = (148 * 8 + g.B - 1) / g.B;
-  const dim3 grid((unsigned)x, (unsigned)g.B);
-  if (bytes % 16 == 0)
-    evict_move_kernel<uint4><<<grid, 256, 0, st>>>(g.S, bytes / 16, (uint4*)cache, weight, position,
-                                                   a.plan);
-  else                                      // rows are an even number of 2- or 4-byte elements
-    evict_move_kernel<uint32_t><<<grid, 256, 0, st>>>(g.S, bytes / 4, (uint32_t*)cache, weight,
-                                                      position, a.plan);
-  e = cudaGetLastError();
+  const unsigned x = (unsigned)((148 * 8 + g.B - 1) / g.B);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(x, (unsigned)g.B);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_move_kernel<V>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
+}
+
+// most: how many rows of a sequence can move
+cudaError_t run(const Geo& g, bool bf, EvictArgs a, int64_t most, cudaStream_t st) {
+  const int bytes = g.row * (bf ? 2 : 4);
+  if (bytes % 16 == 0) {
+    a.per_row = bytes / 16;
+    return run_as<uint4>(g, a, most, st);
+  }
+  a.per_row = bytes / 4;                    // rows are an even number of 2- or 4-byte elements
+  return run_as<uint32_t>(g, a, most, st);
 }
 
 Plan make_plan(const Geo& g, void* workspace) {
   Plan p;
   p.count = static_cast<int32_t*>(workspace);
-  p.move = p.count + ((g.B + 3) / 4) * 4;
+  p.slots = p.count + ((g.B + 3) / 4) * 4;
   p.cap = plan_cap(g.S);
   return p;
 }
@@ -267,9 +367,9 @@ cudaError_t tree_accept(const Geo& g, bool bf, void* cache, int64_t n_nodes, con
                         int32_t* window, float* weight, int32_t* position, void* workspace,
                         cudaStream_t st) {
   EvictArgs a{};
-  a.S = g.S; a.n_nodes = n_nodes; a.accept = accept; a.window = window;
+  a.S = g.S; a.n_nodes = n_nodes; a.accept = accept; a.window = window; a.cache = cache;
   a.weight = weight; a.position = position; a.plan = make_plan(g, workspace);
-  return run(g, bf, cache, weight, position, a, st);
+  return run(g, bf, a, n_nodes / 2, st);
 }
 
 cudaError_t cache_evict(const Geo& g, bool bf, void* cache, int64_t n_keep, int32_t n_sink,
@@ -277,8 +377,8 @@ cudaError_t cache_evict(const Geo& g, bool bf, void* cache, int64_t n_keep, int3
                         void* workspace, cudaStream_t st) {
   EvictArgs a{};
   a.S = g.S; a.n_keep = n_keep; a.n_sink = n_sink; a.n_recent = n_recent; a.window = window;
-  a.weight = weight; a.position = position; a.plan = make_plan(g, workspace);
-  return run(g, bf, cache, weight, position, a, st);
+  a.cache = cache; a.weight = weight; a.position = position; a.plan = make_plan(g, workspace);
+  return run(g, bf, a, n_keep < g.S - n_keep ? n_keep : g.S - n_keep, st);
 }
 
 }  // namespace mla
