@@ -133,11 +133,12 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
   const uint8_t* acc = a.accept ? a.accept + (int64_t)b * a.n_nodes : nullptr;
   const bool held = n <= a.key_rows;        // their keys stay in shared memory
   int newest = INT32_MIN;
+  auto rank_key = [&](int32_t p, float x) -> uint32_t {
+    return p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent ? SAFE : weight_key(x);
+  };
   auto make_key = [&](int j) -> uint32_t {
     const int64_t s = w.slot(j, a.S);
-    const int32_t p = pos[s];
-    if (p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent) return SAFE;
-    return weight_key(wt[s]);
+    return rank_key(pos[s], wt[s]);
   };
   auto key = [&](int j) -> uint32_t { return held ? keys_sh[j] : make_key(j); };
   auto finish = [&](int rows, int moves) {
@@ -159,16 +160,38 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       safe_sh = 0u;
     }
     __syncthreads();
+    // the first HEAD rows of each thread with all loads in flight at once, the rest in turn
+    constexpr int HEAD = 8;
+    int32_t p8[HEAD];
+    float x8[HEAD];
     int mx = INT32_MIN;
+#pragma unroll
+    for (int u = 0; u < HEAD; ++u) {
+      const int j = t + u * NT;
+      const int64_t s = j < n ? w.slot(j, a.S) : 0;
+      p8[u] = j < n ? pos[s] : INT32_MIN;
+      x8[u] = j < n ? wt[s] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < HEAD; ++u) mx = max(mx, p8[u]);
 #pragma unroll 4
-    for (int j = t; j < n; j += NT) mx = max(mx, pos[w.slot(j, a.S)]);
+    for (int j = t + HEAD * NT; j < n; j += NT) mx = max(mx, pos[w.slot(j, a.S)]);
     mx = __reduce_max_sync(FULL, mx);
     if (lane == 0) atomicMax(&newest_sh, mx);
     __syncthreads();
     newest = newest_sh;
     uint32_t safe = 0;
+#pragma unroll
+    for (int u = 0; u < HEAD; ++u) {
+      const int j = t + u * NT;
+      if (j < n) {
+        const uint32_t k = rank_key(p8[u], x8[u]);
+        if (held) keys_sh[j] = k;
+        safe += k == SAFE;
+      }
+    }
 #pragma unroll 4
-    for (int j = t; j < n; j += NT) {
+    for (int j = t + HEAD * NT; j < n; j += NT) {
       const uint32_t k = make_key(j);
       if (held) keys_sh[j] = k;
       safe += k == SAFE;
