@@ -1,16 +1,17 @@
 // Draft-tree attention and the attention weight of cached rows on CUDA cores: every dtype and
 // shape (float32 storage uses it throughout, and bfloat16 shapes the tensor-core kernels do not
 // take).  Accumulation is float32.  A warp owns one row of the score matrix (attention) or one of
-// its columns (weight) and walks it in order; at the sizes float32 serves (a few heads, tens of
-// rows) both are bound by the latency of one dot product after the other.
+// its columns (weight) and walks it in order.  At the sizes float32 serves (a few heads, tens of
+// rows) that is bound by the latency of one dot product after the other, so rows of up to 128
+// elements take eight at a time (57 rows, 4 heads: 32 -> 10 us); wider rows fill the registers
+// one by one.
 #include "launch.h"
 #include "window.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int MAXR = 40;                    // row width <= 32 * MAXR
-constexpr int U = 4;                        // scores in flight per warp
+constexpr int WIDE = 40, NARROW = 4;        // row width <= 32 * either
 constexpr unsigned FULL = 0xffffffffu;
 
 __device__ __forceinline__ float warp_sum(float s) {
@@ -19,9 +20,19 @@ __device__ __forceinline__ float warp_sum(float s) {
   return s;
 }
 
-// One warp per (sequence, node, head): online softmax over the visible rows.  Hidden nodes are
-// skipped, not masked, so nothing of their rows enters the sums.
-template <typename T>
+// Elements lane, lane + 32, ... of a row of `width`; 0 past it.
+template <typename T, int MAXR>
+__device__ __forceinline__ void load_row(const T* row, int width, float (&v)[MAXR]) {
+#pragma unroll
+  for (int r = 0; r < MAXR; ++r) {
+    const int d = (threadIdx.x & 31) + 32 * r;
+    v[r] = d < width ? to_f32(row[d]) : 0.f;
+  }
+}
+
+// One warp per (sequence, node, head): online softmax over the visible rows, U at a time.  Hidden
+// nodes are skipped, not masked, so nothing of their rows enters the sums.
+template <typename T, int MAXR, int U>
 __global__ void __launch_bounds__(256)
     attend_tree_simt_kernel(Geo g, const T* q_abs, int64_t n_nodes, const T* cache,
                             const int32_t* window, const uint8_t* tree, float scale, T* o_lat,
@@ -35,36 +46,48 @@ __global__ void __launch_bounds__(256)
   if (i >= w.nodes) return;
   const uint8_t* tb = tree ? tree + (int64_t)b * n_nodes * n_nodes : nullptr;
   const int64_t qrow = ((int64_t)b * n_nodes + i) * g.H + h;
-  const T* q = q_abs + qrow * g.row;
-  const int nr = (g.row + 31) / 32, nc = (g.Dc + 31) / 32;
   float qv[MAXR], acc[MAXR];
+  load_row<T, MAXR>(q_abs + qrow * g.row, g.row, qv);
 #pragma unroll
   for (int r = 0; r < MAXR; ++r) {
-    const int d = lane + 32 * r;
-    qv[r] = (r < nr && d < g.row) ? to_f32(q[d]) * scale : 0.f;
+    qv[r] *= scale;
     acc[r] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
   const T* base = cache + (int64_t)b * g.S * g.row;
-  for (int64_t j = 0; j < w.len(); ++j) {
-    if (j >= w.rows && !tree_sees(tb, n_nodes, i, j - w.rows)) continue;
-    const T* row = base + w.slot(j, g.S) * g.row;
-    float kv[MAXR], s = 0.f;
+  for (int64_t j0 = 0; j0 < w.len(); j0 += U) {
+    float kv[U][MAXR], s[U];
+    bool in[U];
 #pragma unroll
-    for (int r = 0; r < MAXR; ++r) {
-      const int d = lane + 32 * r;
-      kv[r] = (r < nr && d < g.row) ? to_f32(row[d]) : 0.f;
-      s = fmaf(qv[r], kv[r], s);
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = j0 + u;
+      in[u] = j < w.rows || (j < w.len() && tree_sees(tb, n_nodes, i, j - w.rows));
+      s[u] = 0.f;
+      if (in[u]) {
+        load_row<T, MAXR>(base + w.slot(j, g.S) * g.row, g.row, kv[u]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < MAXR; ++r) kv[u][r] = 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < MAXR; ++r) s[u] = fmaf(qv[r], kv[u][r], s[u]);
     }
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float ref = mn == -INFINITY ? 0.f : mn;       // every score so far -inf
-    const float corr = expf(m - ref), p = expf(s - ref);
-    l = l * corr + p;
 #pragma unroll
-    for (int r = 0; r < MAXR; ++r) {
-      const int d = lane + 32 * r;
-      if (r < nc && d < g.Dc) acc[r] = fmaf(acc[r], corr, p * kv[r]);
+    for (int u = 0; u < U; ++u) s[u] = warp_sum(s[u]);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = in[u] ? fmaxf(mn, s[u]) : mn;
+    const float ref = mn == -INFINITY ? 0.f : mn;       // every score so far -inf
+    const float corr = expf(m - ref);
+    l *= corr;
+#pragma unroll
+    for (int r = 0; r < MAXR; ++r) acc[r] *= corr;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float p = in[u] ? expf(s[u] - ref) : 0.f;
+      l += p;
+#pragma unroll
+      for (int r = 0; r < MAXR; ++r) acc[r] = fmaf(p, kv[u][r], acc[r]);
     }
     m = mn;
   }
@@ -73,14 +96,14 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int r = 0; r < MAXR; ++r) {
     const int d = lane + 32 * r;
-    if (r < nc && d < g.Dc) out[d] = from_f32<T>(acc[r] * inv);
+    if (d < g.Dc) out[d] = from_f32<T>(acc[r] * inv);
   }
   if (lse && lane == 0) lse[qrow] = l != 0.f ? m + logf(l) : -INFINITY;
 }
 
 // One warp per (sequence, row of the window): the row stays in registers while the warp walks
-// the queries in order.
-template <typename T>
+// the queries in order, U heads at a time.
+template <typename T, int MAXR, int U>
 __global__ void __launch_bounds__(256)
     attend_weight_simt_kernel(Geo g, const T* q_abs, int64_t n_nodes, const T* cache,
                               const int32_t* window, const uint8_t* tree, float scale,
@@ -92,14 +115,10 @@ __global__ void __launch_bounds__(256)
   if (j >= w.len()) return;
   const uint8_t* tb = tree ? tree + (int64_t)b * n_nodes * n_nodes : nullptr;
   const int64_t at = (int64_t)b * g.S + w.slot(j, g.S);
-  const T* row = cache + at * g.row;
-  const int nr = (g.row + 31) / 32;
   float kv[MAXR];
+  load_row<T, MAXR>(cache + at * g.row, g.row, kv);
 #pragma unroll
-  for (int r = 0; r < MAXR; ++r) {
-    const int d = lane + 32 * r;
-    kv[r] = (r < nr && d < g.row) ? to_f32(row[d]) * scale : 0.f;
-  }
+  for (int r = 0; r < MAXR; ++r) kv[r] *= scale;
   float total = 0.f;
   for (int64_t i = 0; i < w.nodes; ++i) {
     const float c = qw ? qw[(int64_t)b * n_nodes + i] : 1.f;
@@ -109,12 +128,12 @@ __global__ void __launch_bounds__(256)
       float s[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const T* q = q_abs + (q0 + h0 + u) * g.row;
         s[u] = 0.f;
+        if (h0 + u < g.H) {
+          float qv[MAXR];
+          load_row<T, MAXR>(q_abs + (q0 + h0 + u) * g.row, g.row, qv);
 #pragma unroll
-        for (int r = 0; r < MAXR; ++r) {
-          const int d = lane + 32 * r;
-          if (h0 + u < g.H && r < nr && d < g.row) s[u] = fmaf(to_f32(q[d]), kv[r], s[u]);
+          for (int r = 0; r < MAXR; ++r) s[u] = fmaf(qv[r], kv[r], s[u]);
         }
       }
 #pragma unroll
@@ -130,20 +149,45 @@ __global__ void __launch_bounds__(256)
   if (lane == 0) wout[at] = (j < w.rows && win ? win[at] : 0.f) + total;
 }
 
+template <typename T>
+void launch_attend(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                   const int32_t* window, const uint8_t* tree, float scale, void* o_lat, float* lse,
+                   cudaStream_t st) {
+  const dim3 grid((g.H + 7) / 8, (unsigned)n_nodes, g.B);
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, st>>>(g, (const T*)q_abs, n_nodes, (const T*)cache, window, tree, scale,
+                               (T*)o_lat, lse);
+  };
+  if (g.row <= 32 * NARROW)
+    run(attend_tree_simt_kernel<T, NARROW, 8>);
+  else
+    run(attend_tree_simt_kernel<T, WIDE, 1>);
+}
+
+template <typename T>
+void launch_weight(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
+                   const int32_t* window, const uint8_t* tree, float scale, const float* lse,
+                   const float* qw, const float* win, float* wout, cudaStream_t st) {
+  const dim3 grid((unsigned)((g.S + 7) / 8), g.B);
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, st>>>(g, (const T*)q_abs, n_nodes, (const T*)cache, window, tree, scale,
+                               lse, qw, win, wout);
+  };
+  if (g.row <= 32 * NARROW)
+    run(attend_weight_simt_kernel<T, NARROW, 4>);
+  else
+    run(attend_weight_simt_kernel<T, WIDE, 2>);
+}
+
 }  // namespace
 
 cudaError_t simt_attend_tree(const Geo& g, bool bf, const void* q_abs, int64_t n_nodes,
                              const void* cache, const int32_t* window, const uint8_t* tree,
                              float scale, void* o_lat, float* lse, cudaStream_t st) {
-  dim3 grid((g.H + 7) / 8, (unsigned)n_nodes, g.B);
   if (bf)
-    attend_tree_simt_kernel<bf16><<<grid, 256, 0, st>>>(g, (const bf16*)q_abs, n_nodes,
-                                                        (const bf16*)cache, window, tree, scale,
-                                                        (bf16*)o_lat, lse);
+    launch_attend<bf16>(g, q_abs, n_nodes, cache, window, tree, scale, o_lat, lse, st);
   else
-    attend_tree_simt_kernel<float><<<grid, 256, 0, st>>>(g, (const float*)q_abs, n_nodes,
-                                                         (const float*)cache, window, tree, scale,
-                                                         (float*)o_lat, lse);
+    launch_attend<float>(g, q_abs, n_nodes, cache, window, tree, scale, o_lat, lse, st);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launches(1);
   return e;
@@ -153,15 +197,10 @@ cudaError_t simt_attend_weight(const Geo& g, bool bf, const void* q_abs, int64_t
                                const void* cache, const int32_t* window, const uint8_t* tree,
                                float scale, const float* lse, const float* qw, const float* win,
                                float* wout, cudaStream_t st) {
-  dim3 grid((unsigned)((g.S + 7) / 8), g.B);
   if (bf)
-    attend_weight_simt_kernel<bf16><<<grid, 256, 0, st>>>(g, (const bf16*)q_abs, n_nodes,
-                                                          (const bf16*)cache, window, tree, scale,
-                                                          lse, qw, win, wout);
+    launch_weight<bf16>(g, q_abs, n_nodes, cache, window, tree, scale, lse, qw, win, wout, st);
   else
-    attend_weight_simt_kernel<float><<<grid, 256, 0, st>>>(g, (const float*)q_abs, n_nodes,
-                                                           (const float*)cache, window, tree,
-                                                           scale, lse, qw, win, wout);
+    launch_weight<float>(g, q_abs, n_nodes, cache, window, tree, scale, lse, qw, win, wout, st);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launches(1);
   return e;
