@@ -491,7 +491,8 @@ size_t mla_cache_evict_workspace_size(const mla_shape* shape);
  *   window   [B, 3] int32                              read and written
  *   workspace: at least mla_cache_evict_workspace_size() bytes (required); calls that share
  *   one must not run concurrently.
- * Errors: MLA_ERR_ARG, MLA_ERR_RANGE (n_nodes > S), MLA_ERR_ALIGN.
+ * Errors: MLA_ERR_ARG, MLA_ERR_RANGE (n_nodes > S), MLA_ERR_UNSUPPORTED (S > 2^30),
+ * MLA_ERR_ALIGN.
  */
 mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
                            const uint8_t* accept, int32_t* window, float* weight,
@@ -512,7 +513,8 @@ mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
  *   weight [B, S] float32, position [B, S] int32       read, moved with the rows
  *   cache, window, workspace                           as in mla_tree_accept
  * Errors: MLA_ERR_ARG for a NULL tensor or workspace, one that is too small, or a negative
- * n_keep, n_sink or n_recent; MLA_ERR_RANGE for n_keep > S; MLA_ERR_ALIGN.
+ * n_keep, n_sink or n_recent; MLA_ERR_RANGE for n_keep > S; MLA_ERR_UNSUPPORTED for S > 2^30;
+ * MLA_ERR_ALIGN.
  */
 mla_status mla_cache_evict(const mla_shape* shape, void* cache, int64_t n_keep, int32_t n_sink,
                            int32_t n_recent, int32_t* window, float* weight, int32_t* position,

@@ -69,7 +69,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object takes longer than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -177,18 +178,48 @@ def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
+def _args(item: int, *tensors) -> list:
+    """Device pointers of tensors whose elements have ``item`` bytes.  A tensor of the host or of
+    another device than the current one, one with strides of its own, and one of another element
+    size raise ValueError: the library sees pointers only."""
+    current = _current_device()
+    out = []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            out.append(t)
+        elif t.get_device() == current and t.element_size() == item and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            raise ValueError(f"a contiguous tensor with {item}-byte elements on cuda:{current}, the "
+                             f"current device, is needed, not {t.dtype} {tuple(t.shape)} with "
+                             f"strides {t.stride()} on {t.device}")
+    return out
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _item(shape: MlaShape) -> int:
+    return 2 if shape.dtype == native.MLA_BF16 else 4
+
+
 def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
                    cache, position=None, stream=None) -> None:
+    h, w_dkv, w_kr, cache = _args(_item(shape), h, w_dkv, w_kr, cache)
+    window, token, position = _args(4, window, token, position)
     native.check("mla_tree_write", native.lib().mla_tree_write(
-        ctypes.byref(shape), _ptr(h), d_model, n_nodes, _ptr(window), _ptr(token), _ptr(w_dkv),
-        _ptr(w_kr), _ptr(cache), _ptr(position), _stream(stream)))
+        ctypes.byref(shape), h, d_model, n_nodes, window, token, w_dkv, w_kr, cache, position,
+        _stream(stream)))
 
 
 def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
                       stream=None) -> None:
+    q_nope, q_rope, w_uk, q_abs = _args(_item(shape), q_nope, q_rope, w_uk, q_abs)
+    token, = _args(4, token)
     native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
-        ctypes.byref(shape), _ptr(q_nope), _ptr(q_rope), n_nodes, _ptr(token), _ptr(w_uk),
-        _ptr(q_abs), _stream(stream)))
+        ctypes.byref(shape), q_nope, q_rope, n_nodes, token, w_uk, q_abs, _stream(stream)))
 
 
 def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
@@ -198,19 +229,25 @@ def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
 def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                     softmax_scale: float, o_lat, lse=None, workspace=None,
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
+    n = _bytes(workspace, workspace_bytes)
+    q_abs, cache, o_lat = _args(_item(shape), q_abs, cache, o_lat)
+    window, lse = _args(4, window, lse)
+    tree, = _args(1, tree)
     native.check("mla_attend_tree", native.lib().mla_attend_tree(
-        ctypes.byref(shape), _ptr(q_abs), n_nodes, _ptr(cache), _ptr(window), _ptr(tree),
-        softmax_scale, _ptr(o_lat), _ptr(lse), _ptr(workspace), _bytes(workspace, workspace_bytes),
-        _stream(stream)))
+        ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, o_lat, lse,
+        _ptr(workspace), n, _stream(stream)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                       softmax_scale: float, lse, query_weight, weight_in, weight_out,
                       stream=None) -> None:
+    q_abs, cache = _args(_item(shape), q_abs, cache)
+    window, lse, query_weight, weight_in, weight_out = _args(4, window, lse, query_weight,
+                                                             weight_in, weight_out)
+    tree, = _args(1, tree)
     native.check("mla_attend_weight", native.lib().mla_attend_weight(
-        ctypes.byref(shape), _ptr(q_abs), n_nodes, _ptr(cache), _ptr(window), _ptr(tree),
-        softmax_scale, _ptr(lse), _ptr(query_weight), _ptr(weight_in), _ptr(weight_out),
-        _stream(stream)))
+        ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
+        query_weight, weight_in, weight_out, _stream(stream)))
 
 
 def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
@@ -219,17 +256,24 @@ def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
 
 def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    n = _bytes(workspace, workspace_bytes)
+    cache, = _args(_item(shape), cache)
+    window, weight, position = _args(4, window, weight, position)
+    accept, = _args(1, accept)
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
-        ctypes.byref(shape), _ptr(cache), n_nodes, _ptr(accept), _ptr(window), _ptr(weight),
-        _ptr(position), _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))
+        ctypes.byref(shape), cache, n_nodes, accept, window, weight, position, _ptr(workspace), n,
+        _stream(stream)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
                     weight, position, workspace, workspace_bytes: Optional[int] = None,
                     stream=None) -> None:
+    n = _bytes(workspace, workspace_bytes)
+    cache, = _args(_item(shape), cache)
+    window, weight, position = _args(4, window, weight, position)
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
-        ctypes.byref(shape), _ptr(cache), n_keep, n_sink, n_recent, _ptr(window), _ptr(weight),
-        _ptr(position), _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))
+        ctypes.byref(shape), cache, n_keep, n_sink, n_recent, window, weight, position,
+        _ptr(workspace), n, _stream(stream)))
 
 
 def mla_kernel_launches() -> int:

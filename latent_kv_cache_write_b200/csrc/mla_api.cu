@@ -129,6 +129,7 @@ mla_status check_move(const mla_shape* shape, Geo* g, const void* cache, const i
   if (st != MLA_OK) return st;
   if (!cache || !window || !workspace || workspace_bytes < evict_workspace(*g))
     return MLA_ERR_ARG;
+  if (g->S > (1 << 30)) return MLA_ERR_UNSUPPORTED;     // rows are counted in steps of a block
   if (!aligned16(cache) || !aligned4(window) || !aligned4(weight) || !aligned4(position) ||
       !aligned16(workspace))
     return MLA_ERR_ALIGN;

@@ -99,7 +99,54 @@ def test_scales_and_workspaces(L):
     assert L.mla_cache_evict_workspace_size(ctypes.byref(shape(batch=0))) == 0
 
 
+def test_evict_long_rings(L):
+    long = shape(batch=1, ring_slots=(1 << 30) + 1)
+    for name in ("mla_tree_accept", "mla_cache_evict"):
+        assert call(L, name, long, ws_bytes=1 << 62) == UNS
+
+
 def test_evict_budgets(L):
     for k in ("keep", "sink", "recent"):
         assert call(L, "mla_cache_evict", **{k: -1}) == ARG
     assert call(L, "mla_cache_evict", keep=8193) == RANGE
+
+
+def test_binding_refuses_tensors_it_cannot_pass(monkeypatch):
+    """The library sees pointers: host tensors, strided ones, other element sizes and other devices
+    stop in the binding."""
+    import torch
+
+    import latent_kv_cache_write_b200 as mla
+
+    class Fake:
+        dtype, shape, device = torch.bfloat16, (4, 4), "cuda:1"
+
+        def __init__(self, item=2, contiguous=True, dev=0):
+            self.item, self.contiguous, self.dev = item, contiguous, dev
+
+        def element_size(self):
+            return self.item
+
+        def is_contiguous(self):
+            return self.contiguous
+
+        def stride(self):
+            return (4, 1)
+
+        def get_device(self):
+            return self.dev
+
+        def data_ptr(self):
+            return FAKE
+
+    monkeypatch.setattr(mla, "_current_device", lambda: 0)
+    assert mla._args(2, Fake(), None, 7) == [FAKE, None, 7]
+    for bad in (Fake(item=4), Fake(contiguous=False), Fake(dev=1), torch.zeros(4, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            mla._args(2, bad)
+    s = shape()
+    with pytest.raises(ValueError):
+        mla.mla_attend_tree(s, torch.zeros(4), 1, FAKE, FAKE, None, 0.1, FAKE, stream=0)
+    with pytest.raises(ValueError):
+        mla.mla_cache_evict(s, FAKE, 1, 0, 0, torch.zeros(3, dtype=torch.int32), FAKE, FAKE, FAKE, 1,
+                            stream=0)
