@@ -653,9 +653,22 @@ __device__ __forceinline__ uint64_t tree_bits(const AttnArgs& a, int64_t b, int6
     nodes = m <= 0 ? 0ull : (m >= 64 ? ~0ull : (1ull << m) - 1ull);
     nodes &= n >= 64 ? ~0ull : (1ull << n) - 1ull;
   } else {
-    const uint8_t* row = a.tree + (b * a.n_q + i) * a.n_q + k0;
+    const uint8_t* row = a.tree + (b * a.n_q + i) * a.n_q;
+    if (((reinterpret_cast<uintptr_t>(a.tree) | (uintptr_t)a.n_q) & 3) == 0) {
+      // rows of whole words: four bytes at a time, each byte's "not 0" to a bit of a nibble
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (k0 >> 2);
+      const int skip = (int)(k0 & 3), words = (skip + n + 3) >> 2;
+#pragma unroll 4
+      for (int q = 0; q < words; ++q) {
+        const uint32_t nib = (__vsetne4(w[q], 0u) * 0x01020408u) >> 24 & 0xFu;
+        nodes |= q == 0 ? (uint64_t)(nib >> skip) : (uint64_t)nib << (4 * q - skip);
+      }
+      nodes &= n >= 64 ? ~0ull : (1ull << n) - 1ull;
+    } else {
+      row += k0;
 #pragma unroll 8
-    for (int e = 0; e < n; ++e) nodes |= (uint64_t)(row[e] != 0) << e;
+      for (int e = 0; e < n; ++e) nodes |= (uint64_t)(row[e] != 0) << e;
+    }
   }
   return bits | nodes << nctx;                 // nctx < 64 here
 }
