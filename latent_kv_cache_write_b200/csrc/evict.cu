@@ -9,10 +9,10 @@
 // the first hole).  The order of the rows does not matter to the attention: a cached key carries
 // its rotation, and the position array moves along.
 //
-// A block per sequence chooses the rows and lists the moves: the rows' ranks as 32-bit keys in shared
-// memory (up to KEYS_SH rows; longer contexts recompute them), a radix selection of the budget's
-// threshold, then ballots and scans that keep the rows' order.  It is bound by the latency of its
-// passes (8192 rows: about 10 us).  Where at most MOVE_HERE rows can move (accepted nodes, a full
+// A block per sequence chooses the rows and lists the moves: the rows' ranks as 32-bit keys (in
+// registers up to 8192 rows, then in shared memory), a radix selection of the budget's threshold,
+// then ballots and scans that keep the rows' order.  It is bound by its instructions (one SM per
+// sequence) and the latency of its passes.  Where at most MOVE_HERE rows can move (accepted nodes, a full
 // cache that drops a few rows per step) the block also moves them; otherwise a second launch lets the
 // whole GPU copy the listed rows, each read and written once (bound by HBM).
 #include "launch.h"
@@ -27,6 +27,7 @@ namespace {
 constexpr int NT = 1024;                    // threads of a planning block
 constexpr int NW = NT / 32;
 constexpr int KEYS_SH = 48 * 1024;          // keys kept in shared memory
+constexpr int HEAD = 8;                     // keys a thread holds in registers
 constexpr int MOVE_HERE = 128;              // rows a planning block moves itself
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -77,30 +78,32 @@ __device__ __forceinline__ uint32_t warp_offsets(uint32_t v, uint32_t* sums, uin
   return warp ? before : 0u;
 }
 
-// Rows listed in dst / src of one sequence, by `warps` warps of which this is number w: four rows'
-// vectors in flight per lane.
+// Rows listed in dst / src of one sequence, by `warps` warps of which this is number w: two rows at a
+// time, all vectors of both loaded before the first is stored (up to 128 of a row; compilers do not
+// move loads over stores, and one vector per row in flight left the copy waiting on latency).
 template <typename V>
 __device__ __forceinline__ void move_rows(V* rows, int per_row, float* weight, int32_t* position,
                                           const int32_t* dst, const int32_t* src, int n, int w,
                                           int warps) {
   const int lane = threadIdx.x & 31;
-  for (int k0 = 4 * w; k0 < n; k0 += 4 * warps) {
-    const V* from[4];
-    V* to[4];
+  for (int k0 = 2 * w; k0 < n; k0 += 2 * warps) {
+    const int k1 = k0 + 1 < n ? k0 + 1 : k0;           // (an odd last row twice: the same values)
+    const V* from[2] = {rows + (int64_t)src[k0] * per_row, rows + (int64_t)src[k1] * per_row};
+    V* to[2] = {rows + (int64_t)dst[k0] * per_row, rows + (int64_t)dst[k1] * per_row};
+    for (int c0 = lane; c0 < per_row; c0 += 128) {
+      V v[2][4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u < n ? k0 + u : n - 1;       // (the last row again: the same values)
-      from[u] = rows + (int64_t)src[k] * per_row;
-      to[u] = rows + (int64_t)dst[k] * per_row;
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c0 + 32 * q < per_row) v[u][q] = from[u][c0 + 32 * q];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c0 + 32 * q < per_row) to[u][c0 + 32 * q] = v[u][q];
     }
-    for (int c = lane; c < per_row; c += 32) {
-      V v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = from[u][c];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) to[u][c] = v[u];
-    }
-    if (lane < 4 && k0 + lane < n) {
+    if (lane < 2 && k0 + lane < n) {
       const int d = dst[k0 + lane], s = src[k0 + lane];
       if (weight) weight[d] = weight[s];
       if (position) position[d] = position[s];
@@ -131,16 +134,37 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
   int count = 0;                            // how many of them stay
   uint32_t thr = 0, ties = 0;
   const uint8_t* acc = a.accept ? a.accept + (int64_t)b * a.n_nodes : nullptr;
-  const bool held = n <= a.key_rows;        // their keys stay in shared memory
+  // A warp owns consecutive rows, 32 at a time, so that ballots keep their order.  Of up to HEAD * NT
+  // rows each thread holds the keys of its own in registers; more go through shared memory
+  // (key_rows of them), and past that are worked out again at each pass.
+  const bool small = n <= HEAD * NT, held = !acc && n <= a.key_rows;
+  const int per = small ? HEAD * 32 : ((n + NT - 1) / NT) * 32;
+  const int j0 = min(warp * per, n), j1 = min(j0 + per, n);
+  uint32_t k8[HEAD];
   int newest = INT32_MIN;
   auto rank_key = [&](int32_t p, float x) -> uint32_t {
     return p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent ? SAFE : weight_key(x);
   };
-  auto make_key = [&](int j) -> uint32_t {
+  auto make_key = [&](int j) -> uint32_t {  // accept: the node's byte
+    if (acc) return acc[j];
     const int64_t s = w.slot(j, a.S);
     return rank_key(pos[s], wt[s]);
   };
-  auto key = [&](int j) -> uint32_t { return held ? keys_sh[j] : make_key(j); };
+  // f(row, its key, whether it exists) for this lane's rows, the warp together; a row that does not
+  // exist has key 0
+  auto each = [&](auto&& f) {
+    if (small) {
+#pragma unroll
+      for (int u = 0; u < HEAD; ++u)
+        if (j0 + 32 * u < j1) f(j0 + 32 * u + lane, k8[u], j0 + 32 * u + lane < j1);
+    } else {
+#pragma unroll 2
+      for (int j = j0 + lane; j - lane < j1; j += 32) {
+        const bool in = j < j1;
+        f(j, in ? (held ? keys_sh[j] : make_key(j)) : 0u, in);
+      }
+    }
+  };
   auto finish = [&](int rows, int moves) {
     if (!MOVE) a.plan.count[b] = moves;
     a.window[3 * b] = w.first;
@@ -160,41 +184,44 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       safe_sh = 0u;
     }
     __syncthreads();
-    // the first HEAD rows of each thread with all loads in flight at once, the rest in turn
-    constexpr int HEAD = 8;
-    int32_t p8[HEAD];
-    float x8[HEAD];
+    // newest position, then the keys
     int mx = INT32_MIN;
-#pragma unroll
-    for (int u = 0; u < HEAD; ++u) {
-      const int j = t + u * NT;
-      const int64_t s = j < n ? w.slot(j, a.S) : 0;
-      p8[u] = j < n ? pos[s] : INT32_MIN;
-      x8[u] = j < n ? wt[s] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < HEAD; ++u) mx = max(mx, p8[u]);
-#pragma unroll 4
-    for (int j = t + HEAD * NT; j < n; j += NT) mx = max(mx, pos[w.slot(j, a.S)]);
-    mx = __reduce_max_sync(FULL, mx);
-    if (lane == 0) atomicMax(&newest_sh, mx);
-    __syncthreads();
-    newest = newest_sh;
     uint32_t safe = 0;
+    if (small) {
+      int32_t p8[HEAD];
+      float x8[HEAD];
 #pragma unroll
-    for (int u = 0; u < HEAD; ++u) {
-      const int j = t + u * NT;
-      if (j < n) {
-        const uint32_t k = rank_key(p8[u], x8[u]);
-        if (held) keys_sh[j] = k;
+      for (int u = 0; u < HEAD; ++u) {                 // all loads in flight at once
+        const int j = j0 + 32 * u + lane;
+        const int64_t s = j < j1 ? w.slot(j, a.S) : 0;
+        p8[u] = j < j1 ? pos[s] : INT32_MIN;
+        x8[u] = j < j1 ? wt[s] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < HEAD; ++u) mx = max(mx, p8[u]);
+      mx = __reduce_max_sync(FULL, mx);
+      if (lane == 0) atomicMax(&newest_sh, mx);
+      __syncthreads();
+      newest = newest_sh;
+#pragma unroll
+      for (int u = 0; u < HEAD; ++u) {
+        const bool in = j0 + 32 * u + lane < j1;
+        k8[u] = in ? rank_key(p8[u], x8[u]) : 0u;
+        safe += k8[u] == SAFE;
+      }
+    } else {
+#pragma unroll 4
+      for (int j = j0 + lane; j < j1; j += 32) mx = max(mx, pos[w.slot(j, a.S)]);
+      mx = __reduce_max_sync(FULL, mx);
+      if (lane == 0) atomicMax(&newest_sh, mx);
+      __syncthreads();
+      newest = newest_sh;
+#pragma unroll 4
+      for (int j = j0 + lane; j < j1; j += 32) {
+        const uint32_t k = make_key(j);
+        if (held) keys_sh[j] = k;                      // (read by this thread only)
         safe += k == SAFE;
       }
-    }
-#pragma unroll 4
-    for (int j = t + HEAD * NT; j < n; j += NT) {
-      const uint32_t k = make_key(j);
-      if (held) keys_sh[j] = k;
-      safe += k == SAFE;
     }
     safe = __reduce_add_sync(FULL, safe);
     if (lane == 0 && safe) atomicAdd(&safe_sh, safe);
@@ -214,11 +241,10 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
         __syncthreads();
         const int sh = shift[pass], above = sh + bits[pass];
         const uint32_t mask = (1u << bits[pass]) - 1u;
-#pragma unroll 4
-        for (int j = t; j < n; j += NT) {
-          const uint32_t k = key(j);
-          if (k != SAFE && (above == 32 || (k >> above) == prefix)) atomicAdd(&hist[(k >> sh) & mask], 1u);
-        }
+        each([&](int, uint32_t k, bool in) {
+          if (in && k != SAFE && (pass == 0 || (k >> above) == prefix))
+            atomicAdd(&hist[(k >> sh) & mask], 1u);
+        });
         __syncthreads();
         // warp v owns digits 2047 - 64 v .. : rows above each by a scan within the warp
         const int d0 = 2047 - 2 * t;
@@ -247,52 +273,55 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
     }
   }
 
-  // Each warp takes a run of consecutive rows, 32 at a time, so that ballots order them.
-  const int per = ((n + NT - 1) / NT) * 32;
-  const int j0 = min(warp * per, n), j1 = min(j0 + per, n);
+  // which rows stay: all above the threshold, and the first `ties` at it
   uint32_t tie0 = 0, total;
   if (a.accept) {
+    if (small) {
+#pragma unroll
+      for (int u = 0; u < HEAD; ++u) {
+        const int j = j0 + 32 * u + lane;
+        k8[u] = j < j1 ? acc[j] : 0u;
+      }
+    }
     uint32_t c = 0;
-    for (int j = j0; j < j1; j += 32) c += __popc(__ballot_sync(FULL, j + lane < j1 && acc[j + lane] != 0));
+    each([&](int, uint32_t k, bool) { c += __popc(__ballot_sync(FULL, k != 0u)); });
     warp_offsets(c, sums, &total);
     count = (int)total;
+    thr = 0u;
   } else if (count > 0) {
     uint32_t c = 0;
-    for (int j = j0; j < j1; j += 32) c += __popc(__ballot_sync(FULL, j + lane < j1 && key(j + lane) == thr));
+    each([&](int, uint32_t k, bool in) { c += __popc(__ballot_sync(FULL, in && k == thr)); });
     tie0 = warp_offsets(c, sums, &total);
+  } else {
+    thr = SAFE;                             // nothing stays
   }
-  // whether row j (this lane's of the 32 at hand) stays; `tie` counts threshold rows before the 32
-  auto stays = [&](int j, uint32_t& tie) -> bool {
-    const bool in = j < j1;
-    if (a.accept) return in && acc[j] != 0;
-    if (count == 0) return false;
-    const uint32_t k = in ? key(j) : 0u;
+  const unsigned below = (1u << lane) - 1u;
+  // whether a row stays; `tie` counts the threshold's rows before the 32 at hand
+  auto stays = [&](uint32_t k, bool in, uint32_t& tie) -> bool {
     const unsigned m = __ballot_sync(FULL, in && k == thr);
-    const uint32_t rank = tie + __popc(m & ((1u << lane) - 1u));
+    const bool s = in && (k > thr || (k == thr && tie + __popc(m & below) < ties));
     tie += __popc(m);
-    return in && (k == thr ? rank < ties : k > thr);
+    return s;
   };
   uint32_t holes = 0, late = 0, tie = tie0;
-  for (int j = j0; j < j1; j += 32) {
-    const bool s = stays(j + lane, tie), in = j + lane < j1;
-    holes += __popc(__ballot_sync(FULL, in && j + lane < count && !s));
-    late += __popc(__ballot_sync(FULL, j + lane >= count && s));
-  }
+  each([&](int j, uint32_t k, bool in) {
+    const bool s = stays(k, in, tie);
+    holes += __popc(__ballot_sync(FULL, in && j < count && !s));
+    late += __popc(__ballot_sync(FULL, j >= count && s));
+  });
   uint32_t n_move, n_late;
   uint32_t hole = warp_offsets(holes, sums, &n_move);
   uint32_t lt = warp_offsets(late, sums, &n_late);
   tie = tie0;
-  for (int j = j0; j < j1; j += 32) {
-    const bool s = stays(j + lane, tie), in = j + lane < j1;
-    const int32_t slot = in ? (int32_t)w.slot(base + j + lane, a.S) : 0;
-    const bool is_hole = in && j + lane < count && !s, is_late = j + lane >= count && s;
+  each([&](int j, uint32_t k, bool in) {
+    const bool s = stays(k, in, tie);
+    const bool is_hole = in && j < count && !s, is_late = j >= count && s;
     const unsigned mh = __ballot_sync(FULL, is_hole), ml = __ballot_sync(FULL, is_late);
-    const unsigned below = (1u << lane) - 1u;
-    if (is_hole) dst[hole + __popc(mh & below)] = slot;
-    if (is_late) src[lt + __popc(ml & below)] = slot;
+    if (is_hole) dst[hole + __popc(mh & below)] = (int32_t)w.slot(base + j, a.S);
+    if (is_late) src[lt + __popc(ml & below)] = (int32_t)w.slot(base + j, a.S);
     hole += __popc(mh);
     lt += __popc(ml);
-  }
+  });
   if (MOVE) {
     __syncthreads();                        // the list is complete
     move_rows(static_cast<V*>(a.cache) + (int64_t)b * a.S * a.per_row, a.per_row, wt, pos, dst, src,
@@ -315,17 +344,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
             (int)(gridDim.x * (blockDim.x / 32)));
 }
 
-template <typename V>
-cudaError_t run_as(const Geo& g, EvictArgs a, int64_t most, cudaStream_t st) {
-  if (most <= MOVE_HERE) {
-    // (the few rows' keys fit without opting in to more shared memory)
-    const int rows = a.accept ? 0 : (int)(g.S < 8192 ? g.S : 8192);
-    a.key_rows = rows;
-    cudaError_t e = launch_dependent(evict_plan_kernel<V, true>, (unsigned)g.B, NT,
-                                     (size_t)rows * 4, st, 1u, a);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
-  }
+template <typename V, bool MOVE>
+cudaError_t launch_plan(const Geo& g, EvictArgs& a, cudaStream_t st) {
   {
     // the shared-memory opt-in is per device
     static std::mutex mu;
@@ -335,20 +355,27 @@ cudaError_t run_as(const Geo& g, EvictArgs a, int64_t most, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !(done >> dev & 1)) {
-      e = cudaFuncSetAttribute(evict_plan_kernel<V, false>,
+      e = cudaFuncSetAttribute(evict_plan_kernel<V, MOVE>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, KEYS_SH * 4);
       if (e != cudaSuccess) return e;
       if (dev < 64) done |= 1ull << dev;
     }
   }
-  a.key_rows = a.accept ? 0 : (int)(g.S < KEYS_SH ? g.S : KEYS_SH);
-  cudaError_t e = launch_dependent(evict_plan_kernel<V, false>, (unsigned)g.B, NT,
-                                   (size_t)a.key_rows * 4, st, 1u, a);
+  // keys go to shared memory where a sequence can have more rows than the registers hold
+  a.key_rows = a.accept || g.S <= HEAD * NT ? 0 : (int)(g.S < KEYS_SH ? g.S : KEYS_SH);
+  const cudaError_t e = launch_dependent(evict_plan_kernel<V, MOVE>, (unsigned)g.B, NT,
+                                         (size_t)a.key_rows * 4, st, 1u, a);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+template <typename V>
+cudaError_t run_as(const Geo& g, EvictArgs a, int64_t most, cudaStream_t st) {
+  if (most <= MOVE_HERE) return launch_plan<V, true>(g, a, st);
+  cudaError_t e = launch_plan<V, false>(g, a, st);
   if (e != cudaSuccess) return e;
-  count_launches(1);
-  const unsigned x = (unsigned)((148 * 8 + g.B - 1) / g.B);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(x, (unsigned)g.B);
+  cfg.gridDim = dim3((unsigned)((148 * 8 + g.B - 1) / g.B), (unsigned)g.B);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at;

@@ -338,6 +338,7 @@ def _check_moved(ref, ct, win, wt, pos):
 @pytest.mark.parametrize("cfg", ["TINY", "ODD", "MAIN"])
 @pytest.mark.parametrize("n,S,windows", [
     (1, 9, [(0, 3, 1), (8, 0, 1), (4, 8, 1), (3, 9, 0)]),
+    (9000, 9100, [(9000, 80, 9000), (3, 100, 8192)]),
     (40, 101, [(90, 50, 40), (0, 0, 40), (7, 61, 40), (100, 1, 0), (-4, 500, 9), (3, 4, 99)]),
 ])
 @pytest.mark.parametrize("extra", [True, False])
@@ -364,6 +365,9 @@ EVICT = [
     (300, [(290, 300, 0), (4, 150, 0)], 60, 200, 500),          # more protected than kept
     (2600, [(2500, 2600, 0), (0, 2049, 0), (1, 1025, 0)], 1024, 0, 0),
     (5000, [(4000, 5000, 0), (0, 4999, 0)], 4990, 7, 100),
+    (8193, [(4000, 8193, 0), (0, 8192, 0), (7, 8191, 0)], 8100, 7, 100),
+    (20000, [(19000, 20000, 0), (0, 8193, 0)], 9000, 7, 5000),
+    (60000, [(59000, 60000, 0), (0, 40000, 0)], 20000, 1, 3),
 ]
 
 
