@@ -11,9 +11,13 @@
 // each CTA loads half: a lone CTA would need 128 rows x 64 dims for every 4 MMAs of M = N = 128,
 // 64 B/clk, and an SM's TMA loads deliver about 44.
 //   RES_K: the keys' tile (9 boxes of 128 rows x 64 dims, 144 KB) stays in shared memory while the
-//          rows stream past it in 4 stages.  MMA-bound: 4608 clk per 256 x 256 x 576 tile.
+//          rows stream past it in 4 stages.  A tile of 256 x 256 x 576 takes 6600 to 7200 clk, the
+//          rate that cuBLAS's bf16 GEMM reaches here; the rest of a call is the start (plan, first
+//          loads) and clusters with fewer units than others.  8 trees of up to 16 nodes, 128
+//          heads, over up to 4096 rows: 74 us against a floor of 48.
 //   RES_Q: at most 128 rows per sequence (single tokens, small trees): the rows stay and the keys
-//          stream, read once from HBM, which bounds it.
+//          stream, read once from HBM, which bounds it (5.9 TB/s in the steady state; 64
+//          sequences of 8191 rows, one token each: 122 us against a floor of 94).
 //   STREAM: d_R = 512 with more rows: 256 KB of keys do not fit, both operands stream.
 //
 // A cluster has one to four pairs.  It takes whole units (256 keys), and its pairs share the tiles of
