@@ -68,6 +68,14 @@ def check_attend(wl, qv, cv, windows, see, n, o, lse, fill=7.0):
                        ds + 2.0 ** -20 * (1 + np.abs(rl[b, :m][fin])) + (r + m) * T.F32, "lse")
 
 
+def weight_tolerance(q, rows, lse, n_heads):
+    """Relative: every term moves by exp(+- its score's error) and carries the exponential's 2^-21,
+    lse in log2 units rounds relative to itself, and the terms (all positive) add up in float32."""
+    lse = np.where(np.isfinite(lse), np.abs(lse), 0.0).max(initial=0)
+    return 2 * T.score_error(q, rows, SCALE) + 2.0 ** -20 + (len(q) * n_heads + 8) * T.F32 \
+        + 2.0 ** -23 * lse
+
+
 # configuration, nodes, ring, windows (first, rows, nodes) with lengths on and beside tile borders
 CASES = [
     ("TINY", 7, 64, [(0, 20, 7), (60, 57, 3), (5, 0, 7), (9, 64, 0), (63, 1, 1)]),
@@ -244,10 +252,79 @@ def test_attend_weight(cuda_ok, cfg, n, S, windows):
             assert (got[rest] == old[b, rest]).all(), "slots outside the window"
             if not at:
                 continue
-            ds = T.score_error(q.values[b], c.values[b, at], SCALE)
-            rel = 2 * ds + 2.0 ** -20 + (m * wl.n_heads + 8) * T.F32 \
-                + 2.0 ** -23 * np.abs(np.where(np.isfinite(lse32[b, :m]), lse32[b, :m], 0)).max(initial=0)
+            rel = weight_tolerance(q.values[b], c.values[b, at], lse32[b, :m], wl.n_heads)
             T.check_within(got[at], ref[b, at], rel * np.abs(ref[b, at]) + 1e-30, "weight")
+
+
+@pytest.mark.parametrize("B,n,S", [(700, 3, 150), (70, 20, 200), (33, 1, 1500)])
+def test_many_sequences(cuda_ok, B, n, S):
+    """More sequences than a warp has lanes, many of them empty or without nodes."""
+    wl = T.workload(T.MAIN, B, S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng([B, n])
+    windows = [(int(rng.integers(0, S)), int(rng.choice([0, rng.integers(0, S + 1)])),
+                int(rng.integers(0, n + 1))) for _ in range(B)]
+    windows = [(f, min(r, S - m), m) for f, r, m in windows]
+    q = T.normal(rng, (B, n, wl.n_heads, wl.row_width), wl.dtype)
+    c = T.normal(rng, (B, S, wl.row_width), wl.dtype)
+    _, see = T.random_tree(rng, B, n)
+    ct, qt = P.upload(c), P.upload(q)
+    o, lse = attend(wl, qt, ct, windows, tree_dev(see), n)
+    check_attend(wl, q.values, c.values, windows, see, n, o, lse)
+    wt = torch.zeros((B, S), device=DEV)
+    mla.mla_attend_weight(shape, qt, n, ct, i32(windows), tree_dev(see), SCALE, lse, None, None, wt)
+    assert mla.mla_device_error() == 0
+    l32 = P.download(lse)
+    ref = D.attend_weight(q.values, c.values, windows, see, SCALE, l32, None, None,
+                          np.zeros((B, S)))
+    got = P.download(wt)
+    for b, (f, r, m) in enumerate(windows):
+        if r + m:
+            rel = weight_tolerance(q.values[b], c.values[b, D.slots(f, r + m, S)], l32[b, :m],
+                                   wl.n_heads)
+            T.check_within(got[b], ref[b], rel * np.abs(ref[b]) + 1e-30, "weight")
+        else:
+            assert (got[b] == 0).all()
+
+
+def test_far_slots(cuda_ok):
+    """A ring of more than 2^31 elements: a step at its end gives the bits of a step at the end of a
+    short ring (neither splits a tile)."""
+    n, rows, far, near = 6, 400, 3_800_000, 1000
+    rng = np.random.default_rng(6)
+    _, see = T.random_tree(rng, 1, n)
+    acc = torch.tensor([[0, 1, 0, 0, 1, 1]], dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    rand = lambda *s: torch.randn(s, device=DEV, generator=g)
+    h, wd, wr = (rand(1, n, 256).bfloat16(), rand(256, 512).bfloat16() / 16,
+                 rand(256, 64).bfloat16() / 16)
+    q, tok, context = rand(1, n, 8, 576).bfloat16(), i32([[9, 9, 9, 10, 10, 11]]), \
+        rand(rows, 576).bfloat16()
+    results = []
+    for S in (far, near):
+        wl = T.workload(T.MAIN, 1, S)
+        shape = mla.make_shape(wl)
+        window = [(S - 20, rows, n)]
+        at = torch.tensor(D.slots(S - 20, rows + n, S), device=DEV)
+        ct = torch.empty((1, S, 576), device=DEV, dtype=torch.bfloat16)
+        ct[0, at[:rows]] = context
+        pos = torch.zeros((1, S), device=DEV, dtype=torch.int32)
+        pos[0, at[:rows]] = torch.arange(rows, device=DEV, dtype=torch.int32)
+        wt, win = torch.zeros((1, S), device=DEV), i32(window)
+        ws = torch.empty(mla.mla_cache_evict_workspace_size(shape), dtype=torch.uint8, device=DEV)
+        mla.mla_tree_write(shape, h, 256, n, win, tok, wd, wr, ct, pos)
+        o, lse = attend(wl, q, ct, window, tree_dev(see), n)
+        mla.mla_attend_weight(shape, q, n, ct, win, tree_dev(see), SCALE, lse, None, wt, wt)
+        one = [x[0, at].clone() for x in (ct, pos, wt)]
+        mla.mla_tree_accept(shape, ct, n, acc, win, wt, pos, ws)
+        mla.mla_cache_evict(shape, ct, 150, 4, 20, win, wt, pos, ws)
+        assert mla.mla_device_error() == 0
+        assert (win - i32([(S - 20, 150, 0)]) == 0).all()
+        results.append([o, lse] + one + [x[0, at[:150]].clone() for x in (ct, pos, wt)])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+    check_attend(T.workload(T.MAIN, 1, rows + n), P.download(q), P.download(results[0][2])[None],
+                 [(0, rows, n)], see, n, results[0][0], results[0][1])
 
 
 @pytest.mark.parametrize("cfg,n,S,windows", [
@@ -257,6 +334,11 @@ def test_attend_weight(cuda_ok, cfg, n, S, windows):
     ("MAIN", 30, 100, [(95, 50, 30)] * 5 + [(1, 2, 17)] * 4 + [(0, 0, 0)]),
     ("VIDEO", 7, 100, [(95, 50, 7), (1, 2, 3)]),
     ("WIDE", 7, 100, [(95, 50, 7), (1, 2, 3)]),
+    # K split 8, 3 and 4 ways (1, 8 and 20 tiles of rows; the last in several turns), and wide
+    ("DEEP", 7, 100, [(95, 50, 7), (1, 2, 3)]),
+    ("DEEP", 30, 100, [(95, 50, 30), (0, 80, 30), (7, 0, 11)] * 11 + [(1, 2, 30)]),
+    ("DEEP", 32, 100, [(95, 50, 32), (0, 80, 30), (7, 0, 11), (1, 2, 31)] * 20),
+    ("WIDE_DEEP", 7, 100, [(95, 50, 7), (1, 2, 3)]),
 ])
 def test_place(cuda_ok, cfg, n, S, windows):
     """tree_write and tree_absorb_q: own positions, own slots, nothing past the nodes."""
@@ -452,7 +534,10 @@ def test_serving_steps(cuda_ok, cfg):
         mla.mla_attend_weight(shape, qa, n, ct, win, tree_dev(see), SCALE, lse, at.float(), wd, wd)
         ref = D.attend_weight(qv, cv, windows, see, SCALE, l_now, acc.astype(float), w_before,
                               w_before)
-        np.testing.assert_allclose(P.download(wd), ref, rtol=2e-2 if wl.dtype == "bf16" else 1e-4)
+        for b in range(B):
+            at_b = D.slots(windows[b, 0], windows[b, 1] + windows[b, 2], S)
+            rel = weight_tolerance(qv[b], cv[b, at_b], l_now[b, :windows[b, 2]], wl.n_heads)
+            T.check_within(P.download(wd)[b], ref[b], rel * np.abs(ref[b]) + 1e-30, "weight")
         w_now, p_now = P.download(wd), pd.cpu().numpy()
         mla.mla_tree_accept(shape, ct, n, at, win, wd, pd, ews)
         r1 = D.tree_accept(cv, windows, w_now, p_now, acc)

@@ -18,6 +18,8 @@ MAIN = dict(dtype="bf16", n_heads=8, d_nope=128, d_latent=512, d_rope=64, rope_p
 HEADS = dict(MAIN, n_heads=128)
 VIDEO = dict(MAIN, n_heads=32, rope_pairs=(8, 12, 12), grid_h=6, grid_w=11)
 WIDE = dict(MAIN, d_rope=512, rope_pairs=(64, 96, 96), grid_h=5, grid_w=9)
+DEEP = dict(VIDEO, n_heads=2, d_model=2304)          # a long K loop, split over several SMs
+WIDE_DEEP = dict(WIDE, n_heads=2, d_model=2304)
 
 
 def workload(cfg, batch, S) -> C.Workload:
