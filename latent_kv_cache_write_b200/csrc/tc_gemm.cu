@@ -29,9 +29,10 @@ constexpr int B_BYTES = GBN * GBK * 2;           // 16 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int MAX_PAIRS = 512;                   // RoPE pairs with a table entry (d_R <= 1024)
 constexpr int STG_BYTES = 32 * 64;                // per epilogue warp: 32 rows x 32 cols bf16
-constexpr int RB_BYTES = GBM * GBN * 4;          // split-K partial accumulator, 64 KB
+constexpr int RB_BYTES = GBM * GBN * 4;          // split-K partials; KS - 1 of 128 / KS columns
 // Shared memory: the stage ring, barriers, the RoPE frequency table, epilogue staging and,
-// with split-K, the buffer the other CTA of the pair sends its fp32 partial tile into.
+// with split-K, the buffer the cluster's other CTAs send their fp32 partials of this one's columns
+// into.
 constexpr int OBOX_BYTES = GBM * 64 * 2;         // TMA-store box: 128 rows x 64 cols bf16
 template <int ST, bool SK> struct GLay {
   static constexpr int OFF_TAB = ST * STAGE_BYTES + 256;
@@ -60,16 +61,17 @@ struct TcGemm {
   const int32_t* token;
   const int32_t* window;
   int32_t* position;
+  int ks;                   // split-K: CTAs per tile
   unsigned int* err;
 };
 
 // GSTAGES-deep TMA ring.  Four stages (one CTA per SM) suit long K loops; two stages let
 // two CTAs share an SM, which hides the latency of short-K tiles (the absorption).
-// SPLITK: launched in clusters of two CTAs that share each tile, rank r taking half of
-// the K blocks; rank 1 sends its fp32 accumulator to rank 0 through distributed shared
-// memory (st.async, completion counted in bytes) and rank 0 adds it before the epilogue.
-// For few tiles with long K (the cache write: 65 tiles of K = 4096) it brings twice the
-// SMs' load bandwidth to the same tiles.
+// SPLITK: launched in clusters of p.ks CTAs that share each tile, rank r taking the r-th part of
+// the K blocks.  For few tiles with long K (the cache write: 65 tiles of K = 4096) that brings
+// more SMs' load bandwidth to the same tiles.  Each rank finishes a part of the tile's columns, in
+// chunks of 8: the others send it their fp32 sums of those through distributed shared memory
+// (st.async, completion counted in bytes), and it adds them to its own, the lower ranks' first.
 template <int GSTAGES, bool SPLITK>
 __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -82,8 +84,8 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
   uint64_t* empty = full + GSTAGES;
   uint64_t* accf = empty + GSTAGES;              // accumulator ready [2]
   uint64_t* acce = accf + 2;                     // accumulator drained [2]
-  uint64_t* rbf = acce + 2;                      // split-K: partial landed (rank 0, tx bytes)
-  uint64_t* rbe = acce + 3;                      // split-K: rank 0 has read it (rank 1)
+  uint64_t* rbf = acce + 2;                      // split-K: partials landed (tx bytes)
+  uint64_t* rbe = acce + 3;                      // split-K: the others have read this rank's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 4);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   using GL = GLay<GSTAGES, SPLITK>;
@@ -93,12 +95,13 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
   const int nm = (p.M + GBM - 1) / GBM, nn = (p.N + GBN - 1) / GBN;
   const int ntiles = nm * nn * p.Z;
   const int nk = (p.K + GBK - 1) / GBK;
-  // tiles this CTA (or CTA pair) walks, and its K blocks
+  // tiles this CTA (or cluster) walks, and its K blocks
   const uint32_t crank = SPLITK ? cluster_ctarank() : 0u;
-  const int t_first = SPLITK ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int t_step = SPLITK ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-  const int kb0 = SPLITK && crank ? nk / 2 : 0;
-  const int kb1 = SPLITK && !crank ? nk / 2 : nk;
+  const int ks = SPLITK ? p.ks : 1;
+  const int t_first = (int)blockIdx.x / ks;
+  const int t_step = (int)gridDim.x / ks;
+  const int kb0 = nk * (int)crank / ks;
+  const int kb1 = nk * ((int)crank + 1) / ks;
 
   if (tid == 0) {
     for (int s = 0; s < GSTAGES; ++s) {
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
       mbar_init(&acce[a], 128);
     }
     mbar_init(rbf, 1);
-    mbar_init(rbe, 1);
+    mbar_init(rbe, ks > 1 ? ks - 1 : 1);
     *abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
     inv_freq[q] = rope_inv_freq(p.geo, q);
   tc_fence_before();
   __syncthreads();
-  if constexpr (SPLITK) cluster_sync();        // the pair's barriers exist before any remote use
+  if constexpr (SPLITK) cluster_sync();        // the cluster's barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();                               // the previous kernel's outputs are visible
@@ -186,12 +189,12 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
           const uint64_t da = desc_sw128(a, 16, 1024);
           const uint64_t db = p.b_mn ? desc_sw128(b, B_BYTES / 2, 1024) : desc_sw128(b, 16, 1024);
 #pragma unroll
-          for (int ks = 0; ks < GBK / 16; ++ks) {
+          for (int k16 = 0; k16 < GBK / 16; ++k16) {
             // K-major operands advance 32 bytes per 16-element K step inside the swizzle
             // atom; the MN-major B advances 16 rows of 128 bytes.
-            const uint64_t bstep = p.b_mn ? (uint64_t)(ks * 2048 >> 4) : (uint64_t)(ks * 32 >> 4);
-            mma_ss(d, da + (uint64_t)(ks * 32 >> 4), db + bstep, idesc,
-                   (kb != kb0 || ks != 0) ? 1u : 0u);
+            const uint64_t bstep = p.b_mn ? (uint64_t)(k16 * 2048 >> 4) : (uint64_t)(k16 * 32 >> 4);
+            mma_ss(d, da + (uint64_t)(k16 * 32 >> 4), db + bstep, idesc,
+                   (kb != kb0 || k16 != 0) ? 1u : 0u);
           }
           mma_commit(&empty[s]);
         }
@@ -210,47 +213,23 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const Geo& G = p.geo;
     uint8_t* stg = smem + GL::OFF_STG + (warp - 2) * STG_BYTES;
-    // split-K partial tile, chunk-major [32 chunks of 4 floats][128 rows]: conflict-free
-    // for both the sending and the reading thread of a row
+    // split-K partials, [rank][8-column chunk][2][128 rows] of 4 floats: conflict-free for both the
+    // sending and the reading thread of a row
     const float4* rb = reinterpret_cast<const float4*>(smem + GL::OFF_RB) + r;
+    const uint32_t rb_addr = smem_u32(rb), rbf_addr = smem_u32(rbf);
     uint32_t tc = 0, ost = 0;                   // ost: output boxes stored so far
     for (int t = t_first; t < ntiles; t += t_step, ++tc) {
       int m0, n0, z;
       tile_coords(t, m0, n0, z);
       const int acc = tc & 1;
-      if constexpr (SPLITK) {
-        if (crank == 1) {
-          // drain this CTA's half-K accumulator into rank 0's buffer once rank 0 has read
-          // the previous tile's
-          bool okr = __all_sync(0xffffffffu, mbar_wait(&accf[acc], (tc >> 1) & 1, abort, p.err,
-                                                         0x15, (r << 16) | tc));
-          if (okr)
-            okr = __all_sync(0xffffffffu, mbar_wait_cluster(rbe, (tc & 1) ^ 1, abort, p.err,
-                                                             0x16, (r << 16) | tc));
-          tc_fence_after();
-          const uint32_t trow = tmem + lane_base + acc * GBN;
-          const uint32_t dst = mapa(smem_u32(smem + GL::OFF_RB), 0) + (uint32_t)r * 16;
-          const uint32_t dbar = mapa(smem_u32(rbf), 0);
-          for (int c0 = 0; c0 < GBN; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(trow + c0, v);
-            tmem_wait_ld();
-            if (c0 + 32 == GBN) {
-              tc_fence_before();
-              mbar_arrive(&acce[acc]);          // accumulator may be overwritten
-            }
-            if (!okr) continue;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              st_async_v4(dst + (uint32_t)(c0 / 4 + q) * (GBM * 16), v[4 * q], v[4 * q + 1],
-                          v[4 * q + 2], v[4 * q + 3], dbar);
-          }
-          if (!okr) break;
-          continue;
-        }
-        // rank 0: the partial of this tile lands in its buffer (armed here, per tile)
-        if (r == 0) mbar_expect_tx(rbf, RB_BYTES);
-      }
+      const uint32_t trow = tmem + lane_base + acc * GBN;
+      // split-K: this rank finishes chunks [own0, own1) of the tile's nch
+      const int nch = p.N - n0 < GBN ? (p.N - n0) / 8 : GBN / 8;
+      const int own0 = nch * (int)crank / ks, own1 = nch * ((int)crank + 1) / ks;
+      const int mrows = p.M - m0 < GBM ? p.M - m0 : GBM;
+      bool ok = true;
+      // (armed per tile)
+      if (SPLITK && r == 0) mbar_expect_tx(rbf, (uint32_t)((ks - 1) * mrows * (own1 - own0) * 32));
       const int64_t m = m0 + r;
       const bool row_ok = m < p.M;
       // the absorption's share of RoPE(q_R) for this row: its loads are issued before the
@@ -288,7 +267,7 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
               g = p.token[m];
               const int64_t at = b * G.S + w.slot(w.rows + i, G.S);
               base = at * G.row;
-              if (p.position && n0 == 0) p.position[at] = (int32_t)g;
+              if (p.position && n0 == 0 && crank == 0) p.position[at] = (int32_t)g;
             }
           }
         }
@@ -298,15 +277,111 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
       } else {
         base = (m * G.H + z) * G.Dn;
       }
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&accf[acc], (tc >> 1) & 1, abort, p.err,
-                                                   0x13, (r << 16) | tc));
+      ok = __all_sync(0xffffffffu, mbar_wait(&accf[acc], (tc >> 1) & 1, abort, p.err, 0x13,
+                                             (r << 16) | tc));
+      // nq chunks of 8 columns from column n on: the rotation, bf16, the ring
+      auto store_cols = [&](float (&f)[32], int n, int nq) {
+        if (p.mode == MODE_CACHE && n >= p.n_split && row_ok) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            if (j >= 8 * nq) break;
+            const int q = (n + j - p.n_split) / 2;
+            rope_rotate_fast(f[j], f[j + 1], rope_axis_pos(G, ax, q), inv_freq[q]);
+          }
+        }
+        uint4* srow = reinterpret_cast<uint4*>(stg + lane * 64);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          srow[q ^ ((lane >> 1) & 3)] = make_uint4(
+              pack_bf16(f[8 * q + 0], f[8 * q + 1]), pack_bf16(f[8 * q + 2], f[8 * q + 3]),
+              pack_bf16(f[8 * q + 4], f[8 * q + 5]), pack_bf16(f[8 * q + 6], f[8 * q + 7]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + (lane >> 2), j = lane & 3;        // row of the warp, chunk
+          const int64_t rbase = __shfl_sync(0xffffffffu, base, rr);
+          if (m0 + (warp & 3) * 32 + rr < p.M && rbase >= 0 && j < nq) {
+            const uint4 w = reinterpret_cast<const uint4*>(stg + rr * 64)[j ^ ((rr >> 1) & 3)];
+            *reinterpret_cast<uint4*>(p.out + rbase + n + 8 * j) = w;
+          }
+        }
+        __syncwarp();
+      };
       if constexpr (SPLITK) {
+        // send the others' columns once they have read the previous tile's
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(rbe, (tc & 1) ^ 1, abort, p.err, 0x16,
+                                                         (r << 16) | tc));
+        tc_fence_after();
+        for (int c0 = 0; c0 < GBN / 8; c0 += 4) {
+          uint32_t v[32];
+          tmem_ld32(trow + c0 * 8, v);
+          tmem_wait_ld();
+          if (!ok || !row_ok) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = c0 + q;
+            const int d = ((c + 1) * ks - 1) / nch;          // the rank that finishes chunk c
+            if (c >= nch || d == (int)crank) continue;
+            const int d0 = nch * d / ks, dn = nch * (d + 1) / ks - d0;
+            const int from = (int)crank - ((int)crank > d);
+            const uint32_t dst = mapa(rb_addr, d) + (uint32_t)((from * dn + c - d0) * 2 * GBM) * 16;
+            const uint32_t dbar = mapa(rbf_addr, d);
+            st_async_v4(dst, v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3], dbar);
+            st_async_v4(dst + GBM * 16, v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7],
+                        dbar);
+          }
+        }
         if (ok)
           ok = __all_sync(0xffffffffu, mbar_wait_cluster(rbf, tc & 1, abort, p.err, 0x17,
                                                          (r << 16) | tc));
+        if (!ok) break;
+        for (int c0 = own0; c0 < own1; c0 += 4) {
+          const int nq = own1 - c0 < 4 ? own1 - c0 : 4;
+          uint32_t v[4][8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < nq) tmem_ld8(trow + (c0 + q) * 8, v[q]);
+          tmem_wait_ld();
+          if (c0 + 4 >= own1) {
+            tc_fence_before();
+            mbar_arrive(&acce[acc]);            // accumulator may be overwritten
+          }
+          float f[32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[8 * q + j] = 0.f;
+            if (q >= nq) continue;
+            bool own = false;
+            for (int k = 0; k < ks; ++k) {
+              if (k == (int)crank) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[8 * q + j] += __uint_as_float(v[q][j]);
+                own = true;
+                continue;
+              }
+              const float4* o = rb + ((k - own) * (own1 - own0) + c0 - own0 + q) * 2 * GBM;
+              const float4 lo = o[0], hi = o[GBM];
+              f[8 * q] += lo.x;
+              f[8 * q + 1] += lo.y;
+              f[8 * q + 2] += lo.z;
+              f[8 * q + 3] += lo.w;
+              f[8 * q + 4] += hi.x;
+              f[8 * q + 5] += hi.y;
+              f[8 * q + 6] += hi.z;
+              f[8 * q + 7] += hi.w;
+            }
+          }
+          store_cols(f, n0 + c0 * 8, nq);
+        }
+        // every partial is read (its sums have been stored): the others may send the next tile's
+        named_bar(1, 128);
+        if (r < ks && r != (int)crank) mbar_arrive_cluster_relaxed(mapa(smem_u32(rbe), r));
+        if (row_ok && n0 == 0 && crank == 0 && p.slots) p.slots[m] = (int32_t)(g % G.S);
+        continue;
       }
       tc_fence_after();
-      const uint32_t trow = tmem + lane_base + acc * GBN;
       // two 32-column TMEM loads in flight per wait
       for (int c0 = 0; c0 < GBN; c0 += 64) {
         uint32_t v[2][32];
@@ -317,7 +392,7 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
           tc_fence_before();
           mbar_arrive(&acce[acc]);              // accumulator may be overwritten
         }
-        if (!SPLITK && p.mode != MODE_CACHE) {
+        if (p.mode != MODE_CACHE) {
           // The absorption's and the up-projection's outputs are plain 3-D tensors: the
           // warps fill one 128-row x 64-column box (128-byte swizzle) of a two-buffer
           // ring and one thread stores it with TMA, which writes the rows whole.
@@ -353,47 +428,8 @@ __global__ void __launch_bounds__(GTHREADS, GSTAGES == 2 ? 2 : 1)
           float f[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[hh][j]);
-          if constexpr (SPLITK) {
-            // plus the other half of K, from the pair's rank 1
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 o = rb[((c0 + 32 * hh) / 4 + q) * GBM];
-              f[4 * q] += o.x;
-              f[4 * q + 1] += o.y;
-              f[4 * q + 2] += o.z;
-              f[4 * q + 3] += o.w;
-            }
-          }
-          if (p.mode == MODE_CACHE && n >= p.n_split && row_ok) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const int q = (n + j - p.n_split) / 2;
-              rope_rotate_fast(f[j], f[j + 1], rope_axis_pos(G, ax, q), inv_freq[q]);
-            }
-          }
-          uint4* srow = reinterpret_cast<uint4*>(stg + lane * 64);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            srow[q ^ ((lane >> 1) & 3)] = make_uint4(
-                pack_bf16(f[8 * q + 0], f[8 * q + 1]), pack_bf16(f[8 * q + 2], f[8 * q + 3]),
-                pack_bf16(f[8 * q + 4], f[8 * q + 5]), pack_bf16(f[8 * q + 6], f[8 * q + 7]));
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), j = lane & 3;      // row of the warp, chunk
-            const int64_t rbase = __shfl_sync(0xffffffffu, base, rr);
-            if (m0 + (warp & 3) * 32 + rr < p.M && rbase >= 0) {
-              const uint4 w = reinterpret_cast<const uint4*>(stg + rr * 64)[j ^ ((rr >> 1) & 3)];
-              *reinterpret_cast<uint4*>(p.out + rbase + n + 8 * j) = w;
-            }
-          }
-          __syncwarp();
+          store_cols(f, n, 4);
         }
-      }
-      if constexpr (SPLITK) {
-        // every row of the partial is read: rank 1 may send the next tile's
-        named_bar(1, 128);
-        if (r == 0) mbar_arrive_cluster_relaxed(mapa(smem_u32(rbe), 1));
       }
       if (ok && row_ok && n0 == 0 && p.mode == MODE_CACHE && p.slots)
         p.slots[m] = (int32_t)(g % G.S);
@@ -450,6 +486,34 @@ int sm_count() {
   return n;
 }
 
+// Split-K clusters of ks CTAs that can be resident at once on the current device (0: error).
+int split_clusters(int ks) {
+  using GL = GLay<4, true>;
+  static std::mutex mu;
+  static int cached[64][9] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && cached[dev][ks] > 0) return cached[dev][ks];
+  if (cudaFuncSetAttribute(tc_gemm_kernel<4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           GL::SMEM) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ks * sm_count()));
+  cfg.blockDim = dim3(GTHREADS);
+  cfg.dynamicSmemBytes = GL::SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_kernel<4, true>, &cfg) != cudaSuccess) return 0;
+  if (dev < 64) cached[dev][ks] = n;
+  return n;
+}
+
 template <int ST, bool SK>
 cudaError_t launch_st(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B2,
                       const CUtensorMap& O, const TcGemm& q, long long tiles, cudaStream_t st) {
@@ -477,12 +541,12 @@ cudaError_t launch_st(const CUtensorMap& A, const CUtensorMap& B, const CUtensor
                                      1u, A, B, B2, O, q);
     if (e != cudaSuccess) return e;
   } else {
-    // clusters of two CTAs, one cluster per tile up to one per SM pair
-    const long long pairs = sm_count() / 2;
-    const int nclu = (int)(tiles < pairs ? tiles : pairs);
+    // one cluster per tile up to what the GPU holds
+    const long long most = q.ks == 2 ? sm_count() / 2 : split_clusters(q.ks);
+    const int nclu = (int)(tiles < most ? tiles : most);
     if (nclu == 0) return cudaSuccess;
-    cudaError_t e = launch_dependent(tc_gemm_kernel<ST, SK>, (unsigned)(2 * nclu), GTHREADS,
-                                     GL::SMEM, st, 2u, A, B, B2, O, q);
+    cudaError_t e = launch_dependent(tc_gemm_kernel<ST, SK>, (unsigned)(q.ks * nclu), GTHREADS,
+                                     GL::SMEM, st, (unsigned)q.ks, A, B, B2, O, q);
     if (e != cudaSuccess) return e;
   }
   cudaError_t e = cudaGetLastError();
@@ -502,9 +566,29 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap
   // whole non-absorbed call, while the up-projection measured slower that way)
   if (p.mode == MODE_ABSORB || p.mode == MODE_MAT)
     return launch_st<2, false>(A, B, B2, O, q, tiles, st);
-  // fewer tiles than SMs and a long K loop (the cache write): split K over CTA pairs
-  if (p.mode == MODE_CACHE && nk >= 2 && tiles < sm_count())
+  // Fewer tiles than SMs and a long K loop (the cache write): split K over CTA pairs; draft nodes'
+  // rows, mostly a few tiles, over the number of CTAs with the shortest sequence of K blocks, a turn
+  // after the first costing some 8 more, while each keeps a ring's worth.  Measured, us by 2 CTAs
+  // / by the rule's, K = 4096, d_R = 64: 32 rows 16.0 / 8.6 (8 CTAs), 384 rows 16.3 / 11.0 (8), 1024
+  // rows 17.6 / 14.7 (3).
+  if (p.mode == MODE_CACHE && nk >= 2 && tiles < sm_count()) {
+    q.ks = 2;
+    if (p.window) {
+      long long best = 0;
+      for (int k : {2, 3, 4, 6, 8}) {
+        if (k > 2 && nk < 4 * k) break;
+        const long long at_once = k == 2 ? sm_count() / 2 : split_clusters(k);
+        if (at_once == 0) continue;
+        const long long turns = (tiles + at_once - 1) / at_once;
+        const long long cost = turns * ((nk + k - 1) / k) + 8 * (turns - 1);
+        if (best == 0 || cost < best) {
+          best = cost;
+          q.ks = k;
+        }
+      }
+    }
     return launch_st<4, true>(A, B, B2, O, q, tiles, st);
+  }
   return launch_st<4, false>(A, B, B2, O, q, tiles, st);
 }
 
