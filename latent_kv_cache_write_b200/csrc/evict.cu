@@ -29,7 +29,7 @@ namespace {
 constexpr int NT = 1024;                    // threads of a planning block
 constexpr int NW = NT / 32;
 constexpr int KEYS_SH = 48 * 1024;          // keys kept in shared memory
-constexpr int HEAD = 8;                     // keys a thread holds in registers
+constexpr int HEAD = 8192 / NT;             // keys a thread holds in registers
 constexpr int MOVE_HERE = 128;              // rows a planning block moves itself
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -63,21 +63,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 constexpr uint32_t SAFE = 0xFFFFFFFFu;      // protected rows (+inf is 0xFF800000)
 
-// Warp w's count -> the sum over the warps before it; *total: over all.  `sums`: one word per warp.
-__device__ __forceinline__ uint32_t warp_offsets(uint32_t v, uint32_t* sums, uint32_t* total) {
+// Warp w's count -> the sum over the warps before it; *total: over all.  `sums`: one per warp, for
+// this call alone.
+template <typename T>
+__device__ __forceinline__ T warp_offsets(T v, T* sums, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) sums[warp] = v;
   __syncthreads();
-  uint32_t x = sums[lane];
+  T x = lane < NW ? sums[lane] : 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(FULL, x, o);
+  for (int o = 1; o < NW; o <<= 1) {
+    const T y = __shfl_up_sync(FULL, x, o);
     if (lane >= o) x += y;
   }
-  *total = __shfl_sync(FULL, x, 31);
-  const uint32_t before = __shfl_sync(FULL, x, warp ? warp - 1 : 0);
-  __syncthreads();
-  return warp ? before : 0u;
+  *total = __shfl_sync(FULL, x, NW - 1);
+  const T before = __shfl_sync(FULL, x, warp ? warp - 1 : 0);
+  return warp ? before : 0;
 }
 
 // Rows listed in dst / src of one sequence, by `warps` warps of which this is number w: two rows at a
@@ -116,13 +117,21 @@ __device__ __forceinline__ void move_rows(V* rows, int per_row, float* weight, i
 template <typename V, bool MOVE>
 __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t keys_sh[];     // [key_rows]
-  __shared__ uint32_t hist[2048];
-  __shared__ uint32_t sums[32];
-  __shared__ uint32_t pick[2];              // chosen digit, rows still to take inside it
+  // of each pass: the digits' counts; chosen digit, rows still to take inside it, its rows
+  __shared__ uint32_t hist[3][2048];
+  __shared__ uint32_t pick[3][3];
+  __shared__ uint32_t sums[4][NW];
+  __shared__ uint64_t sums2[NW];
   __shared__ int newest_sh;
   __shared__ uint32_t safe_sh;
   __shared__ int32_t list[MOVE ? 2 * MOVE_HERE : 1];
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (!a.accept)
+    for (int q = t; q < 3 * 2048; q += NT) hist[q / 2048][q % 2048] = 0u;
+  if (t == 0) {
+    newest_sh = INT32_MIN;
+    safe_sh = 0u;
+  }
   tc::grid_dep_wait();                      // the previous kernel's outputs are visible
   tc::grid_dep_launch();
   const Window w = load_window(a.window, b, a.S, a.accept ? a.n_nodes : a.S);
@@ -134,7 +143,10 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
   const int base = a.accept ? w.rows : 0;   // logical rows considered: base .. base + n - 1
   const int n = a.accept ? w.nodes : w.rows;
   int count = 0;                            // how many of them stay
+  // the rows whose key is above thr stay, and `ties` of those at it, the lowest; or, if all_at, all
+  // whose key is at least thr
   uint32_t thr = 0, ties = 0;
+  bool all_at = false;
   const uint8_t* acc = a.accept ? a.accept + (int64_t)b * a.n_nodes : nullptr;
   // A warp owns consecutive rows, 32 at a time, so that ballots keep their order.  Of up to HEAD * NT
   // rows each thread holds the keys of its own in registers; more go through shared memory
@@ -143,9 +155,9 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
   const int per = small ? HEAD * 32 : ((n + NT - 1) / NT) * 32;
   const int j0 = min(warp * per, n), j1 = min(j0 + per, n);
   uint32_t k8[HEAD];
-  int newest = INT32_MIN;
+  int64_t recent = INT64_MAX;               // positions past it are protected
   auto rank_key = [&](int32_t p, float x) -> uint32_t {
-    return p < a.n_sink || (int64_t)p > (int64_t)newest - a.n_recent ? SAFE : weight_key(x);
+    return p < a.n_sink || p > recent ? SAFE : weight_key(x);
   };
   auto make_key = [&](int j) -> uint32_t {  // accept: the node's byte
     if (acc) return acc[j];
@@ -181,14 +193,15 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       return;
     }
     count = (int)a.n_keep;
-    if (t == 0) {
-      newest_sh = INT32_MIN;
-      safe_sh = 0u;
-    }
     __syncthreads();
-    // newest position, then the keys
+    // newest position, then the keys and the counts of their first digit
+    const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
     int mx = INT32_MIN;
     uint32_t safe = 0;
+    auto first_digit = [&](uint32_t k, bool in) {
+      safe += in && k == SAFE;
+      if (in && k != SAFE) atomicAdd(&hist[0][k >> shift[0]], 1u);
+    };
     if (small) {
       int32_t p8[HEAD];
       float x8[HEAD];
@@ -204,12 +217,12 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       mx = __reduce_max_sync(FULL, mx);
       if (lane == 0) atomicMax(&newest_sh, mx);
       __syncthreads();
-      newest = newest_sh;
+      recent = (int64_t)newest_sh - a.n_recent;
 #pragma unroll
       for (int u = 0; u < HEAD; ++u) {
         const bool in = j0 + 32 * u + lane < j1;
         k8[u] = in ? rank_key(p8[u], x8[u]) : 0u;
-        safe += k8[u] == SAFE;
+        first_digit(k8[u], in);
       }
     } else {
 #pragma unroll 4
@@ -217,12 +230,12 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       mx = __reduce_max_sync(FULL, mx);
       if (lane == 0) atomicMax(&newest_sh, mx);
       __syncthreads();
-      newest = newest_sh;
+      recent = (int64_t)newest_sh - a.n_recent;
 #pragma unroll 4
       for (int j = j0 + lane; j < j1; j += 32) {
         const uint32_t k = make_key(j);
         if (held) keys_sh[j] = k;                      // (read by this thread only)
-        safe += k == SAFE;
+        first_digit(k, true);
       }
     }
     safe = __reduce_add_sync(FULL, safe);
@@ -232,51 +245,60 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
     if (count > 0 && safe >= (uint32_t)count) {
       thr = SAFE;                           // protected rows alone fill the budget
       ties = (uint32_t)count;
+      all_at = safe == ties;
     } else if (count > 0) {
       // the largest key such that `take` rows below SAFE reach it, 11 + 11 + 10 bits at a time (11
-      // bits take the exponent and two mantissa bits at once: weights crowd in few exponents)
+      // bits take the exponent and two mantissa bits at once: weights crowd in few exponents);
+      // done once all rows of the chosen digit stay, as a rule after two passes
       uint32_t prefix = 0, take = (uint32_t)count - safe;
-      const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
-        for (int q = t; q < 2048; q += NT) hist[q] = 0u;
-        __syncthreads();
         const int sh = shift[pass], above = sh + bits[pass];
         const uint32_t mask = (1u << bits[pass]) - 1u;
-        each([&](int, uint32_t k, bool in) {
-          if (in && k != SAFE && (pass == 0 || (k >> above) == prefix))
-            atomicAdd(&hist[(k >> sh) & mask], 1u);
-        });
-        __syncthreads();
-        // warp v owns digits 2047 - 64 v .. : rows above each by a scan within the warp
-        const int d0 = 2047 - 2 * t;
-        const uint32_t h0 = hist[d0], h1 = hist[d0 - 1];
-        uint32_t x = h0 + h1;
+        if (pass > 0) {
+          each([&](int, uint32_t k, bool in) {
+            if (in && k != SAFE && (k >> above) == prefix)
+              atomicAdd(&hist[pass][(k >> sh) & mask], 1u);
+          });
+          __syncthreads();
+        }
+        // a thread owns PT digits from 2047 - PT t down: rows above each by a scan
+        constexpr int PT = 2048 / NT;
+        uint32_t h[PT], mine = 0;
+#pragma unroll
+        for (int q = 0; q < PT; ++q) {
+          h[q] = hist[pass][2047 - PT * t - q];
+          mine += h[q];
+        }
+        uint32_t x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t y = __shfl_up_sync(FULL, x, o);
           if (lane >= o) x += y;
         }
         uint32_t all;
-        const uint32_t before =
-            warp_offsets(__shfl_sync(FULL, x, 31), sums, &all) + x - (h0 + h1);
-        if (before < take && take <= before + h0 + h1) {
-          const bool first = take <= before + h0;
-          pick[0] = (uint32_t)(first ? d0 : d0 - 1);
-          pick[1] = take - before - (first ? 0u : h0);
+        uint32_t before = warp_offsets(__shfl_sync(FULL, x, 31), sums[pass], &all) + x - mine;
+#pragma unroll
+        for (int q = 0; q < PT; ++q) {
+          if (before < take && take <= before + h[q]) {
+            pick[pass][0] = (uint32_t)(2047 - PT * t - q);
+            pick[pass][1] = take - before;
+            pick[pass][2] = h[q];
+          }
+          before += h[q];
         }
         __syncthreads();
-        prefix = (prefix << bits[pass]) | pick[0];
-        take = pick[1];
-        __syncthreads();
+        prefix = (prefix << bits[pass]) | pick[pass][0];
+        take = pick[pass][1];
+        thr = prefix << sh;
+        all_at = take == pick[pass][2];
+        if (all_at) break;
       }
-      thr = prefix;
-      ties = take;                          // rows at the threshold that stay: the lowest ones
+      ties = take;                          // rows at the threshold that stay
     }
   }
 
-  // which rows stay: all above the threshold, and the first `ties` at it
-  uint32_t tie0 = 0, total;
+  uint32_t tie0 = 0;
   if (a.accept) {
     if (small) {
 #pragma unroll
@@ -285,51 +307,81 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
         k8[u] = j < j1 ? acc[j] : 0u;
       }
     }
-    uint32_t c = 0;
+    uint32_t c = 0, total;
     each([&](int, uint32_t k, bool) { c += __popc(__ballot_sync(FULL, k != 0u)); });
-    warp_offsets(c, sums, &total);
+    warp_offsets(c, sums[3], &total);
     count = (int)total;
-    thr = 0u;
-  } else if (count > 0) {
-    uint32_t c = 0;
-    each([&](int, uint32_t k, bool in) { c += __popc(__ballot_sync(FULL, in && k == thr)); });
-    tie0 = warp_offsets(c, sums, &total);
-  } else {
+    thr = 1u;
+    all_at = true;
+  } else if (count == 0) {
     thr = SAFE;                             // nothing stays
+  } else if (!all_at) {
+    uint32_t c = 0, total;
+    each([&](int, uint32_t k, bool in) { c += __popc(__ballot_sync(FULL, in && k == thr)); });
+    tie0 = warp_offsets(c, sums[3], &total);
   }
   const unsigned below = (1u << lane) - 1u;
   // whether a row stays; `tie` counts the threshold's rows before the 32 at hand
   auto stays = [&](uint32_t k, bool in, uint32_t& tie) -> bool {
+    if (all_at) return in && k >= thr;
     const unsigned m = __ballot_sync(FULL, in && k == thr);
     const bool s = in && (k > thr || (k == thr && tie + __popc(m & below) < ties));
     tie += __popc(m);
     return s;
   };
   uint32_t holes = 0, late = 0, tie = tie0;
-  each([&](int j, uint32_t k, bool in) {
-    const bool s = stays(k, in, tie);
-    holes += __popc(__ballot_sync(FULL, in && j < count && !s));
-    late += __popc(__ballot_sync(FULL, j >= count && s));
-  });
-  uint32_t n_move, n_late;
-  uint32_t hole = warp_offsets(holes, sums, &n_move);
-  uint32_t lt = warp_offsets(late, sums, &n_late);
-  tie = tie0;
-  each([&](int j, uint32_t k, bool in) {
-    const bool s = stays(k, in, tie);
-    const bool is_hole = in && j < count && !s, is_late = j >= count && s;
-    const unsigned mh = __ballot_sync(FULL, is_hole), ml = __ballot_sync(FULL, is_late);
-    if (is_hole) dst[hole + __popc(mh & below)] = (int32_t)w.slot(base + j, a.S);
-    if (is_late) src[lt + __popc(ml & below)] = (int32_t)w.slot(base + j, a.S);
-    hole += __popc(mh);
-    lt += __popc(ml);
-  });
+  uint32_t mh[HEAD], ml[HEAD];              // (small) which of each 32 rows are holes, late rows
+  if (small) {
+#pragma unroll
+    for (int u = 0; u < HEAD; ++u) {
+      const int j = j0 + 32 * u + lane;
+      const bool in = j < j1, s = stays(k8[u], in, tie);
+      mh[u] = __ballot_sync(FULL, in && j < count && !s);
+      ml[u] = __ballot_sync(FULL, j >= count && s);
+      holes += __popc(mh[u]);
+      late += __popc(ml[u]);
+    }
+  } else {
+    each([&](int j, uint32_t k, bool in) {
+      const bool s = stays(k, in, tie);
+      holes += __popc(__ballot_sync(FULL, in && j < count && !s));
+      late += __popc(__ballot_sync(FULL, j >= count && s));
+    });
+  }
+  uint64_t moves;
+  const uint64_t off = warp_offsets((uint64_t)late << 32 | holes, sums2, &moves);
+  const int n_move = (int)(uint32_t)moves;
+  uint32_t hole = (uint32_t)off, lt = (uint32_t)(off >> 32);
+  const int32_t S = (int32_t)a.S, at0 = w.first + base;      // below 2^31: S <= 2^30
+  auto list_row = [&](int j, unsigned h, unsigned l) {
+    int32_t slot = at0 + j;                 // (base + j < S)
+    if (slot >= S) slot -= S;
+    if (h) {
+      if (h >> lane & 1u) dst[hole + __popc(h & below)] = slot;
+      hole += __popc(h);
+    }
+    if (l) {
+      if (l >> lane & 1u) src[lt + __popc(l & below)] = slot;
+      lt += __popc(l);
+    }
+  };
+  if (small) {
+#pragma unroll
+    for (int u = 0; u < HEAD; ++u) list_row(j0 + 32 * u + lane, mh[u], ml[u]);
+  } else {
+    tie = tie0;
+    each([&](int j, uint32_t k, bool in) {
+      const bool s = stays(k, in, tie);
+      const unsigned h = __ballot_sync(FULL, in && j < count && !s);
+      list_row(j, h, __ballot_sync(FULL, j >= count && s));
+    });
+  }
   if (MOVE) {
     __syncthreads();                        // the list is complete
     move_rows(static_cast<V*>(a.cache) + (int64_t)b * a.S * a.per_row, a.per_row, wt, pos, dst, src,
-              (int)n_move, warp, NW);
+              n_move, warp, NW);
   }
-  if (t == 0) finish(base + count, (int)n_move);
+  if (t == 0) finish(base + count, n_move);
 }
 
 // Copy the listed rows; blockIdx.y is the sequence.
