@@ -178,20 +178,22 @@ def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _args(item: int, *tensors) -> list:
-    """Device pointers of tensors whose elements have ``item`` bytes.  A tensor of the host or of
-    another device than the current one, one with strides of its own, and one of another element
-    size raise ValueError: the library sees pointers only."""
-    current = _current_device()
+def _args(item: int, *tensors, current: Optional[int] = None) -> list:
+    """Device pointers of tensors whose elements have ``item`` bytes (0: any, for a workspace).  A
+    tensor of the host or of another device than ``current``, the current one, one with strides of
+    its own, and one of another element size raise ValueError: the library sees pointers only."""
+    if current is None:
+        current = _current_device()
     out = []
     for t in tensors:
         if t is None or isinstance(t, int):
             out.append(t)
-        elif t.get_device() == current and t.element_size() == item and t.is_contiguous():
+        elif (t.get_device() == current and (t.element_size() == item or not item)
+              and t.is_contiguous()):
             out.append(t.data_ptr())
         else:
-            raise ValueError(f"a contiguous tensor with {item}-byte elements on cuda:{current}, the "
-                             f"current device, is needed, not {t.dtype} {tuple(t.shape)} with "
+            raise ValueError(f"a contiguous tensor with {item or 'any'}-byte elements on "
+                             f"cuda:{current}, the current device, is needed, not {t.dtype} {tuple(t.shape)} with "
                              f"strides {t.stride()} on {t.device}")
     return out
 
@@ -207,8 +209,9 @@ def _item(shape: MlaShape) -> int:
 
 def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
                    cache, position=None, stream=None) -> None:
-    h, w_dkv, w_kr, cache = _args(_item(shape), h, w_dkv, w_kr, cache)
-    window, token, position = _args(4, window, token, position)
+    dev = _current_device()
+    h, w_dkv, w_kr, cache = _args(_item(shape), h, w_dkv, w_kr, cache, current=dev)
+    window, token, position = _args(4, window, token, position, current=dev)
     native.check("mla_tree_write", native.lib().mla_tree_write(
         ctypes.byref(shape), h, d_model, n_nodes, window, token, w_dkv, w_kr, cache, position,
         _stream(stream)))
@@ -216,8 +219,9 @@ def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token
 
 def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
                       stream=None) -> None:
-    q_nope, q_rope, w_uk, q_abs = _args(_item(shape), q_nope, q_rope, w_uk, q_abs)
-    token, = _args(4, token)
+    dev = _current_device()
+    q_nope, q_rope, w_uk, q_abs = _args(_item(shape), q_nope, q_rope, w_uk, q_abs, current=dev)
+    token, = _args(4, token, current=dev)
     native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
         ctypes.byref(shape), q_nope, q_rope, n_nodes, token, w_uk, q_abs, _stream(stream)))
 
@@ -229,22 +233,25 @@ def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
 def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                     softmax_scale: float, o_lat, lse=None, workspace=None,
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
+    dev = _current_device()
     n = _bytes(workspace, workspace_bytes)
-    q_abs, cache, o_lat = _args(_item(shape), q_abs, cache, o_lat)
-    window, lse = _args(4, window, lse)
-    tree, = _args(1, tree)
+    q_abs, cache, o_lat = _args(_item(shape), q_abs, cache, o_lat, current=dev)
+    window, lse = _args(4, window, lse, current=dev)
+    tree, = _args(1, tree, current=dev)
+    ws, = _args(0, workspace, current=dev)
     native.check("mla_attend_tree", native.lib().mla_attend_tree(
         ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, o_lat, lse,
-        _ptr(workspace), n, _stream(stream)))
+        ws, n, _stream(stream)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                       softmax_scale: float, lse, query_weight, weight_in, weight_out,
                       stream=None) -> None:
-    q_abs, cache = _args(_item(shape), q_abs, cache)
+    dev = _current_device()
+    q_abs, cache = _args(_item(shape), q_abs, cache, current=dev)
     window, lse, query_weight, weight_in, weight_out = _args(4, window, lse, query_weight,
-                                                             weight_in, weight_out)
-    tree, = _args(1, tree)
+                                                             weight_in, weight_out, current=dev)
+    tree, = _args(1, tree, current=dev)
     native.check("mla_attend_weight", native.lib().mla_attend_weight(
         ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
         query_weight, weight_in, weight_out, _stream(stream)))
@@ -256,24 +263,28 @@ def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
 
 def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    dev = _current_device()
     n = _bytes(workspace, workspace_bytes)
-    cache, = _args(_item(shape), cache)
-    window, weight, position = _args(4, window, weight, position)
-    accept, = _args(1, accept)
+    cache, = _args(_item(shape), cache, current=dev)
+    window, weight, position = _args(4, window, weight, position, current=dev)
+    accept, = _args(1, accept, current=dev)
+    ws, = _args(0, workspace, current=dev)
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
-        ctypes.byref(shape), cache, n_nodes, accept, window, weight, position, _ptr(workspace), n,
+        ctypes.byref(shape), cache, n_nodes, accept, window, weight, position, ws, n,
         _stream(stream)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
                     weight, position, workspace, workspace_bytes: Optional[int] = None,
                     stream=None) -> None:
+    dev = _current_device()
     n = _bytes(workspace, workspace_bytes)
-    cache, = _args(_item(shape), cache)
-    window, weight, position = _args(4, window, weight, position)
+    cache, = _args(_item(shape), cache, current=dev)
+    window, weight, position = _args(4, window, weight, position, current=dev)
+    ws, = _args(0, workspace, current=dev)
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
         ctypes.byref(shape), cache, n_keep, n_sink, n_recent, window, weight, position,
-        _ptr(workspace), n, _stream(stream)))
+        ws, n, _stream(stream)))
 
 
 def mla_kernel_launches() -> int:

@@ -144,9 +144,20 @@ def test_binding_refuses_tensors_it_cannot_pass(monkeypatch):
     for bad in (Fake(item=4), Fake(contiguous=False), Fake(dev=1), torch.zeros(4, dtype=torch.bfloat16)):
         with pytest.raises(ValueError):
             mla._args(2, bad)
+    assert mla._args(0, Fake(item=1)) == [FAKE]
+    for bad in (Fake(contiguous=False), Fake(dev=1), torch.zeros(4)):
+        with pytest.raises(ValueError):
+            mla._args(0, bad)
     s = shape()
     with pytest.raises(ValueError):
         mla.mla_attend_tree(s, torch.zeros(4), 1, FAKE, FAKE, None, 0.1, FAKE, stream=0)
     with pytest.raises(ValueError):
         mla.mla_cache_evict(s, FAKE, 1, 0, 0, torch.zeros(3, dtype=torch.int32), FAKE, FAKE, FAKE, 1,
                             stream=0)
+    host = torch.zeros(1 << 16, dtype=torch.uint8)              # a workspace of the host
+    for call in (lambda: mla.mla_attend_tree(s, FAKE, 1, FAKE, FAKE, None, 0.1, FAKE, None, host,
+                                             stream=0),
+                 lambda: mla.mla_tree_accept(s, FAKE, 1, FAKE, FAKE, None, None, host, stream=0),
+                 lambda: mla.mla_cache_evict(s, FAKE, 1, 0, 0, FAKE, FAKE, FAKE, host, stream=0)):
+        with pytest.raises(ValueError):
+            call()
