@@ -342,6 +342,10 @@ struct TreeWalk {
 // Costs in key blocks: of a segment (the switch: Q reload, output epilogue, pipeline refill), and of
 // split tiles (the merge).  Measured on B200 (video chunk, long window and decode shapes).
 constexpr int SEG_COST = 7, COMBINE_COST = 16;
+// Draft trees, what it costs to split tiles when every cluster has one piece of one tile: 8 to 9 us,
+// against some 1.2 us per block, for a merge launch; and, where the launch is made anyway (3.5 to 5
+// us that merge nothing), for the pieces.
+constexpr int MERGE_COST = 7, PIECE_COST = 3;
 
 // Where cluster u's equal share of a line of W positions starts.
 __device__ __forceinline__ uint32_t line_cut(uint32_t W, uint32_t G, uint32_t u) {
@@ -453,6 +457,53 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
   if (W > 0) {
     p0 = line_cut(W, G, c);
     p1 = line_cut(W, G, c + 1);
+    // With no more tiles than clusters, a cluster takes one piece of one tile: no more than `len`
+    // blocks, the fewest for which the clusters suffice, if that pays for the merge (1 sequence of
+    // 900 rows, 128 heads: 31.7 -> 21.3 us; 32 of 1500: 44 -> 41), else a whole tile (70 sequences of up to 800 rows:
+    // 49 us by equal shares, where short neighbours meet in a cluster, -> 34).
+    const float share = (float)W / (float)G;
+    uint32_t len = 0;
+    if (T <= (uint32_t)G) {
+      auto pieces = [&](uint32_t l) {
+        uint32_t n = 0;
+        for (int b = lane; b - lane < B; b += 32) {
+          const Span s = b == lane ? mine : (b < B ? span(b) : Span{0, 0});
+          n += s.tiles * ((s.blocks + l - 1) / l);
+        }
+        n = __reduce_add_sync(FULL, n);
+        return n;
+      };
+      len = nmax;
+      if (sc.split) {
+        uint32_t lo = (W + G - 1) / G, hi = nmax;
+        while (lo < hi) {
+          const uint32_t mid = (lo + hi) >> 1;
+          if (pieces(mid) <= (uint32_t)G)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        if (lo + PIECE_COST < nmax) len = lo;
+        // (a share may still be much shorter: one piece more and a merge of more pieces)
+        const float most = len == nmax ? (float)nmax : (float)(len + PIECE_COST);
+        if (share + SEG_COST + COMBINE_COST < most) len = 0;
+      }
+      if (len > 0) {
+        uint32_t n = 0;
+        if ((uint32_t)c < pieces(len)) {
+          const uint32_t u[1] = {(uint32_t)c};
+          Spot s[1];
+          auto cut = [&](Span v) { return Span{v.tiles, (v.blocks + len - 1) / len}; };
+          line_find(B, [&](int b) { return cut(span(b)); }, cut(mine), u, s);
+          const uint32_t np = s[0].s.blocks, nblk = span(s[0].b).blocks;
+          const uint32_t tile = s[0].off / np, k = s[0].off - tile * np, from = nblk * k / np;
+          n = nblk * (k + 1) / np - from;
+          at[0] = {s[0].b, 0, tile * nblk + from, {s[0].s.tiles, nblk}};
+        }
+        sw.begin(a, list, 0, at[0].b, at[0].off, at[0].s.blocks, n, c);
+        return;
+      }
+    }
     if (K > sc.l2_blocks && a.tiles_per_batch > 2 && B <= TREE_MAXB) {
       R = tree_rounds<NT>(span, pl, x, list, B, W, T, G, c);
       p0 = x.start[c];
@@ -463,7 +514,6 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
     // Split tiles, or cut on tile boundaries?  Whole tiles take as long as the longest one, or a
     // share plus what rounding up to tiles adds (for sequences of one length (ceil(T / G) - T / G)
     // tiles); split ones take a share, one segment more and the merge.
-    const float share = (float)W / (float)G;
     const float up = ((float)((T + G - 1) / G) - (float)T / (float)G) * (float)nmax;
     const bool whole = !sc.split || fmaxf((float)nmax, share + up) <= share + SEG_COST + COMBINE_COST;
     if (p0 < p1) {
@@ -1926,10 +1976,13 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
   a.window = window;
   a.tree = tree;
   a.err = err;
-  // A tile is only split when that saves more than a segment and the merge cost, so rings whose
-  // longest tile is shorter never need the merge launch.
+  // A tile is only split when that saves more than it costs: rings whose longest tile is too short
+  // for that, with the clusters there are per tile, never need the merge launch.
+  const int64_t most = g.S / a.bn + 2, tiles = (int64_t)g.B * a.tiles_per_batch;
+  const int64_t per = ncl / tiles;                    // pieces of a tile
   const bool split = workspace && workspace_bytes >= tc_attend_tree_workspace(g) &&
-                     g.S / a.bn + 2 > SEG_COST + COMBINE_COST;
+                     (most > SEG_COST + COMBINE_COST ||
+                      (per > 1 && (most + per - 1) / per + MERGE_COST < most));
   TreeSched sc{split ? 1 : 0, UINT32_MAX};
   {
     // keys beyond a third of L2 are read again from HBM by every tile that comes to them later
