@@ -451,12 +451,9 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
   T = __reduce_add_sync(FULL, T);
   K = __reduce_add_sync(FULL, K);
   nmax = __reduce_max_sync(FULL, nmax);
-  uint32_t p0 = 0, p1 = 0;                     // the tail's ends in the line
-  int R = 0;
-  Spot at[2] = {{0, 0, 0, mine}, {0, 0, 0, mine}};
+  int b = 0, R = 0;                            // the tail: n blocks from block `off` of sequence b on
+  uint32_t off = 0, nblk = 0, n = 0;
   if (W > 0) {
-    p0 = line_cut(W, G, c);
-    p1 = line_cut(W, G, c + 1);
     // With no more tiles than clusters, a cluster takes one piece of one tile: no more than `len`
     // blocks, the fewest for which the clusters suffice, if that pays for the merge (1 sequence of
     // 900 rows, 128 heads: 31.7 -> 21.3 us; 32 of 1500: 44 -> 41), else a whole tile (70 sequences of up to 800 rows:
@@ -489,25 +486,34 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
         if (share + SEG_COST + COMBINE_COST < most) len = 0;
       }
       if (len > 0) {
-        uint32_t n = 0;
         if ((uint32_t)c < pieces(len)) {
           const uint32_t u[1] = {(uint32_t)c};
           Spot s[1];
           auto cut = [&](Span v) { return Span{v.tiles, (v.blocks + len - 1) / len}; };
           line_find(B, [&](int b) { return cut(span(b)); }, cut(mine), u, s);
-          const uint32_t np = s[0].s.blocks, nblk = span(s[0].b).blocks;
-          const uint32_t tile = s[0].off / np, k = s[0].off - tile * np, from = nblk * k / np;
-          n = nblk * (k + 1) / np - from;
-          at[0] = {s[0].b, 0, tile * nblk + from, {s[0].s.tiles, nblk}};
+          const uint32_t np = s[0].s.blocks, tile = s[0].off / np, k = s[0].off - tile * np;
+          b = s[0].b;
+          nblk = span(b).blocks;
+          off = tile * nblk + nblk * k / np;
+          n = nblk * (k + 1) / np - nblk * k / np;
         }
-        sw.begin(a, list, 0, at[0].b, at[0].off, at[0].s.blocks, n, c);
+        sw.begin(a, list, 0, b, off, nblk, n, c);
         return;
       }
     }
+    // Else equal shares of a line on which each tile has SEG_COST positions before its blocks: of
+    // ragged sequences a share holds few long tiles or fewer blocks of short ones (24 of 16 nodes, 64
+    // heads, up to 2000 rows: 154 -> 127 us, 16 of 8 nodes, 128 heads, up to 600: 58 -> 50).
+    uint32_t seg = SEG_COST, line = W + T * SEG_COST;
+    uint32_t p[2] = {line_cut(line, G, c), line_cut(line, G, c + 1)};
     if (K > sc.l2_blocks && a.tiles_per_batch > 2 && B <= TREE_MAXB) {
       R = tree_rounds<NT>(span, pl, x, list, B, W, T, G, c);
-      p0 = x.start[c];
-      p1 = x.start[c + 1];
+      if (R > 0) {
+        seg = 0;
+        line = W;
+        p[0] = x.start[c];
+        p[1] = x.start[c + 1];
+      }
       fence_proxy_async_smem();                // the arrays are read before TMA writes over them
       __syncthreads();
     }
@@ -516,27 +522,47 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
     // tiles); split ones take a share, one segment more and the merge.
     const float up = ((float)((T + G - 1) / G) - (float)T / (float)G) * (float)nmax;
     const bool whole = !sc.split || fmaxf((float)nmax, share + up) <= share + SEG_COST + COMBINE_COST;
-    if (p0 < p1) {
-      // (an end at W has no sequence: the last position's stands for it)
-      const uint32_t q[2] = {p0, p1 < W ? p1 : W - 1};
-      line_find(B, span, mine, q, at);
-      if (whole) {                             // the first boundaries at or past the cuts
-        const uint32_t n0 = (at[0].off + at[0].s.blocks - 1) / at[0].s.blocks * at[0].s.blocks;
-        const uint32_t n1 = (at[1].off + at[1].s.blocks - 1) / at[1].s.blocks * at[1].s.blocks;
-        p0 += n0 - at[0].off;
-        at[0].off = n0;
-        if (p1 < W) p1 += n1 - at[1].off;
-        // (which may be the start of the next sequence that has tiles)
-        if (p0 < p1 && n0 >= at[0].s.tiles * at[0].s.blocks) {
-          const uint32_t q0[1] = {p0};
-          Spot s[1];
-          line_find(B, span, mine, q0, s);
-          at[0] = s[0];
+    if (p[0] < p[1]) {
+      // (an end of the line has no sequence: the last position's stands for it)
+      const uint32_t q[2] = {p[0], p[1] < line ? p[1] : line - 1};
+      auto wide = [&](Span s) { return Span{s.tiles, s.tiles ? s.blocks + seg : 0}; };
+      auto wide_at = [&](int b) { return wide(span(b)); };
+      Spot at[2];
+      line_find(B, wide_at, wide(mine), q, at);
+      uint32_t tile[2], jb[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t each = at[k].s.blocks, off = at[k].off + (p[k] - q[k]);
+        tile[k] = off / each;
+        const uint32_t in = off - tile[k] * each;
+        jb[k] = in > seg ? in - seg : 0;
+        if (whole && in > 0) {                 // the first boundary at or past the cut
+          ++tile[k];
+          jb[k] = 0;
         }
       }
+      // blocks between the two
+      for (int b = lane; b - lane < B; b += 32) {
+        const Span s = b == lane ? mine : (b < B ? span(b) : Span{0, 0});
+        const uint32_t t0 = b < at[0].b ? s.tiles : (b == at[0].b ? tile[0] : 0);
+        const uint32_t t1 = b < at[1].b ? s.tiles : (b == at[1].b ? tile[1] : 0);
+        n += s.blocks * (t1 - t0);
+      }
+      n = __reduce_add_sync(FULL, n);
+      n += jb[1] - jb[0];
+      if (n > 0 && tile[0] == at[0].s.tiles) {             // the start of the next sequence
+        const uint32_t q0[1] = {at[0].start + at[0].s.tiles * at[0].s.blocks};
+        Spot s[1];
+        line_find(B, wide_at, wide(mine), q0, s);
+        at[0] = s[0];
+        tile[0] = 0;
+      }
+      nblk = at[0].s.blocks - seg;
+      b = at[0].b;
+      off = tile[0] * nblk + jb[0];
     }
   }
-  sw.begin(a, list, R, at[0].b, at[0].off, at[0].s.blocks, p0 < p1 ? p1 - p0 : 0u, c);
+  sw.begin(a, list, R, b, off, nblk, n, c);
 }
 
 template <bool TREE> struct SchedOf { using S = Sched; using Walk = SegWalk; };
@@ -1944,8 +1970,9 @@ cudaError_t tc_attend_ring(const Geo& g, const void* q_abs, int64_t n_q, int64_t
 }
 
 bool tc_attend_tree_supported(const Geo& g, int64_t n_nodes) {
-  // the line of key blocks (at most one block more per run of slots) is counted in 31 bits
-  const int64_t tiles = (n_nodes * g.H + TM - 1) / TM, blocks = g.S / Lay<0>::BNK + 3;
+  // the line of key blocks (at most one block more per run of slots, and SEG_COST positions per
+  // tile) is counted in 31 bits
+  const int64_t tiles = (n_nodes * g.H + TM - 1) / TM, blocks = g.S / Lay<0>::BNK + 3 + SEG_COST;
   return tc_attend_supported(g) && (double)g.B * tiles * blocks < 2147483648.0;
 }
 
