@@ -287,6 +287,31 @@ def test_many_sequences(cuda_ok, B, n, S):
             assert (got[b] == 0).all()
 
 
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("B,long", [
+    (80, 1),         # more tiles than clusters, one of them far longer: cut inside tiles
+    (80, 80),        # all long: whole tiles
+    (40, 40),        # some tiles in pieces, others whole
+    (30, 3),         # three in many pieces
+    (2, 2),
+])
+def test_attend_plans(cuda_ok, B, long, split):
+    """Ragged batches on both sides of each rule by which tiles are shared among the SMs."""
+    n, S = 16, 2600
+    wl = T.workload(T.MAIN, B, S)
+    rng = np.random.default_rng([B, long])
+    windows = [(int(rng.integers(0, S)), int(rng.integers(1000, S - n + 1)) if b < long
+                else int(rng.integers(0, 60)), int(rng.integers(1, n + 1))) for b in range(B)]
+    windows = [windows[b] for b in rng.permutation(B)]
+    q = T.normal(rng, (B, n, wl.n_heads, wl.row_width), wl.dtype)
+    one = T.normal(rng, (1, S, wl.row_width), wl.dtype)      # (every sequence's ring, at own windows)
+    _, see = T.random_tree(rng, B, n)
+    ct = P.upload(one).expand(B, -1, -1).contiguous()
+    o, lse = attend(wl, P.upload(q), ct, windows, tree_dev(see), n, split)
+    check_attend(wl, q.values, np.broadcast_to(one.values, (B,) + one.values.shape[1:]), windows, see,
+                 n, o, lse)
+
+
 def test_far_slots(cuda_ok):
     """A ring of more than 2^31 elements: a step at its end gives the bits of a step at the end of a
     short ring (neither splits a tile)."""
