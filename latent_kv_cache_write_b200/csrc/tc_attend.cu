@@ -1297,32 +1297,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
         int64_t slot0, g0;
         int valid;
         blk.get(j, slot0, g0, valid);
-        if (valid < BN && t < BN && t >= valid) {
-          // a partial block: zero this CTA's latent rows past the last key so that masked
-          // keys contribute exact zeros to P.V whatever the ring holds there (the stage
-          // has landed: the score MMAs of this block have completed)
-          uint8_t* st = sm + OFF_KV + ((gbase + jl) % NST) * BOX_BYTES + t * 128;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) p[w] = make_uint4(0, 0, 0, 0);
-          }
-        }
-
-        // A block with draft nodes: finite node rows.  A hidden row's weight is 0, but 0 * NaN would
-        // still reach every row of the tile through the PV product (a node that does see a NaN
-        // row gets it through its scores).
+        // A partial block: zero this CTA's latent rows past the last key so that masked keys contribute
+        // exact zeros to P.V whatever the ring holds there (the stage has landed: the score MMAs of
+        // this block have completed).  A block with draft nodes: finite node rows, since a hidden
+        // row's weight is 0, but 0 * NaN would still reach every row of the tile (a node that does
+        // see a NaN row gets it through its scores).  Eight threads share a row: a thread per row
+        // meets the others in the same banks (3 us of a block that is nearly all past the end).
         int nctx = BN;                                 // context keys of the block
-        if constexpr (TREE) {
-          nctx = max(min(ctx - (int)g0, valid), 0);
-          if (nctx < BN && t < valid && t >= nctx) {
-            uint8_t* st = sm + OFF_KV + ((gbase + jl) % NST) * BOX_BYTES + t * 128;
+        if constexpr (TREE) nctx = max(min(ctx - (int)g0, valid), 0);
+        if ((TREE ? nctx : valid) < BN) {
+          uint8_t* st = sm + OFF_KV + ((gbase + jl) % NST) * BOX_BYTES + t * 16;
 #pragma unroll 1
+          for (int r = t >> 3; r < BN; r += TM / 8, st += TM * 16) {
+            if (r < (TREE ? nctx : valid)) continue;
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint4* p = reinterpret_cast<uint4*>(st + q * NST * BOX_BYTES);
-#pragma unroll
-              for (int w = 0; w < 8; ++w) p[w] = finite8(p[w]);
+              *p = r < valid ? finite8(*p) : make_uint4(0, 0, 0, 0);
             }
           }
         }
