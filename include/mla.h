@@ -375,8 +375,9 @@ mla_status mla_attend_materialised(const mla_shape* shape, const void* q_nope,
  *   the context, rows + i is node i.  Values outside the ring are clipped: first to
  *   [0, S - 1], rows to [0, S], nodes to [0, min(n_nodes, S - rows)].
  *
- * n_nodes is the stride of the per-node tensors and the most nodes a sequence can have; a
- * sequence's nodes past its own count are not read, and their results are left as they were.
+ * n_nodes is the stride of the per-node tensors and the most nodes a sequence can have; what a
+ * sequence's nodes past its own count hold does not matter, and their results are left as they
+ * were.
  * The arrays named here and below by their element type (window, token, position, weights, lse)
  * need that type's alignment only; tree and accept are bytes.
  * The order of the context rows does not matter to the attention (a cached key carries its
@@ -436,7 +437,8 @@ size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes);
  *   lse[b][i][h]   = log(sum_j exp(s(j)))    (natural log, float32; if lse != NULL)
  * A node that sees nothing (no context and an empty tree row) gets o_lat = 0, lse = -inf.  What
  * a hidden node's row holds, infinities and NaN included, does not reach a node that does not
- * see it.
+ * see it.  (A node that does see it gets NaN, or, where an infinite element makes its weight 0,
+ * nothing of it.)
  *
  *   q_abs [B, n_nodes, n_h, d_latent + d_rope]  read    o_lat [B, n_nodes, n_h, d_latent] written
  *   cache [B, S, d_latent + d_rope]             read    lse   [B, n_nodes, n_h] float32 or NULL

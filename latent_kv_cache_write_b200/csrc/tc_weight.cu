@@ -62,7 +62,8 @@ struct WLay {
   static constexpr int OFF_ROW = OFF_ST + NST * SBOX;      // (lse, weight) of rows [2][2][256]
   static constexpr int OFF_SUM = OFF_ROW + 4 * 256 * 8;    // sums handed between warpgroups [128]
   static constexpr int OFF_PART = OFF_SUM + 128 * 4;       // sums of the cluster's other pairs
-  static constexpr int OFF_BAR = OFF_PART + MAXCP * 128 * 4;
+  static constexpr int OFF_MASK = OFF_PART + MAXCP * 128 * 4;   // rows that add, bits [2][2][8]
+  static constexpr int OFF_BAR = OFF_MASK + 4 * 8 * 4;
   static constexpr int B_SF = 0;                           // stage loaded, both CTAs   [NST]
   static constexpr int B_SE = B_SF + NST;                  // stage free                [NST]
   static constexpr int B_RF = B_SE + NST;                  // resident box loaded       [NRES]
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(WT, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t drained = mapa(smem_u32(&bar[LY::B_AE + wg]), leader);
     float2* rowbuf = reinterpret_cast<float2*>(sm + LY::OFF_ROW) + wg * 512;
+    uint32_t* rowmask = reinterpret_cast<uint32_t*>(sm + LY::OFF_MASK) + wg * 16;
     float* handed = reinterpret_cast<float*>(sm + LY::OFF_SUM);
     const uint32_t H = (uint32_t)a.g.H;
     uint32_t tc = 0, mine = 0;                 // tiles of the pair, tiles this warpgroup has taken
@@ -440,9 +442,9 @@ __global__ void __launch_bounds__(WT, 1)
         }
         if ((int)(tc & 1) != wg) continue;
         took = true;
-        // log-sum-exps (log2 units) and weights of the tile's rows; a row that adds nothing has
-        // an infinite one, so that its exponentials are 0
+        // log-sum-exps (log2 units) and weights of the tile's rows, and which of them add anything
         float2* rb = rowbuf + (mine & 1) * 256;
+        uint32_t* rm = rowmask + (mine & 1) * 8;
 #pragma unroll
         for (int h = 0; h < NT / 128; ++h) {
           float2 v = make_float2(INFINITY, 0.f);
@@ -452,6 +454,8 @@ __global__ void __launch_bounds__(WT, 1)
             if (g != 0.f && l != -INFINITY) v = make_float2(l * 1.4426950408889634f, g);
           }
           rb[h * 128 + t] = v;
+          const uint32_t adds = __ballot_sync(FULL, v.y != 0.f);
+          if (lane == 0) rm[h * 4 + (warp & 3)] = adds;
         }
         named_bar(1 + wg, 128);
         ok = __all_sync(FULL, ok && mbar_wait_cluster(&bar[LY::B_AF + wg], mine & 1, abort, a.err,
@@ -471,12 +475,12 @@ __global__ void __launch_bounds__(WT, 1)
           }
           // rows of these 32 columns that exist, the first one, and (where it matters) their nodes
           const bool second = NT > 128 && c0 >= 128;
-          const int live = (second ? n[NT / 128 - 1] : n[0]) - (c0 & 127);
-          if (!ok || live <= 0) continue;
+          const uint32_t adds = rm[c0 / 32];             // (rows past the last have no weight)
+          if (!ok || adds == 0) continue;
           const uint32_t r0 = (second ? row[NT / 128 - 1] : row[0]) + (c0 & 127);
           const uint32_t i0 = nodes ? r0 / H : 0, i1 = nodes ? (r0 + 31) / H : 0;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          if (live >= 32 && i0 == i1) {
+          if (adds == ~0u && i0 == i1) {
             const float4* rv = reinterpret_cast<const float4*>(rb + c0);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -489,9 +493,11 @@ __global__ void __launch_bounds__(WT, 1)
             const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (!nodes || sees(i0)) total += s;
           } else {
-            // rows past the last, or rows of several nodes next to draft keys: a bit per row
-            uint32_t in = live >= 32 ? ~0u : (1u << live) - 1u;
+            // rows that add nothing, whatever their queries hold, or rows of several nodes next to draft
+            // keys: a bit per row
+            uint32_t in = adds;
             if (nodes) {
+              const int live = 32 - __clz((int)adds);
               uint32_t seen = 0u;
               for (uint32_t i = i0; i <= i1; ++i) {
                 const int lo = max((int)(i * H) - (int)r0, 0), hi = (int)((i + 1) * H) - (int)r0;

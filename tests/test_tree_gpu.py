@@ -256,6 +256,37 @@ def test_attend_weight(cuda_ok, cfg, n, S, windows):
             T.check_within(got[at], ref[b, at], rel * np.abs(ref[b, at]) + 1e-30, "weight")
 
 
+@pytest.mark.parametrize("cfg", ["TINY", "ODD", "MAIN", "VIDEO", "HEADS", "WIDE"])
+@pytest.mark.parametrize("n", [5, 19])
+def test_weight_ignores_rows_without_weight(cuda_ok, cfg, n):
+    """Queries of weight 0 and queries that saw nothing may hold anything: the same bits come out."""
+    S = 300
+    windows = [(250, 200, n), (3, 0, n), (1, 9, n - 2)]
+    wl = T.workload(getattr(T, cfg), 3, S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng([n, 8])
+    q = P.upload(T.normal(rng, (3, n, wl.n_heads, wl.row_width), wl.dtype))
+    ct = P.upload(T.normal(rng, (3, S, wl.row_width), wl.dtype))
+    tree = tree_dev(T.random_tree(rng, 3, n)[1])
+    _, lse = attend(wl, q, ct, windows, tree, n, fill=0.0)
+    lse[1, 2] = float("-inf")
+    lse[0, 3, ::2] = float("-inf")                        # some heads of a node
+    qw = torch.ones((3, n), device=DEV)
+    qw[:, 1] = 0.0
+    qw[2, 0] = 0.0
+    out = []
+    for bad in (None, float("nan"), float("inf")):
+        x = q.clone()
+        if bad is not None:
+            x[:, 1] = x[2, 0] = x[1, 2] = x[0, 3, ::2] = bad
+        wt = torch.zeros((3, S), device=DEV)
+        mla.mla_attend_weight(shape, x, n, ct, i32(windows), tree, SCALE, lse, qw, None, wt)
+        out.append(wt)
+    assert torch.isfinite(out[0]).all()
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+    assert mla.mla_device_error() == 0
+
+
 @pytest.mark.parametrize("B,n,S", [(700, 3, 150), (70, 20, 200), (33, 1, 1500)])
 def test_many_sequences(cuda_ok, B, n, S):
     """More sequences than a warp has lanes, many of them empty or without nodes."""
