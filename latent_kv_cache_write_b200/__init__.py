@@ -178,24 +178,18 @@ def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _args(item: int, *tensors, current: Optional[int] = None) -> list:
-    """Device pointers of tensors whose elements have ``item`` bytes (0: any, for a workspace).  A
+def _arg(t, item: int, current: int) -> Optional[int]:
+    """Device pointer of a tensor whose elements have ``item`` bytes (0: any, for a workspace).  A
     tensor of the host or of another device than ``current``, the current one, one with strides of
     its own, and one of another element size raise ValueError: the library sees pointers only."""
-    if current is None:
-        current = _current_device()
-    out = []
-    for t in tensors:
-        if t is None or isinstance(t, int):
-            out.append(t)
-        elif (t.get_device() == current and (t.element_size() == item or not item)
-              and t.is_contiguous()):
-            out.append(t.data_ptr())
-        else:
-            raise ValueError(f"a contiguous tensor with {item or 'any'}-byte elements on "
-                             f"cuda:{current}, the current device, is needed, not {t.dtype} {tuple(t.shape)} with "
-                             f"strides {t.stride()} on {t.device}")
-    return out
+    if t is None or isinstance(t, int):
+        return t
+    if (t.get_device() == current and (not item or t.element_size() == item)
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"a contiguous tensor with {item or 'any'}-byte elements on cuda:{current}, "
+                     f"the current device, is needed, not {t.dtype} {tuple(t.shape)} with strides "
+                     f"{t.stride()} on {t.device}")
 
 
 def _current_device() -> int:
@@ -209,21 +203,19 @@ def _item(shape: MlaShape) -> int:
 
 def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
                    cache, position=None, stream=None) -> None:
-    dev = _current_device()
-    h, w_dkv, w_kr, cache = _args(_item(shape), h, w_dkv, w_kr, cache, current=dev)
-    window, token, position = _args(4, window, token, position, current=dev)
+    dev, item = _current_device(), _item(shape)
     native.check("mla_tree_write", native.lib().mla_tree_write(
-        ctypes.byref(shape), h, d_model, n_nodes, window, token, w_dkv, w_kr, cache, position,
-        _stream(stream)))
+        ctypes.byref(shape), _arg(h, item, dev), d_model, n_nodes, _arg(window, 4, dev),
+        _arg(token, 4, dev), _arg(w_dkv, item, dev), _arg(w_kr, item, dev),
+        _arg(cache, item, dev), _arg(position, 4, dev), _stream(stream)))
 
 
 def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
                       stream=None) -> None:
-    dev = _current_device()
-    q_nope, q_rope, w_uk, q_abs = _args(_item(shape), q_nope, q_rope, w_uk, q_abs, current=dev)
-    token, = _args(4, token, current=dev)
+    dev, item = _current_device(), _item(shape)
     native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
-        ctypes.byref(shape), q_nope, q_rope, n_nodes, token, w_uk, q_abs, _stream(stream)))
+        ctypes.byref(shape), _arg(q_nope, item, dev), _arg(q_rope, item, dev), n_nodes,
+        _arg(token, 4, dev), _arg(w_uk, item, dev), _arg(q_abs, item, dev), _stream(stream)))
 
 
 def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
@@ -233,28 +225,23 @@ def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
 def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                     softmax_scale: float, o_lat, lse=None, workspace=None,
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
-    dev = _current_device()
-    n = _bytes(workspace, workspace_bytes)
-    q_abs, cache, o_lat = _args(_item(shape), q_abs, cache, o_lat, current=dev)
-    window, lse = _args(4, window, lse, current=dev)
-    tree, = _args(1, tree, current=dev)
-    ws, = _args(0, workspace, current=dev)
+    dev, item = _current_device(), _item(shape)
     native.check("mla_attend_tree", native.lib().mla_attend_tree(
-        ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, o_lat, lse,
-        ws, n, _stream(stream)))
+        ctypes.byref(shape), _arg(q_abs, item, dev), n_nodes, _arg(cache, item, dev),
+        _arg(window, 4, dev), _arg(tree, 1, dev), softmax_scale, _arg(o_lat, item, dev),
+        _arg(lse, 4, dev), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
+        _stream(stream)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                       softmax_scale: float, lse, query_weight, weight_in, weight_out,
                       stream=None) -> None:
-    dev = _current_device()
-    q_abs, cache = _args(_item(shape), q_abs, cache, current=dev)
-    window, lse, query_weight, weight_in, weight_out = _args(4, window, lse, query_weight,
-                                                             weight_in, weight_out, current=dev)
-    tree, = _args(1, tree, current=dev)
+    dev, item = _current_device(), _item(shape)
     native.check("mla_attend_weight", native.lib().mla_attend_weight(
-        ctypes.byref(shape), q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
-        query_weight, weight_in, weight_out, _stream(stream)))
+        ctypes.byref(shape), _arg(q_abs, item, dev), n_nodes, _arg(cache, item, dev),
+        _arg(window, 4, dev), _arg(tree, 1, dev), softmax_scale, _arg(lse, 4, dev),
+        _arg(query_weight, 4, dev), _arg(weight_in, 4, dev), _arg(weight_out, 4, dev),
+        _stream(stream)))
 
 
 def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
@@ -264,27 +251,20 @@ def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
 def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
     dev = _current_device()
-    n = _bytes(workspace, workspace_bytes)
-    cache, = _args(_item(shape), cache, current=dev)
-    window, weight, position = _args(4, window, weight, position, current=dev)
-    accept, = _args(1, accept, current=dev)
-    ws, = _args(0, workspace, current=dev)
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
-        ctypes.byref(shape), cache, n_nodes, accept, window, weight, position, ws, n,
-        _stream(stream)))
+        ctypes.byref(shape), _arg(cache, _item(shape), dev), n_nodes, _arg(accept, 1, dev),
+        _arg(window, 4, dev), _arg(weight, 4, dev), _arg(position, 4, dev),
+        _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
                     weight, position, workspace, workspace_bytes: Optional[int] = None,
                     stream=None) -> None:
     dev = _current_device()
-    n = _bytes(workspace, workspace_bytes)
-    cache, = _args(_item(shape), cache, current=dev)
-    window, weight, position = _args(4, window, weight, position, current=dev)
-    ws, = _args(0, workspace, current=dev)
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
-        ctypes.byref(shape), cache, n_keep, n_sink, n_recent, window, weight, position,
-        ws, n, _stream(stream)))
+        ctypes.byref(shape), _arg(cache, _item(shape), dev), n_keep, n_sink, n_recent,
+        _arg(window, 4, dev), _arg(weight, 4, dev), _arg(position, 4, dev),
+        _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def mla_kernel_launches() -> int:

@@ -140,14 +140,14 @@ def test_binding_refuses_tensors_it_cannot_pass(monkeypatch):
             return FAKE
 
     monkeypatch.setattr(mla, "_current_device", lambda: 0)
-    assert mla._args(2, Fake(), None, 7) == [FAKE, None, 7]
+    assert [mla._arg(t, 2, 0) for t in (Fake(), None, 7)] == [FAKE, None, 7]
     for bad in (Fake(item=4), Fake(contiguous=False), Fake(dev=1), torch.zeros(4, dtype=torch.bfloat16)):
         with pytest.raises(ValueError):
-            mla._args(2, bad)
-    assert mla._args(0, Fake(item=1)) == [FAKE]
+            mla._arg(bad, 2, 0)
+    assert mla._arg(Fake(item=1), 0, 0) == FAKE
     for bad in (Fake(contiguous=False), Fake(dev=1), torch.zeros(4)):
         with pytest.raises(ValueError):
-            mla._args(0, bad)
+            mla._arg(bad, 0, 0)
     s = shape()
     with pytest.raises(ValueError):
         mla.mla_attend_tree(s, torch.zeros(4), 1, FAKE, FAKE, None, 0.1, FAKE, stream=0)
