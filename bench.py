@@ -715,7 +715,7 @@ ATTEND_TRAFFIC = {"workload": "video_chunk_bf16",
                   "bytes": (74_559_744 + 24_711_424) + (19_032_064 + 0),
                   "sources": {
                       "latent_kv_cache_write_b200/csrc/tc_attend.cu":
-                          "f1144f9bd2fb73afdc61fe3ad4249e2bc7310b909919189b6217477b33c03cbb",
+                          "32c346b3836404b5f719d22ee4b91e0d62faded6571a9931cfdf1be56f0856cf",
                       "latent_kv_cache_write_b200/csrc/attend_combine.cu":
                           "222c5ba1c566d18775f2ce1bc5e60a70032d348e1177714588169359a78c1a85",
                       "latent_kv_cache_write_b200/csrc/attend_common.cuh":

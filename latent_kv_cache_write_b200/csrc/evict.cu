@@ -195,12 +195,11 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
     count = (int)a.n_keep;
     __syncthreads();
     // newest position, then the keys and the counts of their first digit
-    const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
     int mx = INT32_MIN;
     uint32_t safe = 0;
     auto first_digit = [&](uint32_t k, bool in) {
       safe += in && k == SAFE;
-      if (in && k != SAFE) atomicAdd(&hist[0][k >> shift[0]], 1u);
+      if (in && k != SAFE) atomicAdd(&hist[0][k >> 21], 1u);
     };
     if (small) {
       int32_t p8[HEAD];
@@ -253,8 +252,9 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
       uint32_t prefix = 0, take = (uint32_t)count - safe;
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
-        const int sh = shift[pass], above = sh + bits[pass];
-        const uint32_t mask = (1u << bits[pass]) - 1u;
+        const int bits = pass < 2 ? 11 : 10, sh = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const int above = sh + bits;
+        const uint32_t mask = (1u << bits) - 1u;
         if (pass > 0) {
           each([&](int, uint32_t k, bool in) {
             if (in && k != SAFE && (k >> above) == prefix)
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const __grid_constant__ 
           before += h[q];
         }
         __syncthreads();
-        prefix = (prefix << bits[pass]) | pick[pass][0];
+        prefix = (prefix << bits) | pick[pass][0];
         take = pick[pass][1];
         thr = prefix << sh;
         all_at = take == pick[pass][2];

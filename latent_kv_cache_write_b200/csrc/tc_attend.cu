@@ -451,7 +451,7 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
   T = __reduce_add_sync(FULL, T);
   K = __reduce_add_sync(FULL, K);
   nmax = __reduce_max_sync(FULL, nmax);
-  int b = 0, R = 0;                            // the tail: n blocks from block `off` of sequence b on
+  int seq = 0, R = 0;                          // the tail: n blocks from block `off` of sequence seq on
   uint32_t off = 0, nblk = 0, n = 0;
   if (W > 0) {
     // With no more tiles than clusters, a cluster takes one piece of one tile: no more than `len`
@@ -492,12 +492,12 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
           auto cut = [&](Span v) { return Span{v.tiles, (v.blocks + len - 1) / len}; };
           line_find(B, [&](int b) { return cut(span(b)); }, cut(mine), u, s);
           const uint32_t np = s[0].s.blocks, tile = s[0].off / np, k = s[0].off - tile * np;
-          b = s[0].b;
-          nblk = span(b).blocks;
+          seq = s[0].b;
+          nblk = span(seq).blocks;
           off = tile * nblk + nblk * k / np;
           n = nblk * (k + 1) / np - nblk * k / np;
         }
-        sw.begin(a, list, 0, b, off, nblk, n, c);
+        sw.begin(a, list, 0, seq, off, nblk, n, c);
         return;
       }
     }
@@ -558,11 +558,11 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
         tile[0] = 0;
       }
       nblk = at[0].s.blocks - seg;
-      b = at[0].b;
+      seq = at[0].b;
       off = tile[0] * nblk + jb[0];
     }
   }
-  sw.begin(a, list, R, b, off, nblk, n, c);
+  sw.begin(a, list, R, seq, off, nblk, n, c);
 }
 
 template <bool TREE> struct SchedOf { using S = Sched; using Walk = SegWalk; };
