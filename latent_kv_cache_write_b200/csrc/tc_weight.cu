@@ -56,11 +56,16 @@ struct WLay {
   static constexpr int RBOX = MODE == RES_K ? KBOX : (MODE == RES_Q ? QBOX : 0);
   static constexpr int NRES = MODE == STREAM ? 0 : NSL;               // resident boxes
   static constexpr int SBOX = MODE == RES_K ? QBOX : (MODE == RES_Q ? KBOX : KBOX + QBOX);
-  static constexpr int NST = MODE == RES_K ? 4 : (MODE == RES_Q ? (NSL == 9 ? 8 : 5) : 6);
+  // slices of a stage, stages.  A stage costs the loading and the MMA thread some 500 clk of waits
+  // and arrivals whatever it holds: single slices bound RES_Q by that.
+  static constexpr int SPS = MODE == RES_Q && NSL == 9 ? 3 : 1;
+  static constexpr int NST = MODE == RES_K ? 4 : (MODE == RES_Q ? (NSL == 9 ? 3 : 5) : 6);
+  static constexpr int STAGE = SPS * SBOX;
+  static_assert(NSL % SPS == 0, "whole stages");
   static constexpr int OFF_RES = 0;
   static constexpr int OFF_ST = NRES * RBOX;
-  static constexpr int OFF_ROW = OFF_ST + NST * SBOX;      // (lse, weight) of rows [2][2][256]
-  static constexpr int OFF_SUM = OFF_ROW + 4 * 256 * 8;    // sums handed between warpgroups [128]
+  static constexpr int OFF_ROW = OFF_ST + NST * STAGE;     // (lse, weight) of rows [2][2][NT]
+  static constexpr int OFF_SUM = OFF_ROW + 4 * NT * 8;    // sums handed between warpgroups [128]
   static constexpr int OFF_PART = OFF_SUM + 128 * 4;       // sums of the cluster's other pairs
   static constexpr int OFF_MASK = OFF_PART + MAXCP * 128 * 4;   // rows that add, bits [2][2][8]
   static constexpr int OFF_BAR = OFF_MASK + 4 * 8 * 4;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(WT, 1)
                          const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ WeightArgs p, int CP) {
   using LY = WLay<NSL, MODE>;
-  constexpr int NT = LY::NT, NST = LY::NST, NRES = LY::NRES;
+  constexpr int NT = LY::NT, SPS = LY::SPS, NST = LY::NST, NRES = LY::NRES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
@@ -318,20 +323,24 @@ __global__ void __launch_bounds__(WT, 1)
             const int g = rank == 0 ? g0 : g1;
             row += (int64_t)(g < 0 ? 0 : g) * 128;
           }
-          for (int i = 0; ok && i < NSL; ++i, ++it) {
-            if (fill && q == w.qb) ok = resident(i);
+          for (int i = 0; ok && i < NSL; i += SPS, ++it) {
+            if (fill && q == w.qb)
+              for (int e = 0; ok && e < SPS; ++e) ok = resident(i + e);
             if (!ok) break;
             const int s = it % NST;
             ok = mbar_wait(&bar[LY::B_SE + s], ((it / NST) & 1) ^ 1, abort, a.err, 0x32, it);
             if (!ok) break;
-            if (rank == 0) mbar_expect_tx(&bar[LY::B_SF + s], 2 * LY::SBOX);
+            if (rank == 0) mbar_expect_tx(&bar[LY::B_SF + s], 2 * LY::STAGE);
             const uint32_t full = even + (LY::B_SF + s) * 8;
-            uint8_t* st = sm + LY::OFF_ST + s * LY::SBOX;
-            if (MODE != RES_Q)
-              tma_load_2d_pair(st, &tmQ, full, i * 64, (int32_t)row);
-            if (MODE != RES_K)
-              tma_load_3d_pair(st + (MODE == STREAM ? LY::QBOX : 0), &tmK, full, i * 64,
-                               (int32_t)slot0, w.b);
+#pragma unroll
+            for (int e = 0; e < SPS; ++e) {
+              uint8_t* st = sm + LY::OFF_ST + s * LY::STAGE + e * LY::SBOX;
+              if (MODE != RES_Q)
+                tma_load_2d_pair(st, &tmQ, full, (i + e) * 64, (int32_t)row);
+              if (MODE != RES_K)
+                tma_load_3d_pair(st + (MODE == STREAM ? LY::QBOX : 0), &tmK, full, (i + e) * 64,
+                                 (int32_t)slot0, w.b);
+            }
           }
         }
         if (fill) {
@@ -374,24 +383,29 @@ __global__ void __launch_bounds__(WT, 1)
           ok = mbar_wait_cluster(&bar[LY::B_AE + acc], ((tc >> 1) & 1) ^ 1, abort, a.err, 0x33, tc);
           if (!ok) break;
           tc_fence_after();
-          for (int i = 0; i < NSL; ++i, ++it) {
+          for (int i = 0; i < NSL; i += SPS, ++it) {
             const int s = it % NST;
             if (fill && q == 0)
-              ok = mbar_wait_cluster(&bar[LY::B_RF + i], un & 1, abort, a.err, 0x34, i);
+              for (int e = 0; ok && e < SPS; ++e)
+                ok = mbar_wait_cluster(&bar[LY::B_RF + i + e], un & 1, abort, a.err, 0x34, i + e);
             if (ok)
               ok = mbar_wait_cluster(&bar[LY::B_SF + s], (it / NST) & 1, abort, a.err, 0x35, it);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(sm + LY::OFF_ST + s * LY::SBOX);
-            const uint32_t rs = smem_u32(sm + LY::OFF_RES + i * LY::RBOX);
-            const uint32_t kk = MODE == RES_K ? rs : (MODE == RES_Q ? st : st + LY::QBOX);
-            const uint32_t qq = MODE == RES_Q ? rs : st;
-            const uint64_t da = desc_sw128(kk, 16, 1024), db = desc_sw128(qq, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)        // 16-dim steps: +32 bytes inside the swizzle atom
-              mma_ss_pair(tmem + acc * 256, da + 2 * k, db + 2 * k, id, (i | k) ? 1u : 0u);
+            for (int e = 0; e < SPS; ++e) {
+              const uint32_t st = smem_u32(sm + LY::OFF_ST + s * LY::STAGE + e * LY::SBOX);
+              const uint32_t rs = smem_u32(sm + LY::OFF_RES + (i + e) * LY::RBOX);
+              const uint32_t kk = MODE == RES_K ? rs : (MODE == RES_Q ? st : st + LY::QBOX);
+              const uint32_t qq = MODE == RES_Q ? rs : st;
+              const uint64_t da = desc_sw128(kk, 16, 1024), db = desc_sw128(qq, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)      // 16-dim steps: +32 bytes inside the swizzle atom
+                mma_ss_pair(tmem + acc * 256, da + 2 * k, db + 2 * k, id, (i | e | k) ? 1u : 0u);
+            }
             mma_commit_pair(&bar[LY::B_SE + s], both);
-            if (NRES > 0 && last && q == tiles - 1) mma_commit_pair(&bar[LY::B_RE + i], both);
+            if (NRES > 0 && last && q == tiles - 1)
+              for (int e = 0; e < SPS; ++e) mma_commit_pair(&bar[LY::B_RE + i + e], both);
           }
           if (ok) mma_commit_pair(&bar[LY::B_AF + acc], both);
         }
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(WT, 1)
     const int wg = warp >> 2, t = tid & 127;   // accumulator, key = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t drained = mapa(smem_u32(&bar[LY::B_AE + wg]), leader);
-    float2* rowbuf = reinterpret_cast<float2*>(sm + LY::OFF_ROW) + wg * 512;
+    float2* rowbuf = reinterpret_cast<float2*>(sm + LY::OFF_ROW) + wg * 2 * NT;
     uint32_t* rowmask = reinterpret_cast<uint32_t*>(sm + LY::OFF_MASK) + wg * 16;
     float* handed = reinterpret_cast<float*>(sm + LY::OFF_SUM);
     const uint32_t H = (uint32_t)a.g.H;
@@ -443,7 +457,7 @@ __global__ void __launch_bounds__(WT, 1)
         if ((int)(tc & 1) != wg) continue;
         took = true;
         // log-sum-exps (log2 units) and weights of the tile's rows, and which of them add anything
-        float2* rb = rowbuf + (mine & 1) * 256;
+        float2* rb = rowbuf + (mine & 1) * NT;
         uint32_t* rm = rowmask + (mine & 1) * 8;
 #pragma unroll
         for (int h = 0; h < NT / 128; ++h) {
