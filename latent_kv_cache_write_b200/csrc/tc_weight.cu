@@ -16,8 +16,8 @@
 //          loads) and clusters with fewer units than others.  8 trees of up to 16 nodes, 128
 //          heads, over up to 4096 rows: 74 us against a floor of 48.
 //   RES_Q: at most 128 rows per sequence (single tokens, small trees): the rows stay and the keys
-//          stream, read once from HBM, which bounds it (5.9 TB/s in the steady state; 64
-//          sequences of 8191 rows, one token each: 122 us against a floor of 94).
+//          stream, read once from HBM, which bounds it (64 sequences of 8191 rows, one token
+//          each: 115 us against a floor of 94; a kernel that only streams them by TMA takes 102).
 //   STREAM: d_R = 512 with more rows: 256 KB of keys do not fit, both operands stream.
 //
 // A cluster has one to four pairs.  It takes whole units (256 keys), and its pairs share the tiles of
@@ -57,7 +57,8 @@ struct WLay {
   static constexpr int NRES = MODE == STREAM ? 0 : NSL;               // resident boxes
   static constexpr int SBOX = MODE == RES_K ? QBOX : (MODE == RES_Q ? KBOX : KBOX + QBOX);
   // slices of a stage, stages.  A stage costs the loading and the MMA thread some 500 clk of waits
-  // and arrivals whatever it holds: single slices bound RES_Q by that.
+  // and arrivals whatever it holds: single slices bound RES_Q by that (129 us where three take 115;
+  // with d_R = 512 two took as long as one).
   static constexpr int SPS = MODE == RES_Q && NSL == 9 ? 3 : 1;
   static constexpr int NST = MODE == RES_K ? 4 : (MODE == RES_Q ? (NSL == 9 ? 3 : 5) : 6);
   static constexpr int STAGE = SPS * SBOX;
