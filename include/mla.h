@@ -377,7 +377,7 @@ mla_status mla_attend_materialised(const mla_shape* shape, const void* q_nope,
  *
  * n_nodes is the stride of the per-node tensors and the most nodes a sequence can have; what a
  * sequence's nodes past its own count hold does not matter, and their results are left as they
- * were.
+ * were.  n_nodes = 0 is a call in which no sequence has a node, whatever its window says.
  * The arrays named here and below by their element type (window, token, position, weights, lse)
  * need that type's alignment only; tree and accept are bytes.
  * The order of the context rows does not matter to the attention (a cached key carries its
@@ -461,7 +461,8 @@ mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_
  *   weight_out[b][r] = w0 + sum over i < nodes, h of query_weight[b][i] * exp(s(b, i, h, j) - lse[b][i][h])
  * over the (i, h) that see row j, with w0 = weight_in[b][r] for a context row and 0 for a node's
  * row.  A query whose lse is -inf, or whose query_weight is 0, adds nothing.  The sums are
- * float32 and their order is fixed: the same inputs give the same bits.
+ * float32 and their order is fixed: the same inputs give the same bits.  Without nodes (n_nodes = 0,
+ * or none in a sequence) every context row gets w0.
  *
  *   q_abs, cache, window, tree, softmax_scale   as in mla_attend_tree
  *   lse          [B, n_nodes, n_h] float32      read

@@ -136,6 +136,17 @@ mla_status check_move(const mla_shape* shape, Geo* g, const void* cache, const i
   return MLA_OK;
 }
 
+// Whether p is memory that CUDA knows (without a device there is none).  Asked where a call has no
+// nodes, and so only the windows to go by.
+bool cuda_memory(const void* p) {
+  cudaPointerAttributes at{};
+  const cudaError_t e = cudaPointerGetAttributes(&at, p);
+  if (e == cudaSuccess) return at.type != cudaMemoryTypeUnregistered;
+  if (e != cudaErrorNoDevice && e != cudaErrorInsufficientDriver) return true;   // the launch reports it
+  cudaGetLastError();
+  return false;
+}
+
 // the launches of a checked attention call (n_q > 0)
 mla_status run_attend(const mla_shape* shape, const Geo& g, const void* q_abs, int64_t n_q,
                       int64_t q_first_tok, const void* cache, int64_t k_first_tok,
@@ -479,9 +490,10 @@ mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t 
   if (!lse || !weight_out) return MLA_ERR_ARG;
   if (!aligned4(lse) || !aligned4(query_weight) || !aligned4(weight_in) || !aligned4(weight_out))
     return MLA_ERR_ALIGN;
-  if (n_nodes == 0) return MLA_OK;
+  // without nodes the context's totals still go to weight_out
+  if (n_nodes == 0 && !cuda_memory(window)) return MLA_OK;
   const bool bf = shape->dtype == MLA_BF16;
-  if (bf && tc_attend_weight_supported(g, n_nodes))
+  if (n_nodes > 0 && bf && tc_attend_weight_supported(g, n_nodes))
     return cuda_status(tc_attend_weight(g, q_abs, n_nodes, cache, window, tree, softmax_scale, lse,
                                         query_weight, weight_in, weight_out, device_error_word(),
                                         (cudaStream_t)stream));

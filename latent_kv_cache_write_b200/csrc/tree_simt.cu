@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(32 * NWARP)
   for (int64_t j = blockIdx.x; j < w.len(); j += gridDim.x, turn ^= 1) {
     const int64_t at = (int64_t)b * g.S + w.slot(j, g.S);
     float kv[MAXR];
-    load_row<T, MAXR>(cache + at * g.row, g.row, kv);
+    load_row<T, MAXR>(cache + at * g.row, queries ? g.row : 0, kv);     // (not read for no one)
 #pragma unroll
     for (int r = 0; r < MAXR; ++r) kv[r] *= scale;
     float total = 0.f;

@@ -1,0 +1,60 @@
+"""Draft-tree calls at the edges of their definitions, on the GPU: no nodes at all, rows that are NaN,
+chains and trees of many nodes, the log-sum-exps of split tiles."""
+
+import numpy as np
+import pytest
+import torch
+
+import latent_kv_cache_write_b200 as mla
+from oracle import draft_tree as D
+from tests import gpu_path as P
+from tests import tree_cases as T
+from tests.test_tree_gpu import SCALE, i32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+# sequences with and without context, one that wraps, values that are clipped; all with stale nodes
+STALE = [(0, 20, 7), (35, 21, 3), (5, 0, 2), (9, 40, 1), (-4, 99, 5)]
+
+
+@pytest.mark.parametrize("cfg", ["TINY", "ODD", "MAIN", "WIDE"])
+@pytest.mark.parametrize("given", ["apart", "none", "in place"])
+def test_weight_without_nodes(cuda_ok, cfg, given):
+    """Every context row's total goes to weight_out (0 where none was given), and nothing else; also
+    captured, with windows that change before the replay."""
+    S, n = 40, 3
+    wl = T.workload(getattr(T, cfg), len(STALE), S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng(3)
+    q = P.upload(T.normal(rng, (wl.batch, n, wl.n_heads, wl.row_width), wl.dtype))
+    c = torch.full((wl.batch, S, wl.row_width), float("nan"), device=DEV, dtype=q.dtype)
+    lse = torch.zeros((wl.batch, n, wl.n_heads), device=DEV)
+    old = rng.random((wl.batch, S)).astype(np.float32)
+    before = rng.random((wl.batch, S)).astype(np.float32)
+    win = i32(STALE)
+    w_in = None if given == "none" else torch.from_numpy(old).to(DEV)
+    w_out = w_in if given == "in place" else torch.from_numpy(before).to(DEV)
+
+    def call():
+        mla.mla_attend_weight(shape, q, 0, c, win, None, SCALE, lse, None, w_in, w_out)
+
+    def check(windows):
+        none = np.zeros((wl.batch, 0, wl.n_heads, 1))
+        start = old if given == "in place" else before
+        ref = D.attend_weight(none, np.zeros((wl.batch, S, 1)), windows, None, SCALE, none, None,
+                              None if given == "none" else old, start)
+        np.testing.assert_array_equal(w_out.cpu().numpy(), ref.astype(np.float32))
+
+    call()
+    check(STALE)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    other = [(3, 12, 7), (0, 0, 3), (39, 40, 2), (1, 1, 1), (0, 5, 0)]
+    win.copy_(i32(other))
+    w_out.copy_(torch.from_numpy(old if given == "in place" else before))
+    graph.replay()
+    check(other)
+    assert mla.mla_device_error() == 0
