@@ -486,7 +486,8 @@ size_t mla_cache_evict_workspace_size(const mla_shape* shape);
  * mla_tree_accept — keep the accepted nodes of every sequence as context.  With
  * count = the accepted nodes among i < nodes of window[b]: nodes i < count that were not
  * accepted are overwritten, in ascending order, by the accepted nodes i >= count, in ascending
- * order (cached row, weight and position); then window[b] = {first, rows + count, 0}.
+ * order (cached row, weight and position); then window[b] = {first, rows + count, 0}, with first and
+ * rows as they were clipped (n_nodes = 0: count is 0, and the nodes a window still had are dropped).
  *
  *   accept   [B, n_nodes] bytes (non-zero: accepted)   read
  *   cache    [B, S, d_latent + d_rope]                 rows moved

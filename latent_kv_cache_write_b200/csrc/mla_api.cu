@@ -518,7 +518,8 @@ mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
   if (st != MLA_OK) return st;
   if (n_nodes < 0 || !accept) return MLA_ERR_ARG;
   if (n_nodes > g.S) return MLA_ERR_RANGE;
-  if (n_nodes == 0) return MLA_OK;
+  // without nodes the windows still drop the ones they had
+  if (n_nodes == 0 && !cuda_memory(window)) return MLA_OK;
   return cuda_status(tree_accept(g, shape->dtype == MLA_BF16, cache, n_nodes, accept, window,
                                  weight, position, workspace, (cudaStream_t)stream));
 }

@@ -58,3 +58,26 @@ def test_weight_without_nodes(cuda_ok, cfg, given):
     graph.replay()
     check(other)
     assert mla.mla_device_error() == 0
+
+
+@pytest.mark.parametrize("cfg", ["TINY", "MAIN"])
+def test_accept_without_nodes(cuda_ok, cfg):
+    """Windows keep their context and drop their nodes; rows, weights and positions stay."""
+    S, n = 40, 3
+    wl = T.workload(getattr(T, cfg), len(STALE), S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng(4)
+    c = T.normal(rng, (wl.batch, S, wl.row_width), wl.dtype)
+    wt = rng.random((wl.batch, S)).astype(np.float32)
+    pos = rng.integers(0, 999, (wl.batch, S))
+    ct, wd, pd, win = P.upload(c), torch.from_numpy(wt).to(DEV), i32(pos), i32(STALE)
+    ws = torch.empty(mla.mla_cache_evict_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    acc = torch.ones((wl.batch, n), dtype=torch.uint8, device=DEV)
+    mla.mla_tree_accept(shape, ct, 0, acc, win, wd, pd, ws)
+    rc, rw, rwt, rp = D.tree_accept(c.values, np.array(STALE), wt, pos,
+                                    np.zeros((wl.batch, 0), dtype=bool))
+    np.testing.assert_array_equal(win.cpu().numpy(), rw)
+    np.testing.assert_array_equal(P.download(ct), rc)
+    np.testing.assert_array_equal(wd.cpu().numpy(), rwt)
+    np.testing.assert_array_equal(pd.cpu().numpy(), rp)
+    assert mla.mla_device_error() == 0
