@@ -377,7 +377,8 @@ mla_status mla_attend_materialised(const mla_shape* shape, const void* q_nope,
  *
  * n_nodes is the stride of the per-node tensors and the most nodes a sequence can have; what a
  * sequence's nodes past its own count hold does not matter, and their results are left as they
- * were.  n_nodes = 0 is a call in which no sequence has a node, whatever its window says.
+ * were.  n_nodes = 0 is a call in which no sequence has a node, whatever its window says; its per-node
+ * tensors are empty and may be NULL.
  * The arrays named here and below by their element type (window, token, position, weights, lse)
  * need that type's alignment only; tree and accept are bytes.
  * The order of the context rows does not matter to the attention (a cached key carries its

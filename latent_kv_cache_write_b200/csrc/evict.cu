@@ -471,7 +471,9 @@ cudaError_t tree_accept(const Geo& g, bool bf, void* cache, int64_t n_nodes, con
                         int32_t* window, float* weight, int32_t* position, void* workspace,
                         cudaStream_t st) {
   EvictArgs a{};
-  a.S = g.S; a.n_nodes = n_nodes; a.accept = accept; a.window = window; a.cache = cache;
+  a.S = g.S; a.n_nodes = n_nodes; a.window = window; a.cache = cache;
+  // (null would mean eviction; without nodes no byte of it is read)
+  a.accept = accept ? accept : reinterpret_cast<const uint8_t*>(window);
   a.weight = weight; a.position = position; a.plan = make_plan(g, workspace);
   return run(g, bf, a, n_nodes / 2, st);
 }

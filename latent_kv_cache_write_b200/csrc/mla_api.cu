@@ -113,7 +113,7 @@ mla_status check_tree(const mla_shape* shape, Geo* g, const void* q_abs, int64_t
                       const void* cache, const int32_t* window, float softmax_scale) {
   mla_status st = check_shape(shape, g);
   if (st != MLA_OK) return st;
-  if (n_nodes < 0 || !q_abs || !cache || !window) return MLA_ERR_ARG;
+  if (n_nodes < 0 || (n_nodes > 0 && !q_abs) || !cache || !window) return MLA_ERR_ARG;
   if (!(softmax_scale > 0.f)) return MLA_ERR_ARG;
   if (n_nodes > g->S) return MLA_ERR_RANGE;
   if (n_nodes > 65535 || (int64_t)g->B * n_nodes * g->H > INT32_MAX) return MLA_ERR_UNSUPPORTED;
@@ -410,7 +410,8 @@ mla_status mla_tree_write(const mla_shape* shape, const void* h, int32_t d_model
   mla_status st = check_shape(shape, &g);
   if (st != MLA_OK) return st;
   if (d_model < 1 || n_nodes < 0) return MLA_ERR_ARG;
-  if (!h || !window || !token || !w_dkv || !cache || (g.Dr > 0 && !w_kr)) return MLA_ERR_ARG;
+  if (!window || !w_dkv || !cache || (g.Dr > 0 && !w_kr)) return MLA_ERR_ARG;
+  if (n_nodes > 0 && (!h || !token)) return MLA_ERR_ARG;
   if (n_nodes > g.S) return MLA_ERR_RANGE;
   if ((int64_t)g.B * n_nodes > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (!aligned16(h) || !aligned4(window) || !aligned4(token) || !aligned16(w_dkv) ||
@@ -433,8 +434,8 @@ mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const v
   Geo g;
   mla_status st = check_shape(shape, &g);
   if (st != MLA_OK) return st;
-  if (n_nodes < 0 || !q_nope || !token || !w_uk || !q_abs || (g.Dr > 0 && !q_rope))
-    return MLA_ERR_ARG;
+  if (n_nodes < 0 || !w_uk) return MLA_ERR_ARG;
+  if (n_nodes > 0 && (!q_nope || !token || !q_abs || (g.Dr > 0 && !q_rope))) return MLA_ERR_ARG;
   if (n_nodes > g.S) return MLA_ERR_RANGE;
   if (n_nodes > INT32_MAX / 2 || (int64_t)g.B * n_nodes * g.H > INT32_MAX)
     return MLA_ERR_UNSUPPORTED;
@@ -464,7 +465,7 @@ mla_status mla_attend_tree(const mla_shape* shape, const void* q_abs, int64_t n_
   Geo g;
   mla_status st = check_tree(shape, &g, q_abs, n_nodes, cache, window, softmax_scale);
   if (st != MLA_OK) return st;
-  if (!o_lat) return MLA_ERR_ARG;
+  if (n_nodes > 0 && !o_lat) return MLA_ERR_ARG;
   if (!aligned16(o_lat) || (lse && !aligned16(lse))) return MLA_ERR_ALIGN;
   const size_t need = mla_attend_tree_workspace_size(shape, n_nodes);
   if ((workspace || workspace_bytes > 0) && (!workspace || workspace_bytes < need))
@@ -487,7 +488,7 @@ mla_status mla_attend_weight(const mla_shape* shape, const void* q_abs, int64_t 
   Geo g;
   mla_status st = check_tree(shape, &g, q_abs, n_nodes, cache, window, softmax_scale);
   if (st != MLA_OK) return st;
-  if (!lse || !weight_out) return MLA_ERR_ARG;
+  if ((n_nodes > 0 && !lse) || !weight_out) return MLA_ERR_ARG;
   if (!aligned4(lse) || !aligned4(query_weight) || !aligned4(weight_in) || !aligned4(weight_out))
     return MLA_ERR_ALIGN;
   // without nodes the context's totals still go to weight_out
@@ -516,7 +517,7 @@ mla_status mla_tree_accept(const mla_shape* shape, void* cache, int64_t n_nodes,
   mla_status st = check_move(shape, &g, cache, window, weight, position, workspace,
                              workspace_bytes);
   if (st != MLA_OK) return st;
-  if (n_nodes < 0 || !accept) return MLA_ERR_ARG;
+  if (n_nodes < 0 || (n_nodes > 0 && !accept)) return MLA_ERR_ARG;
   if (n_nodes > g.S) return MLA_ERR_RANGE;
   // without nodes the windows still drop the ones they had
   if (n_nodes == 0 && !cuda_memory(window)) return MLA_OK;

@@ -81,3 +81,40 @@ def test_accept_without_nodes(cuda_ok, cfg):
     np.testing.assert_array_equal(wd.cpu().numpy(), rwt)
     np.testing.assert_array_equal(pd.cpu().numpy(), rp)
     assert mla.mla_device_error() == 0
+
+
+@pytest.mark.parametrize("cfg", ["TINY", "MAIN"])
+def test_step_without_nodes(cuda_ok, cfg):
+    """A whole step of a batch that drafts nothing, its per-node tensors empty: only the windows'
+    nodes go."""
+    S = 40
+    wl = T.workload(getattr(T, cfg), len(STALE), S)
+    shape = mla.make_shape(wl)
+    B, d, H = wl.batch, wl.d_model, wl.n_heads
+    rng = np.random.default_rng(4)
+    c = P.upload(T.normal(rng, (B, S, wl.row_width), wl.dtype))
+    empty = lambda *s: torch.empty(s, device=DEV, dtype=c.dtype)
+    wt, pos, win = torch.rand((B, S), device=DEV), i32(rng.integers(0, 99, (B, S))), i32(STALE)
+    before = [x.clone() for x in (c, wt, pos)]
+    out = torch.full((B, S), 7.0, device=DEV)
+    token, lse = i32(np.zeros((B, 0))), torch.empty((B, 0, H), device=DEV)
+    q, o = empty(B, 0, H, wl.row_width), empty(B, 0, H, wl.d_latent)
+    byte = torch.empty((B, 0), device=DEV, dtype=torch.uint8)
+    ews = torch.empty(mla.mla_cache_evict_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    w_uk = empty(H, wl.d_nope, wl.d_latent)
+    mla.mla_tree_write(shape, empty(B, 0, d), d, 0, win, token, empty(d, wl.d_latent),
+                       empty(d, wl.d_rope), c, pos)
+    mla.mla_tree_absorb_q(shape, empty(B, 0, H, wl.d_nope), empty(B, 0, H, wl.d_rope), 0, token, w_uk,
+                          q)
+    mla.mla_attend_tree(shape, q, 0, c, win, byte, SCALE, o, lse)
+    mla.mla_attend_weight(shape, q, 0, c, win, byte, SCALE, lse, lse[:, :, 0], wt, out)
+    mla.mla_tree_accept(shape, c, 0, byte, win, wt, pos, ews)
+    for x, y in zip(before, (c, wt, pos)):
+        assert torch.equal(x, y)
+    for b, w in enumerate(STALE):
+        first, rows, _ = D.clip_window(w, S, 0)
+        assert win[b].tolist() == [first, rows, 0]
+        at = torch.tensor(D.slots(first, rows, S), device=DEV, dtype=torch.long)
+        assert torch.equal(out[b, at], wt[b, at])
+        assert (out[b] == 7.0).sum() == S - rows
+    assert mla.mla_device_error() == 0
