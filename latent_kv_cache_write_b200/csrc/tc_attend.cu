@@ -1571,8 +1571,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
       named_bar(3, 2 * TM);
       const float mf = fmaxf(m_last, m_sh[(wg ^ 1) * TM + t]);
       named_bar(3, 2 * TM);
-      // (TREE: a NaN maximum or sum stays NaN)
-      const bool some = TREE ? m_last != -INFINITY : m_last > -INFINITY;
+      // (TREE: a NaN maximum or sum stays NaN.  A maximum passes over NaN, so the sum may be NaN next to
+      // a maximum of -inf: every key seen here was NaN)
+      const bool some = TREE ? m_last != -INFINITY || l != 0.f : m_last > -INFINITY;
       m_sh[wg * TM + t] = some ? l * ex2(m_last - mf) : 0.f;
       named_bar(3, 2 * TM);
       const float lt = m_sh[t] + m_sh[TM + t];

@@ -9,7 +9,7 @@ import latent_kv_cache_write_b200 as mla
 from oracle import draft_tree as D
 from tests import gpu_path as P
 from tests import tree_cases as T
-from tests.test_tree_gpu import SCALE, i32
+from tests.test_tree_gpu import SCALE, attend, i32, tree_dev
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -118,3 +118,45 @@ def test_step_without_nodes(cuda_ok, cfg):
         assert torch.equal(out[b, at], wt[b, at])
         assert (out[b] == 7.0).sum() == S - rows
     assert mla.mla_device_error() == 0
+
+
+# windows, rows (logical) that are NaN: a node that sees itself only, blocks of one warpgroup, blocks
+# of both, the last piece of a split tile (contexts of whole blocks), its first
+NANS = [
+    ("TINY", 4, 64, [(0, 0, 4), (60, 8, 4), (3, 40, 2)], [[0], [9, 11], range(40)]),
+    ("MAIN", 4, 300, [(290, 0, 4), (0, 64, 4), (5, 128, 4), (9, 128, 4), (2, 192, 4)],
+     [[0], [64, 66], range(64), range(64, 128), range(128)]),
+    ("HEADS", 1, 2700, [(7, 2624, 1)], [[2624]]),
+    ("HEADS", 1, 2700, [(7, 2624, 1)], [range(64)]),
+    ("WIDE", 4, 300, [(290, 0, 4), (0, 64, 4), (5, 128, 4), (9, 128, 4)],
+     [[0], [64, 66], range(64), range(64, 128)]),
+    ("WIDE", 2, 2700, [(7, 2624, 2)], [[2624]]),
+]
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("cfg,n,S,windows,bad", NANS)
+def test_nan_rows_reach_those_who_see_them(cuda_ok, cfg, n, S, windows, bad, split):
+    """o_lat and lse are NaN for the nodes that see a NaN row, whatever else of the row's block they
+    see, and for no others."""
+    wl = T.workload(getattr(T, cfg), len(windows), S)
+    rng = np.random.default_rng(S)
+    q = T.normal(rng, (wl.batch, n, wl.n_heads, wl.row_width), wl.dtype)
+    c = T.normal(rng, (wl.batch, S, wl.row_width), wl.dtype)
+    see = np.tile(np.eye(n, dtype=bool), (wl.batch, 1, 1))         # every node sees itself only
+    ct, cv = P.upload(c), c.values.copy()
+    for b, (f, _, _) in enumerate(windows):
+        at = [(f + j) % S for j in bad[b]]
+        ct[b, at] = float("nan")
+        cv[b, at] = np.nan
+    o, lse = attend(wl, P.upload(q), ct, windows, tree_dev(see), n, split)
+    ref, rl, spread = D.attend_tree(q.values, cv, windows, see, SCALE, wl.d_latent)
+    got, gl = P.download(o), P.download(lse)
+    for b, (f, r, m) in enumerate(windows):
+        assert (np.isnan(gl[b, :m]) == np.isnan(rl[b, :m])).all()
+        assert (np.isnan(got[b, :m]) == np.isnan(ref[b, :m])).all()
+        ok = ~np.isnan(rl[b, :m])
+        if ok.any():
+            ds = T.score_error(q.values[b, :m], np.nan_to_num(cv[b]), SCALE)
+            tol = T.attend_tolerance(spread[b, :m], ref[b, :m], r + m, ds, wl.dtype)
+            T.check_within(got[b, :m][ok], ref[b, :m][ok], tol[ok], "o")
