@@ -178,18 +178,19 @@ def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _arg(t, item: int, current: int) -> Optional[int]:
-    """Device pointer of a tensor whose elements have ``item`` bytes (0: any, for a workspace).  A
-    tensor of the host or of another device than ``current``, the current one, one with strides of
-    its own, and one of another element size raise ValueError: the library sees pointers only."""
+def _arg(t, elem, current: int) -> Optional[int]:
+    """Device pointer of a tensor whose elements are ``elem``: a dtype, or any of so many bytes (0:
+    of any size, for a workspace).  A tensor of the host or of another device than ``current``, the
+    current one, one with strides of its own, and one of other elements raise ValueError: the library
+    sees pointers only."""
     if t is None or isinstance(t, int):
         return t
-    if (t.get_device() == current and (not item or t.element_size() == item)
-            and t.is_contiguous()):
+    if (t.get_device() == current and t.is_contiguous()
+            and (not elem or elem == (t.element_size() if isinstance(elem, int) else t.dtype))):
         return t.data_ptr()
-    raise ValueError(f"a contiguous tensor with {item or 'any'}-byte elements on cuda:{current}, "
-                     f"the current device, is needed, not {t.dtype} {tuple(t.shape)} with strides "
-                     f"{t.stride()} on {t.device}")
+    what = f"{elem or 'any'}-byte elements" if isinstance(elem, int) else f"{elem} elements"
+    raise ValueError(f"a contiguous tensor with {what} on cuda:{current}, the current device, is "
+                     f"needed, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _current_device() -> int:
@@ -197,25 +198,28 @@ def _current_device() -> int:
     return torch.cuda.current_device()
 
 
-def _item(shape: MlaShape) -> int:
-    return 2 if shape.dtype == native.MLA_BF16 else 4
+def _kinds(shape: MlaShape):
+    """The dtypes of the storage tensors, of the integer and of the float32 arrays."""
+    import torch
+    return (torch.bfloat16 if shape.dtype == native.MLA_BF16 else torch.float32, torch.int32,
+            torch.float32)
 
 
 def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
                    cache, position=None, stream=None) -> None:
-    dev, item = _current_device(), _item(shape)
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_tree_write", native.lib().mla_tree_write(
-        ctypes.byref(shape), _arg(h, item, dev), d_model, n_nodes, _arg(window, 4, dev),
-        _arg(token, 4, dev), _arg(w_dkv, item, dev), _arg(w_kr, item, dev),
-        _arg(cache, item, dev), _arg(position, 4, dev), _stream(stream)))
+        ctypes.byref(shape), _arg(h, el, dev), d_model, n_nodes, _arg(window, i32, dev),
+        _arg(token, i32, dev), _arg(w_dkv, el, dev), _arg(w_kr, el, dev),
+        _arg(cache, el, dev), _arg(position, i32, dev), _stream(stream)))
 
 
 def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
                       stream=None) -> None:
-    dev, item = _current_device(), _item(shape)
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
-        ctypes.byref(shape), _arg(q_nope, item, dev), _arg(q_rope, item, dev), n_nodes,
-        _arg(token, 4, dev), _arg(w_uk, item, dev), _arg(q_abs, item, dev), _stream(stream)))
+        ctypes.byref(shape), _arg(q_nope, el, dev), _arg(q_rope, el, dev), n_nodes,
+        _arg(token, i32, dev), _arg(w_uk, el, dev), _arg(q_abs, el, dev), _stream(stream)))
 
 
 def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
@@ -225,22 +229,22 @@ def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
 def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                     softmax_scale: float, o_lat, lse=None, workspace=None,
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
-    dev, item = _current_device(), _item(shape)
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_attend_tree", native.lib().mla_attend_tree(
-        ctypes.byref(shape), _arg(q_abs, item, dev), n_nodes, _arg(cache, item, dev),
-        _arg(window, 4, dev), _arg(tree, 1, dev), softmax_scale, _arg(o_lat, item, dev),
-        _arg(lse, 4, dev), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
+        ctypes.byref(shape), _arg(q_abs, el, dev), n_nodes, _arg(cache, el, dev),
+        _arg(window, i32, dev), _arg(tree, 1, dev), softmax_scale, _arg(o_lat, el, dev),
+        _arg(lse, f32, dev), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
         _stream(stream)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                       softmax_scale: float, lse, query_weight, weight_in, weight_out,
                       stream=None) -> None:
-    dev, item = _current_device(), _item(shape)
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_attend_weight", native.lib().mla_attend_weight(
-        ctypes.byref(shape), _arg(q_abs, item, dev), n_nodes, _arg(cache, item, dev),
-        _arg(window, 4, dev), _arg(tree, 1, dev), softmax_scale, _arg(lse, 4, dev),
-        _arg(query_weight, 4, dev), _arg(weight_in, 4, dev), _arg(weight_out, 4, dev),
+        ctypes.byref(shape), _arg(q_abs, el, dev), n_nodes, _arg(cache, el, dev),
+        _arg(window, i32, dev), _arg(tree, 1, dev), softmax_scale, _arg(lse, f32, dev),
+        _arg(query_weight, f32, dev), _arg(weight_in, f32, dev), _arg(weight_out, f32, dev),
         _stream(stream)))
 
 
@@ -250,20 +254,20 @@ def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
 
 def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
-    dev = _current_device()
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
-        ctypes.byref(shape), _arg(cache, _item(shape), dev), n_nodes, _arg(accept, 1, dev),
-        _arg(window, 4, dev), _arg(weight, 4, dev), _arg(position, 4, dev),
+        ctypes.byref(shape), _arg(cache, el, dev), n_nodes, _arg(accept, 1, dev),
+        _arg(window, i32, dev), _arg(weight, f32, dev), _arg(position, i32, dev),
         _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
                     weight, position, workspace, workspace_bytes: Optional[int] = None,
                     stream=None) -> None:
-    dev = _current_device()
+    dev, (el, i32, f32) = _current_device(), _kinds(shape)
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
-        ctypes.byref(shape), _arg(cache, _item(shape), dev), n_keep, n_sink, n_recent,
-        _arg(window, 4, dev), _arg(weight, 4, dev), _arg(position, 4, dev),
+        ctypes.byref(shape), _arg(cache, el, dev), n_keep, n_sink, n_recent,
+        _arg(window, i32, dev), _arg(weight, f32, dev), _arg(position, i32, dev),
         _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
 
 
