@@ -41,6 +41,7 @@ low-bit ring.  Errors raise ``MlaError`` with the library's status.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 from . import native
@@ -66,11 +67,10 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, current: Optional[int] = None) -> Optional[int]:
     if stream is None:
-        import torch
         # the handle alone: building a Stream object takes longer than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _cuda()._cuda_getCurrentRawStream(_current_device() if current is None else current)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -178,48 +178,69 @@ def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _arg(t, elem, current: int) -> Optional[int]:
-    """Device pointer of a tensor whose elements are ``elem``: a dtype, or any of so many bytes (0:
-    of any size, for a workspace).  A tensor of the host or of another device than ``current``, the
-    current one, one with strides of its own, and one of other elements raise ValueError: the library
-    sees pointers only."""
-    if t is None or isinstance(t, int):
+def _arg(t, elem, current: int, count: int = 0) -> Optional[int]:
+    """Device pointer of a tensor of at least ``count`` elements that are ``elem``: a dtype, or any of
+    so many bytes (0: of any size, for a workspace).  A tensor of the host or of another device than
+    ``current``, the current one, one with strides of its own, one that is too short, and one of
+    other elements raise ValueError: the library sees pointers only."""
+    if t is None or type(t) is int:
         return t
-    if (t.get_device() == current and t.is_contiguous()
-            and (not elem or elem == (t.element_size() if isinstance(elem, int) else t.dtype))):
+    if ((t.dtype is elem or elem == 0 or elem == t.element_size()) and t.get_device() == current
+            and t.is_contiguous() and (not count or t.numel() >= count)):
         return t.data_ptr()
     what = f"{elem or 'any'}-byte elements" if isinstance(elem, int) else f"{elem} elements"
-    raise ValueError(f"a contiguous tensor with {what} on cuda:{current}, the current device, is "
-                     f"needed, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    raise ValueError(f"a contiguous tensor with {what} ({count} at least) on cuda:{current}, the "
+                     f"current device, is needed, not {t.dtype} {tuple(t.shape)} with strides "
+                     f"{t.stride()} on {t.device}")
 
 
 def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    # (short calls are bound by what the host does for each: no more than it has to)
+    return _cuda()._cuda_getDevice()
 
 
-def _kinds(shape: MlaShape):
-    """The dtypes of the storage tensors, of the integer and of the float32 arrays."""
+@functools.lru_cache(None)
+def _cuda():
     import torch
-    return (torch.bfloat16 if shape.dtype == native.MLA_BF16 else torch.float32, torch.int32,
+    torch.cuda.init()
+    return torch._C
+
+
+@functools.lru_cache(None)
+def _kinds(dtype: int):
+    """The dtypes of a shape's storage tensors, of the integer and of the float32 arrays."""
+    import torch
+    return (torch.bfloat16 if dtype == native.MLA_BF16 else torch.float32, torch.int32,
             torch.float32)
+
+
+def _ring(shape: MlaShape):
+    """Elements of a [B, S] array and of the cache."""
+    slots = shape.batch * shape.ring_slots
+    return slots, slots * (shape.d_latent + shape.d_rope)
 
 
 def mla_tree_write(shape: MlaShape, h, d_model: int, n_nodes: int, window, token, w_dkv, w_kr,
                    cache, position=None, stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32), (slots, ring) = _current_device(), _kinds(shape.dtype), _ring(shape)
+    B = shape.batch
     native.check("mla_tree_write", native.lib().mla_tree_write(
-        ctypes.byref(shape), _arg(h, el, dev), d_model, n_nodes, _arg(window, i32, dev),
-        _arg(token, i32, dev), _arg(w_dkv, el, dev), _arg(w_kr, el, dev),
-        _arg(cache, el, dev), _arg(position, i32, dev), _stream(stream)))
+        ctypes.byref(shape), _arg(h, el, dev, B * n_nodes * d_model), d_model, n_nodes,
+        _arg(window, i32, dev, 3 * B), _arg(token, i32, dev, B * n_nodes),
+        _arg(w_dkv, el, dev, d_model * shape.d_latent), _arg(w_kr, el, dev, d_model * shape.d_rope),
+        _arg(cache, el, dev, ring), _arg(position, i32, dev, slots), _stream(stream, dev)))
 
 
 def mla_tree_absorb_q(shape: MlaShape, q_nope, q_rope, n_nodes: int, token, w_uk, q_abs,
                       stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32) = _current_device(), _kinds(shape.dtype)
+    rows, dn, dc, dr = (shape.batch * n_nodes * shape.n_heads, shape.d_nope, shape.d_latent,
+                        shape.d_rope)
     native.check("mla_tree_absorb_q", native.lib().mla_tree_absorb_q(
-        ctypes.byref(shape), _arg(q_nope, el, dev), _arg(q_rope, el, dev), n_nodes,
-        _arg(token, i32, dev), _arg(w_uk, el, dev), _arg(q_abs, el, dev), _stream(stream)))
+        ctypes.byref(shape), _arg(q_nope, el, dev, rows * dn), _arg(q_rope, el, dev, rows * dr),
+        n_nodes, _arg(token, i32, dev, shape.batch * n_nodes),
+        _arg(w_uk, el, dev, shape.n_heads * dn * dc), _arg(q_abs, el, dev, rows * (dc + dr)),
+        _stream(stream, dev)))
 
 
 def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
@@ -229,23 +250,27 @@ def mla_attend_tree_workspace_size(shape: MlaShape, n_nodes: int) -> int:
 def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                     softmax_scale: float, o_lat, lse=None, workspace=None,
                     workspace_bytes: Optional[int] = None, stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32), (slots, ring) = _current_device(), _kinds(shape.dtype), _ring(shape)
+    B, rows, dc = shape.batch, shape.batch * n_nodes * shape.n_heads, shape.d_latent
     native.check("mla_attend_tree", native.lib().mla_attend_tree(
-        ctypes.byref(shape), _arg(q_abs, el, dev), n_nodes, _arg(cache, el, dev),
-        _arg(window, i32, dev), _arg(tree, 1, dev), softmax_scale, _arg(o_lat, el, dev),
-        _arg(lse, f32, dev), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
-        _stream(stream)))
+        ctypes.byref(shape), _arg(q_abs, el, dev, rows * (dc + shape.d_rope)), n_nodes,
+        _arg(cache, el, dev, ring), _arg(window, i32, dev, 3 * B),
+        _arg(tree, 1, dev, B * n_nodes * n_nodes), softmax_scale, _arg(o_lat, el, dev, rows * dc),
+        _arg(lse, f32, dev, rows), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
+        _stream(stream, dev)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
                       softmax_scale: float, lse, query_weight, weight_in, weight_out,
                       stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32), (slots, ring) = _current_device(), _kinds(shape.dtype), _ring(shape)
+    B, rows = shape.batch, shape.batch * n_nodes * shape.n_heads
     native.check("mla_attend_weight", native.lib().mla_attend_weight(
-        ctypes.byref(shape), _arg(q_abs, el, dev), n_nodes, _arg(cache, el, dev),
-        _arg(window, i32, dev), _arg(tree, 1, dev), softmax_scale, _arg(lse, f32, dev),
-        _arg(query_weight, f32, dev), _arg(weight_in, f32, dev), _arg(weight_out, f32, dev),
-        _stream(stream)))
+        ctypes.byref(shape), _arg(q_abs, el, dev, rows * (shape.d_latent + shape.d_rope)), n_nodes,
+        _arg(cache, el, dev, ring), _arg(window, i32, dev, 3 * B),
+        _arg(tree, 1, dev, B * n_nodes * n_nodes), softmax_scale, _arg(lse, f32, dev, rows),
+        _arg(query_weight, f32, dev, B * n_nodes), _arg(weight_in, f32, dev, slots),
+        _arg(weight_out, f32, dev, slots), _stream(stream, dev)))
 
 
 def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
@@ -254,21 +279,24 @@ def mla_cache_evict_workspace_size(shape: MlaShape) -> int:
 
 def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight, position,
                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32), (slots, ring) = _current_device(), _kinds(shape.dtype), _ring(shape)
+    B = shape.batch
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
-        ctypes.byref(shape), _arg(cache, el, dev), n_nodes, _arg(accept, 1, dev),
-        _arg(window, i32, dev), _arg(weight, f32, dev), _arg(position, i32, dev),
-        _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
+        ctypes.byref(shape), _arg(cache, el, dev, ring), n_nodes,
+        _arg(accept, 1, dev, B * n_nodes), _arg(window, i32, dev, 3 * B),
+        _arg(weight, f32, dev, slots), _arg(position, i32, dev, slots), _arg(workspace, 0, dev),
+        _bytes(workspace, workspace_bytes), _stream(stream, dev)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
                     weight, position, workspace, workspace_bytes: Optional[int] = None,
                     stream=None) -> None:
-    dev, (el, i32, f32) = _current_device(), _kinds(shape)
+    dev, (el, i32, f32), (slots, ring) = _current_device(), _kinds(shape.dtype), _ring(shape)
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
-        ctypes.byref(shape), _arg(cache, el, dev), n_keep, n_sink, n_recent,
-        _arg(window, i32, dev), _arg(weight, f32, dev), _arg(position, i32, dev),
-        _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes), _stream(stream)))
+        ctypes.byref(shape), _arg(cache, el, dev, ring), n_keep, n_sink, n_recent,
+        _arg(window, i32, dev, 3 * shape.batch), _arg(weight, f32, dev, slots),
+        _arg(position, i32, dev, slots), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
+        _stream(stream, dev)))
 
 
 def mla_kernel_launches() -> int:

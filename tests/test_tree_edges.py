@@ -108,3 +108,16 @@ def test_binding_refuses_other_dtypes(reached, name, dtype):
         if v.dtype == U8:
             bind(name, s, dict(tensors(s, name), **{k: Fake(torch.bool, *v.size)}))
     assert set(reached) == {name}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_binding_refuses_short_tensors(reached, name):
+    """One element less than the call reads or writes; longer ones (a batch's largest) pass."""
+    s = shape(ring_slots=300, batch=2)
+    for k, v in tensors(s, name).items():
+        if k == "ws":
+            continue
+        with pytest.raises(ValueError, match="needed"):
+            bind(name, s, dict(tensors(s, name), **{k: Fake(v.dtype, math.prod(v.size) - 1)}))
+        bind(name, s, dict(tensors(s, name), **{k: Fake(v.dtype, math.prod(v.size) + 7)}))
+    assert set(reached) == {name}
