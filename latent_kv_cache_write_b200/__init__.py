@@ -172,12 +172,6 @@ def mla_up_v(shape: MlaShape, o_lat, n_q: int, w_uv, out, stream=None) -> None:
         ctypes.byref(shape), _ptr(o_lat), n_q, _ptr(w_uv), _ptr(out), _stream(stream)))
 
 
-def _bytes(workspace, workspace_bytes: Optional[int]) -> int:
-    if workspace_bytes is not None:
-        return workspace_bytes
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
 def _arg(t, elem, current: int, count: int = 0) -> Optional[int]:
     """Device pointer of a tensor of at least ``count`` elements that are ``elem``: a dtype, or any of
     so many bytes (0: of any size, for a workspace).  A tensor of the host or of another device than
@@ -212,6 +206,22 @@ def _kinds(dtype: int):
     import torch
     return (torch.bfloat16 if dtype == native.MLA_BF16 else torch.float32, torch.int32,
             torch.float32)
+
+
+def _work(workspace, workspace_bytes: Optional[int], current: int):
+    """Pointer and size of a workspace: all of a tensor unless a size is given, which then has to be
+    inside it; a raw pointer needs a size."""
+    if workspace is None or type(workspace) is int:
+        if workspace_bytes is None and workspace is not None:
+            raise ValueError("a workspace given as a pointer needs workspace_bytes")
+        size = workspace_bytes = workspace_bytes or 0
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace_bytes is None:
+            workspace_bytes = size
+    if not 0 <= workspace_bytes <= size:
+        raise ValueError(f"workspace_bytes is {workspace_bytes}, the workspace has {size} bytes")
+    return _arg(workspace, 0, current), workspace_bytes
 
 
 def _ring(shape: MlaShape):
@@ -256,8 +266,7 @@ def mla_attend_tree(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
         ctypes.byref(shape), _arg(q_abs, el, dev, rows * (dc + shape.d_rope)), n_nodes,
         _arg(cache, el, dev, ring), _arg(window, i32, dev, 3 * B),
         _arg(tree, 1, dev, B * n_nodes * n_nodes), softmax_scale, _arg(o_lat, el, dev, rows * dc),
-        _arg(lse, f32, dev, rows), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
-        _stream(stream, dev)))
+        _arg(lse, f32, dev, rows), *_work(workspace, workspace_bytes, dev), _stream(stream, dev)))
 
 
 def mla_attend_weight(shape: MlaShape, q_abs, n_nodes: int, cache, window, tree,
@@ -284,8 +293,8 @@ def mla_tree_accept(shape: MlaShape, cache, n_nodes: int, accept, window, weight
     native.check("mla_tree_accept", native.lib().mla_tree_accept(
         ctypes.byref(shape), _arg(cache, el, dev, ring), n_nodes,
         _arg(accept, 1, dev, B * n_nodes), _arg(window, i32, dev, 3 * B),
-        _arg(weight, f32, dev, slots), _arg(position, i32, dev, slots), _arg(workspace, 0, dev),
-        _bytes(workspace, workspace_bytes), _stream(stream, dev)))
+        _arg(weight, f32, dev, slots), _arg(position, i32, dev, slots),
+        *_work(workspace, workspace_bytes, dev), _stream(stream, dev)))
 
 
 def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: int, window,
@@ -295,8 +304,8 @@ def mla_cache_evict(shape: MlaShape, cache, n_keep: int, n_sink: int, n_recent: 
     native.check("mla_cache_evict", native.lib().mla_cache_evict(
         ctypes.byref(shape), _arg(cache, el, dev, ring), n_keep, n_sink, n_recent,
         _arg(window, i32, dev, 3 * shape.batch), _arg(weight, f32, dev, slots),
-        _arg(position, i32, dev, slots), _arg(workspace, 0, dev), _bytes(workspace, workspace_bytes),
-        _stream(stream, dev)))
+        _arg(position, i32, dev, slots),
+        *_work(workspace, workspace_bytes, dev), _stream(stream, dev)))
 
 
 def mla_kernel_launches() -> int:

@@ -121,3 +121,26 @@ def test_binding_refuses_short_tensors(reached, name):
             bind(name, s, dict(tensors(s, name), **{k: Fake(v.dtype, math.prod(v.size) - 1)}))
         bind(name, s, dict(tensors(s, name), **{k: Fake(v.dtype, math.prod(v.size) + 7)}))
     assert set(reached) == {name}
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if "ws" in CALLS[n]])
+def test_binding_workspaces(reached, name):
+    """A raw pointer needs a size, and a size has to lie inside the tensor."""
+    s = shape(ring_slots=300, batch=2)
+    args = {k: v for k, v in tensors(s, name).items() if k != "ws"}
+    numbers = dict(n=N, scale=0.07, keep=4, sink=0, recent=0)
+    head = [args.get(k, numbers.get(k)) for k in CALLS[name] if k not in ("ws", "ws_bytes")]
+    run = lambda ws, size=None: getattr(mla, name)(s, *head, ws, size, stream=0)  # noqa: E731
+    with pytest.raises(ValueError, match="needs workspace_bytes"):
+        run(FAKE)
+    with pytest.raises(ValueError, match="has 64 bytes"):
+        run(Fake(U8, 64), 65)
+    for ws in (FAKE, Fake(U8, 64), None):
+        with pytest.raises(ValueError):
+            run(ws, -1)                                 # (no size_t)
+    assert not reached
+    run(FAKE, 64)
+    run(Fake(U8, 64), 63)
+    run(Fake(F32, 16))
+    run(None)
+    assert reached == [name] * 4
