@@ -424,7 +424,8 @@ mla_status mla_tree_absorb_q(const mla_shape* shape, const void* q_nope, const v
 
 /*
  * mla_attend_tree_workspace_size — bytes of device workspace that lets mla_attend_tree split
- * a tile's keys across SMs (as mla_attend_workspace_size).  May be 0.
+ * a tile's keys across SMs (as mla_attend_workspace_size; the partial outputs are float32).  May be
+ * 0.
  */
 size_t mla_attend_tree_workspace_size(const mla_shape* shape, int64_t n_nodes);
 

@@ -1,6 +1,6 @@
 // Merge of the split-key partials of the tensor-core attention: a tile whose key blocks
-// were cut between clusters left one normalised bf16 partial output and one fp32
-// log-sum-exp per CTA half for each piece in the workspace.
+// were cut between clusters left one normalised partial output (bf16; of draft trees float32)
+// and one fp32 log-sum-exp per CTA half for each piece in the workspace.
 #include "attend_common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
@@ -21,9 +21,10 @@ using tc::pack_bf16;
 // that computed it.
 //
 // Row r of the tile (if row_ok) becomes row grow of the outputs; piece p of np is in workspace
-// slot slot(p).  NANS: a NaN piece makes the row NaN (draft trees: a node that sees a NaN row),
-// otherwise it counts as empty.
-template <int CSPLIT, bool NANS, typename Slot>
+// slot slot(p).  TREE: the pieces are float32, so that a row is rounded once however many pieces it
+// came in, and a NaN piece makes the row NaN (a node that sees a NaN row); otherwise they are bf16, and
+// a NaN piece counts as empty.
+template <int CSPLIT, bool TREE, typename Slot>
 __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_lse, float* red,
                                             int rr, int part, int lane, int r, bool row_ok,
                                             int64_t grow, int np, const Slot& slot) {
@@ -38,7 +39,7 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
       const float l1 = ws_lse[((int64_t)slot(p) * 2 + 1) * TM + r];
       m0 = fmaxf(m0, l0);
       m1 = fmaxf(m1, l1);
-      if (NANS) nan = nan || l0 != l0 || l1 != l1;
+      if (TREE) nan = nan || l0 != l0 || l1 != l1;
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -46,23 +47,33 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
   float mx = half ? m1 : m0;
-  if (NANS && __any_sync(0xffffffffu, nan) && mx == -INFINITY) mx = 0.f;
+  if (TREE && __any_sync(0xffffffffu, nan) && mx == -INFINITY) mx = 0.f;
   const float* lse_h = ws_lse + half * TM + r;   // + slot * 2 * TM
   float acc[16];
 #pragma unroll
   for (int q = 0; q < 16; ++q) acc[q] = 0.f;
   float wsum = 0.f;
-  // a piece's 16 dims of this lane: two 16-byte vectors of bf16
-  auto add = [&](float lp, const uint4 (&v)[2]) {
-    const float w = (NANS ? lp != -INFINITY : lp > -INFINITY) ? expf(lp - mx) : 0.f;
+  // a piece's 16 dims of this lane: 16-byte vectors of bf16 or float32
+  constexpr int NV = TREE ? 4 : 2;
+  auto vectors = [&](int64_t ps) {
+    const int64_t at = (ps * TM + r) * a.g.Dc + d;
+    return TREE ? reinterpret_cast<const uint4*>(a.ws_f + at)
+                : reinterpret_cast<const uint4*>(a.ws_o + at);
+  };
+  auto add = [&](float lp, const uint4 (&v)[NV]) {
+    const float w = (TREE ? lp != -INFINITY : lp > -INFINITY) ? expf(lp - mx) : 0.f;
     wsum += w;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < NV; ++q) {
       const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        acc[8 * q + 2 * e] += w * __uint_as_float(u[e] << 16);
-        acc[8 * q + 2 * e + 1] += w * __uint_as_float(u[e] & 0xffff0000u);
+        if constexpr (TREE) {
+          acc[4 * q + e] += w * __uint_as_float(u[e]);
+        } else {
+          acc[8 * q + 2 * e] += w * __uint_as_float(u[e] << 16);
+          acc[8 * q + 2 * e + 1] += w * __uint_as_float(u[e] & 0xffff0000u);
+        }
       }
     }
   };
@@ -71,25 +82,25 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
     if constexpr (CSPLIT > 1) {
       for (; p + 3 * CSPLIT < np; p += 4 * CSPLIT) {
         float lp[4];
-        uint4 v[4][2];
+        uint4 v[4][NV];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int64_t pu = slot(p + u * CSPLIT);
           lp[u] = lse_h[pu * 2 * TM];
-          const uint4* o = reinterpret_cast<const uint4*>(a.ws_o + (pu * TM + r) * a.g.Dc + d);
+          const uint4* o = vectors(pu);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) v[u][q] = o[q];
+          for (int q = 0; q < NV; ++q) v[u][q] = o[q];
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) add(lp[u], v[u]);
       }
     }
     for (; p < np; p += CSPLIT) {
-      uint4 v[2];
+      uint4 v[NV];
       const int64_t ps = slot(p);
-      const uint4* o = reinterpret_cast<const uint4*>(a.ws_o + (ps * TM + r) * a.g.Dc + d);
+      const uint4* o = vectors(ps);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) v[q] = o[q];
+      for (int q = 0; q < NV; ++q) v[q] = o[q];
       add(lse_h[ps * 2 * TM], v);
     }
   }
@@ -109,7 +120,7 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
   } else {
     if (!row_ok) return;
   }
-  const bool any = NANS ? wsum != 0.f : wsum > 0.f;
+  const bool any = TREE ? wsum != 0.f : wsum > 0.f;
   const float inv = any ? 1.f / wsum : 0.f;
   uint4* dst = reinterpret_cast<uint4*>(a.o_lat + grow * a.g.Dc + d);
 #pragma unroll

@@ -20,6 +20,7 @@ struct AttnArgs {
   bf16* o_lat;
   float* lse;
   bf16* ws_o;               // partial outputs [slot][TM][Dc], bf16, normalised by their l
+  float* ws_f;              // draft trees: the same in float32
   float* ws_lse;            // their natural log-sum-exps, one per CTA half [slot][2][TM]
   int tiles_per_batch;
   int bn;                   // keys per block of the launch

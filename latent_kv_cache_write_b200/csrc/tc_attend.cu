@@ -1599,6 +1599,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = 0u;
         }
+        const int k = t & 3;
+        if constexpr (TREE) {
+          if (part) {
+            // the normalised rows of a piece, in float32: the merge rounds their sum once
+            float* dst = a.ws_f + ((int64_t)ws_slot * TM + (t - k)) * G.Dc + rank * HALF + c + 4 * k;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4 w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                w[q] = make_uint4(__float_as_uint(__uint_as_float(v[16 * h + 4 * q]) * inv),
+                                  __float_as_uint(__uint_as_float(v[16 * h + 4 * q + 1]) * inv),
+                                  __float_as_uint(__uint_as_float(v[16 * h + 4 * q + 2]) * inv),
+                                  __float_as_uint(__uint_as_float(v[16 * h + 4 * q + 3]) * inv));
+              quad_transpose(w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (live_rows >> j & 1)
+                  *reinterpret_cast<uint4*>(dst + j * G.Dc + 16 * h) = w[j];
+            }
+            continue;
+          }
+        }
         // the normalised rows in bf16: a final output, or a partial that the merge adds in fp32
         uint4 w[4];
 #pragma unroll
@@ -1609,8 +1632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<V>::NT, 1)
               pack_bf16(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv),
               pack_bf16(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
         quad_transpose(w);
-        const int k = t & 3;
-        bf16* dst = (part ? a.ws_o + ((int64_t)ws_slot * TM + (t - k)) * G.Dc
+        bf16* dst = (!TREE && part ? a.ws_o + ((int64_t)ws_slot * TM + (t - k)) * G.Dc
                           : a.o_lat + (grow - k) * G.Dc) + rank * HALF + c + 8 * k;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -1969,7 +1991,8 @@ bool tc_attend_tree_supported(const Geo& g, int64_t n_nodes) {
 }
 
 size_t tc_attend_tree_workspace(const Geo& g) {
-  return tc_attend_workspace(g) + MAXC * sizeof(int4);
+  // two slots per cluster: float32 rows, their log-sum-exps per CTA half; then the cuts
+  return 2 * (size_t)cluster_slots() * TM * ((size_t)g.Dc + 2) * sizeof(float) + MAXC * sizeof(int4);
 }
 
 cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, const void* cache,
@@ -2011,9 +2034,9 @@ cudaError_t tc_attend_tree(const Geo& g, const void* q_abs, int64_t n_nodes, con
       sc.l2_blocks = (uint32_t)(l2 / 3 / ((int64_t)a.bn * g.row * 2));
   }
   if (sc.split) {
-    a.ws_o = (bf16*)workspace;
-    a.ws_lse = reinterpret_cast<float*>(a.ws_o + (size_t)2 * ncl * TM * g.Dc);
-    a.cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + tc_attend_workspace(g));
+    a.ws_f = static_cast<float*>(workspace);
+    a.ws_lse = a.ws_f + (size_t)2 * ncl * TM * g.Dc;
+    a.cuts = reinterpret_cast<int4*>(a.ws_lse + (size_t)2 * ncl * 2 * TM);
   }
   cudaError_t e;
   if (wide)

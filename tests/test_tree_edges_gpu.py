@@ -160,3 +160,27 @@ def test_nan_rows_reach_those_who_see_them(cuda_ok, cfg, n, S, windows, bad, spl
             ds = T.score_error(q.values[b, :m], np.nan_to_num(cv[b]), SCALE)
             tol = T.attend_tolerance(spread[b, :m], ref[b, :m], r + m, ds, wl.dtype)
             T.check_within(got[b, :m][ok], ref[b, :m][ok], tol[ok], "o")
+
+
+@pytest.mark.parametrize("cfg,n,S,windows", [
+    ("HEADS", 1, 2700, [(7, 2690, 1)]),
+    ("HEADS", 2, 3000, [(5, 2990, 2), (0, 1500, 1)]),
+    ("WIDE", 4, 2700, [(2600, 2690, 4), (5, 2001, 4)]),
+])
+def test_split_tiles_round_once(cuda_ok, cfg, n, S, windows):
+    """Queries of 0 over whole numbers: every weight is 1 and every sum exact, so that a row is off by
+    its one rounding to bf16, however many pieces its tile came in."""
+    wl = T.workload(getattr(T, cfg), len(windows), S)
+    rng = np.random.default_rng(S)
+    c = T.G.to_storage(rng.integers(-8, 9, (wl.batch, S, wl.row_width)).astype(float), "bf16")
+    q = T.G.to_storage(np.zeros((wl.batch, n, wl.n_heads, wl.row_width)), "bf16")
+    see = np.tril(np.ones((wl.batch, n, n), dtype=bool))
+    o, lse = attend(wl, P.upload(q), P.upload(c), windows, tree_dev(see), n)
+    ref, rl, spread = D.attend_tree(q.values, c.values, windows, see, SCALE, wl.d_latent)
+    got, gl = P.download(o), P.download(lse)
+    for b, (_, _, m) in enumerate(windows):
+        half = 2.0 ** (np.frexp(ref[b, :m])[1] - 9)               # half a step of the value itself
+        # a piece's lse (below 8) is off by 2^-20 at most, its exponential by 2^-22, above and below the
+        # fraction line; at most 74 pieces add up in float32
+        T.check_within(got[b, :m], ref[b, :m], half + 2.0 ** -17 * spread[b, :m], "o")
+        T.check_within(gl[b, :m], rl[b, :m], 2.0 ** -19, "lse")
