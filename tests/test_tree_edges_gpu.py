@@ -184,3 +184,134 @@ def test_split_tiles_round_once(cuda_ok, cfg, n, S, windows):
         # fraction line; at most 74 pieces add up in float32
         T.check_within(got[b, :m], ref[b, :m], half + 2.0 ** -17 * spread[b, :m], "o")
         T.check_within(gl[b, :m], rl[b, :m], 2.0 ** -19, "lse")
+
+
+# Whole numbers: q below 64 and c below 8 make every score's sum exact in float32 (below 2^24) but
+# wider than 16 bits, and the scale is a power of two, so that what is left are the roundings of the
+# softmax itself.
+WHOLE = 2.0 ** -11
+
+
+def whole_numbers(wl, n, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    draw = lambda top, *s: torch.randint(-top, top + 1, s, device=DEV, generator=g).bfloat16()  # noqa: E731
+    return (draw(64, wl.batch, n, wl.n_heads, wl.row_width),
+            draw(8, wl.batch, wl.ring_slots, wl.row_width))
+
+
+def scores64(q, c, b, window, see, n):
+    """Scores [nodes, heads, rows + nodes] of sequence b in 64 bits (-inf: hidden), and its rows."""
+    f, r, m = D.clip_window(window, c.shape[1], n)
+    at = torch.tensor(D.slots(f, r + m, c.shape[1]), device=DEV, dtype=torch.long)
+    k = c[b, at].double()
+    s = (q[b, :m].double().flatten(0, 1) @ k.T).view(m, q.shape[2], r + m) * WHOLE
+    seen = torch.ones((n, n), device=DEV).tril().bool() if see is None else see[b]
+    s[:, :, r:] = s[:, :, r:].masked_fill(~seen[:m, None, :m], float("-inf"))
+    return s, k, at, r, m
+
+
+def attend_whole(wl, q, c, windows, see, n, split=True):
+    shape = mla.make_shape(wl)
+    o = torch.zeros((wl.batch, n, wl.n_heads, wl.d_latent), device=DEV, dtype=q.dtype)
+    lse = torch.zeros((wl.batch, n, wl.n_heads), device=DEV)
+    ws = torch.empty(mla.mla_attend_tree_workspace_size(shape, n), dtype=torch.uint8,
+                     device=DEV) if split else None
+    mla.mla_attend_tree(shape, q, n, c, i32(windows), see, WHOLE, o, lse, ws)
+    return o, lse
+
+
+LONG = [
+    # tiles in rounds and a tail that cuts them; few sequences, cut in pieces; chains without context
+    ("HEADS", 128, 64, 8192, [(1000 * b, r, m) for b, (r, m) in enumerate(zip(
+        (8000, 61, 7777, 8128, 5000, 8064, 8000, 6500), (64, 60, 64, 33, 64, 1, 64, 64)))], True),
+    ("WIDE", 32, 40, 4000, [(3900, 3960, 40), (5, 1111, 9), (7, 0, 40)], True),
+    ("MAIN", 8, 17, 6000, [(5990, 5983, 17), (1, 640, 5)], True),
+    ("VIDEO", 32, 300, 1400, [(1300, 1100, 300), (0, 0, 300), (9, 64, 129)], False),
+    ("HEADS", 128, 90, 300, [(250, 210, 90), (3, 0, 90)], False),
+    ("WIDE", 16, 260, 700, [(650, 440, 260), (0, 0, 260), (1, 1, 65)], False),
+]
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("cfg,heads,n,S,windows,tree", LONG)
+def test_attend_exact_scores(cuda_ok, cfg, heads, n, S, windows, tree, split):
+    """Long contexts, many nodes: lse to what float32 partial scores leave, and the same bits in every
+    call while the two SMs hand their buffers back and forth over many blocks and tiles."""
+    wl = T.workload(dict(getattr(T, cfg), n_heads=heads), len(windows), S)
+    q, c = whole_numbers(wl, n, S)
+    see = tree_dev(T.random_tree(np.random.default_rng(S), wl.batch, n)[1]) if tree else None
+    o, lse = attend_whole(wl, q, c, windows, see, n, split)
+    for b, w in enumerate(windows):
+        s, k, _, r, m = scores64(q, c, b, w, see, n)
+        rl = s.logsumexp(-1)
+        # in log2 units: the scale 2^-23 of a score (below 16), the exponent's own rounding 2^-20, the
+        # exponential 2^-22; sums some 230 additions deep (64 keys of a block in four chains, 64 blocks
+        # and their rescaling, 74 pieces); lse, below 16, rounds by 2^-21
+        assert rl.abs().max() < 16 and s[s > -1e30].abs().max() < 16
+        assert (lse[b, :m] - rl).abs().max() <= 2.0 ** -15
+        p = (s - rl[..., None]).exp().flatten(0, 1)
+        ref, spread = p @ k[:, :512], p @ k[:, :512].abs()
+        err = (o[b, :m].double().flatten(0, 1) - ref).abs()
+        assert (err <= T.BF16 * ref.abs() + (T.BF16 + 2.0 ** -15) * spread).all()
+        assert (o[b, m:] == 0).all() and (lse[b, m:] == 0).all()
+    for _ in range(20):
+        o2, lse2 = attend_whole(wl, q, c, windows, see, n, split)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert mla.mla_device_error() == 0
+
+
+GROUPS = [
+    # (node, head) rows in groups of 128: whole nodes, several nodes, parts of nodes; 64 groups, more
+    ("HEADS", 128, 16, 3000, 2), ("HEADS", 128, 40, 2500, 24), ("HEADS", 128, 16, 700, 40),
+    ("HEADS", 128, 64, 900, 2), ("HEADS", 128, 65, 900, 2), ("HEADS", 128, 80, 1500, 3),
+    ("HEADS", 96, 30, 1200, 3), ("HEADS", 24, 100, 1200, 3), ("HEADS", 24, 350, 900, 2),
+    ("MAIN", 5, 70, 1200, 3), ("MAIN", 8, 300, 1200, 2), ("HEADS", 300, 11, 600, 3),
+    ("WIDE", 128, 20, 1500, 2), ("WIDE", 128, 70, 700, 2), ("WIDE", 32, 33, 900, 24),
+    ("WIDE", 8, 16, 1500, 4), ("WIDE", 24, 100, 600, 3),
+]
+
+
+@pytest.mark.parametrize("chain", [False, True])
+@pytest.mark.parametrize("cfg,heads,n,S,B", GROUPS)
+def test_weight_row_groups(cuda_ok, cfg, heads, n, S, B, chain):
+    """Query weights that leave half of the nodes out, at random, in runs and all but one."""
+    wl = T.workload(dict(getattr(T, cfg), n_heads=heads), B, S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng([n, S, heads])
+    nodes = [n] + [int(rng.integers(1, n + 1)) for _ in range(B - 1)]
+    windows = [(int(rng.integers(0, S)), int(rng.integers(0, S - m + 1)), m) for m in nodes]
+    q, c = whole_numbers(wl, n, S)
+    see = None if chain else tree_dev(T.random_tree(rng, B, n)[1])
+    qw = (rng.random((B, n)) < 0.5) * rng.uniform(0.5, 2.0, (B, n))
+    qw[0, n // 4:n // 2] = 0.0
+    if B > 2:
+        qw[1] = 0.0
+        qw[1, nodes[1] - 1] = 1.0
+        qw[2] = 0.0
+    qw = torch.from_numpy(qw.astype(np.float32)).to(DEV)
+    old = torch.rand((B, S), device=DEV)
+    win = i32(windows)
+    lse = torch.full((B, n, heads), float("nan"), device=DEV)
+    parts = [scores64(q, c, b, w, see, n) for b, w in enumerate(windows)]
+    for b, (s, _, _, _, m) in enumerate(parts):
+        lse[b, :m] = s.logsumexp(-1).float()
+    lse[0, 0, ::3] = float("-inf")
+    for weights in (qw, None):
+        out = torch.full((B, S), 7.0, device=DEV)
+        mla.mla_attend_weight(shape, q, n, c, win, see, WHOLE, lse, weights, old, out)
+        assert mla.mla_device_error() == 0
+        for b, (s, _, at, r, m) in enumerate(parts):
+            p = (s - lse[b, :m, :, None].double()).exp()
+            p = p.masked_fill(torch.isneginf(lse[b, :m])[..., None], 0.0).sum(1)
+            if weights is not None:
+                p = p * qw[b, :m, None].double()
+            ref = p.sum(0)
+            ref[:r] += old[b, at[:r]].double()
+            # all terms are positive: the exponents (below 32 in log2 units, rounded four times) and the
+            # exponential, then sums of 32 rows' columns, one after the other
+            rel = 2.0 ** -16 + (n * heads / 32 + 24) * T.F32
+            err = (out[b, at].double() - ref).abs()
+            assert (err <= rel * ref).all(), (b, float((err / ref).max()), rel)
+            rest = torch.ones(S, device=DEV, dtype=torch.bool)
+            rest[at] = False
+            assert (out[b, rest] == 7.0).all()
