@@ -315,3 +315,81 @@ def test_weight_row_groups(cuda_ok, cfg, heads, n, S, B, chain):
             rest = torch.ones(S, device=DEV, dtype=torch.bool)
             rest[at] = False
             assert (out[b, rest] == 7.0).all()
+
+
+@pytest.mark.parametrize("cfg,B,n,S", [("MAIN", 40, 128, 300), ("WIDE", 24, 100, 200)])
+def test_write_more_tiles_than_sms(cuda_ok, cfg, B, n, S):
+    """Rows of as many tiles as no split of K is for, ragged: own slots and positions, nothing else."""
+    wl = T.workload(getattr(T, cfg), B, S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng(B)
+    windows = [(int(rng.integers(0, S)), int(rng.integers(0, S - n + 1)), int(rng.integers(0, n + 1)))
+               for _ in range(B)]
+    d = wl.d_model
+    h = T.normal(rng, (B, n, d), wl.dtype)
+    w_dkv = T.normal(rng, (d, wl.d_latent), wl.dtype, d ** -0.5)
+    w_kr = T.normal(rng, (d, wl.d_rope), wl.dtype, d ** -0.5)
+    token = rng.integers(0, 200000, (B, n))
+    ct = torch.full((B, S, wl.row_width), 7.0, device=DEV, dtype=torch.bfloat16)
+    pos = torch.full((B, S), -1, dtype=torch.int32, device=DEV)
+    mla.mla_tree_write(shape, P.upload(h), d, n, i32(windows), i32(token), P.upload(w_dkv),
+                       P.upload(w_kr), ct, pos)
+    assert mla.mla_device_error() == 0
+    ref, rp = D.tree_write(np.full((B, S, wl.row_width), 7.0), np.full((B, S), -1), h.values,
+                           w_dkv.values, w_kr.values, windows, token, wl)
+    assert (pos.cpu().numpy() == rp).all()
+    got, at = P.download(ct), rp >= 0
+    assert (got[~at] == 7.0).all()
+    # as in test_place: d + 2 roundings of sums of sum |h||w|, the rotation, one rounding to bf16
+    size = np.linalg.norm(h.values, axis=-1).max() * max(
+        np.linalg.norm(w_dkv.values, axis=0).max(), np.linalg.norm(w_kr.values, axis=0).max())
+    T.check_within(got[at], ref[at], T.BF16 * np.abs(ref[at])
+                   + 2 * size * ((d + 2) * 2 * T.F32 + 2.0 ** -20), "cache")
+
+
+@pytest.mark.parametrize("B", [8192, 8200])
+def test_thousands_of_sequences(cuda_ok, B):
+    """On both sides of the most sequences whose tiles go in rounds: whole tiles give the bits of calls
+    of a few sequences, and so do the weights."""
+    n, S, H, part = 40, 90, 7, 1100
+    wl = T.workload(dict(T.MAIN, n_heads=H), B, S)
+    rng = np.random.default_rng(B)
+    windows = np.stack([rng.integers(0, S, B), rng.integers(0, S - n + 1, B), rng.integers(0, n + 1, B)], 1)
+    q, c = whole_numbers(wl, n, B)
+    win, w0 = i32(windows), torch.rand((B, S), device=DEV)
+    o, lse = attend_whole(wl, q, c, windows, None, n, split=False)
+    out = torch.zeros((B, S), device=DEV)
+    mla.mla_attend_weight(mla.make_shape(wl), q, n, c, win, None, WHOLE, lse, None, w0, out)
+    for b in range(0, B, part):
+        few = wl.scaled(batch=min(part, B - b))
+        e = b + few.batch
+        ob, lb = attend_whole(few, q[b:e], c[b:e], windows[b:e], None, n, split=False)
+        assert torch.equal(ob, o[b:e]) and torch.equal(lb, lse[b:e])
+        wb = torch.zeros((few.batch, S), device=DEV)
+        mla.mla_attend_weight(mla.make_shape(few), q[b:e], n, c[b:e], win[b:e], None, WHOLE, lb, None,
+                              w0[b:e], wb)
+        assert torch.allclose(wb, out[b:e], rtol=2.0 ** -18, atol=0)      # (pairs may share a unit)
+    for b in range(0, B, 509):                               # and some of them in 64 bits
+        s, k, at, r, m = scores64(q, c, b, windows[b], None, n)
+        if m:
+            assert (lse[b, :m] - s.logsumexp(-1)).abs().max() <= 2.0 ** -15
+    assert mla.mla_device_error() == 0
+
+
+@pytest.mark.parametrize("cfg", ["TINY", "MAIN", "WIDE"])
+@pytest.mark.parametrize("split", [True, False])
+def test_attend_without_lse(cuda_ok, cfg, split):
+    """No lse asked for: the same o_lat."""
+    n, S, windows = 5, 2700, [(2600, 2650, 5), (0, 3, 2)]
+    wl = T.workload(getattr(T, cfg), 2, S)
+    shape = mla.make_shape(wl)
+    rng = np.random.default_rng(1)
+    q = P.upload(T.normal(rng, (2, n, wl.n_heads, wl.row_width), wl.dtype))
+    c = P.upload(T.normal(rng, (2, S, wl.row_width), wl.dtype))
+    o, _ = attend(wl, q, c, windows, None, n, split)
+    o2 = torch.full_like(o, 7.0)
+    nws = mla.mla_attend_tree_workspace_size(shape, n) if split else 0
+    ws = torch.empty(nws, dtype=torch.uint8, device=DEV) if nws else None
+    mla.mla_attend_tree(shape, q, n, c, i32(windows), None, SCALE, o2, None, ws)
+    assert torch.equal(o, o2)
+    assert mla.mla_device_error() == 0
