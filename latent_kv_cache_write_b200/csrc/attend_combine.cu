@@ -15,8 +15,9 @@ using tc::pack_bf16;
 // pieces k, k + CSPLIT, ... (with several warps per row, four pieces' loads in
 // flight at a time) and the row's warps add their sums in shared memory.  One warp per
 // row suits tiles cut in a few pieces (the chunk shapes); more suit a tile cut across
-// every cluster (decode of a few sequences).  Lane l holds latent dims [16 l, 16 l + 16)
-// (d_c = 512).  The output is the partials weighted by exp(lse_p - lse),
+// every cluster (decode of a few sequences).  A lane holds 16 latent dims (d_c = 512): of bf16
+// pieces [16 l, 16 l + 16), of float32 ones 4 of each 128, so that a warp's access is one run of
+// bytes either way.  The output is the partials weighted by exp(lse_p - lse),
 // lse = log sum_p exp(lse_p), each half of the dims with the log-sum-exps of the CTA half
 // that computed it.
 //
@@ -28,8 +29,10 @@ template <int CSPLIT, bool TREE, typename Slot>
 __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_lse, float* red,
                                             int rr, int part, int lane, int r, bool row_ok,
                                             int64_t grow, int np, const Slot& slot) {
-  const int d = lane * 16;
-  const int half = d / HALF;                 // the CTA half these dims were computed in
+  // 16-byte vectors of a piece per lane, and the halves (of the CTAs that computed them) they are in
+  constexpr int NV = TREE ? 4 : 2, NH = TREE ? 2 : 1;
+  const int d = TREE ? lane * 4 : lane * 16, step = TREE ? 128 : 8;      // vector q: dims d + q step ..
+  const int half = TREE ? 0 : d / HALF;      // (TREE: vectors 0, 1 are in half 0, 2 and 3 in half 1)
   // each half's largest log-sum-exp over the row's pieces, the lanes taking pieces in turn
   float m0 = -INFINITY, m1 = -INFINITY;
   bool nan = false;
@@ -46,26 +49,39 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
-  float mx = half ? m1 : m0;
-  if (TREE && __any_sync(0xffffffffu, nan) && mx == -INFINITY) mx = 0.f;
-  const float* lse_h = ws_lse + half * TM + r;   // + slot * 2 * TM
+  float mx[NH], wsum[NH];
+  mx[0] = half ? m1 : m0;
+  if constexpr (TREE) {
+    mx[1] = m1;
+    if (__any_sync(0xffffffffu, nan))
+      for (int h = 0; h < NH; ++h) mx[h] = mx[h] == -INFINITY ? 0.f : mx[h];
+  }
+#pragma unroll
+  for (int h = 0; h < NH; ++h) wsum[h] = 0.f;
+  const float* lse_h = ws_lse + half * TM + r;   // + slot * 2 * TM, + TM: the next half
   float acc[16];
 #pragma unroll
   for (int q = 0; q < 16; ++q) acc[q] = 0.f;
-  float wsum = 0.f;
-  // a piece's 16 dims of this lane: 16-byte vectors of bf16 or float32
-  constexpr int NV = TREE ? 4 : 2;
-  auto vectors = [&](int64_t ps) {
+  auto load = [&](int64_t ps, float (&lp)[NH], uint4 (&v)[NV]) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) lp[h] = lse_h[(ps * 2 + h) * TM];
     const int64_t at = (ps * TM + r) * a.g.Dc + d;
-    return TREE ? reinterpret_cast<const uint4*>(a.ws_f + at)
-                : reinterpret_cast<const uint4*>(a.ws_o + at);
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+      v[q] = TREE ? *reinterpret_cast<const uint4*>(a.ws_f + at + q * step)
+                  : *reinterpret_cast<const uint4*>(a.ws_o + at + q * step);
   };
-  auto add = [&](float lp, const uint4 (&v)[NV]) {
-    const float w = (TREE ? lp != -INFINITY : lp > -INFINITY) ? expf(lp - mx) : 0.f;
-    wsum += w;
+  auto add = [&](const float (&lp)[NH], const uint4 (&v)[NV]) {
+    float wh[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      wh[h] = (TREE ? lp[h] != -INFINITY : lp[h] > -INFINITY) ? expf(lp[h] - mx[h]) : 0.f;
+      wsum[h] += wh[h];
+    }
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
       const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+      const float w = wh[TREE ? q / 2 : 0];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (TREE) {
@@ -77,59 +93,67 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
       }
     }
   };
-  if (row_ok && mx > -INFINITY) {
+  if (row_ok && (TREE || mx[0] > -INFINITY)) {
     int p = part;
     if constexpr (CSPLIT > 1) {
       for (; p + 3 * CSPLIT < np; p += 4 * CSPLIT) {
-        float lp[4];
+        float lp[4][NH];
         uint4 v[4][NV];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t pu = slot(p + u * CSPLIT);
-          lp[u] = lse_h[pu * 2 * TM];
-          const uint4* o = vectors(pu);
-#pragma unroll
-          for (int q = 0; q < NV; ++q) v[u][q] = o[q];
-        }
+        for (int u = 0; u < 4; ++u) load(slot(p + u * CSPLIT), lp[u], v[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) add(lp[u], v[u]);
       }
     }
     for (; p < np; p += CSPLIT) {
+      float lp[NH];
       uint4 v[NV];
-      const int64_t ps = slot(p);
-      const uint4* o = vectors(ps);
-#pragma unroll
-      for (int q = 0; q < NV; ++q) v[q] = o[q];
-      add(lse_h[ps * 2 * TM], v);
+      load(slot(p), lp, v);
+      add(lp, v);
     }
   }
   if constexpr (CSPLIT > 1) {
-    float* mine = red + ((rr * CSPLIT + part) * 32 + lane) * 17;
+    constexpr int RED = TREE ? 19 : 17;            // (odd: free of bank conflicts)
+    float* mine = red + ((rr * CSPLIT + part) * 32 + lane) * RED;
 #pragma unroll
     for (int q = 0; q < 16; ++q) mine[q] = acc[q];
-    mine[16] = wsum;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) mine[16 + h] = wsum[h];
     __syncthreads();
     if (part != 0 || !row_ok) return;
     for (int k = 1; k < CSPLIT; ++k) {
-      const float* other = red + ((rr * CSPLIT + k) * 32 + lane) * 17;
+      const float* other = red + ((rr * CSPLIT + k) * 32 + lane) * RED;
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[q] += other[q];
-      wsum += other[16];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) wsum[h] += other[16 + h];
     }
   } else {
     if (!row_ok) return;
   }
-  const bool any = TREE ? wsum != 0.f : wsum > 0.f;
-  const float inv = any ? 1.f / wsum : 0.f;
-  uint4* dst = reinterpret_cast<uint4*>(a.o_lat + grow * a.g.Dc + d);
+  bool any[NH];
+  float inv[NH];
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    dst[q] = make_uint4(pack_bf16(acc[8 * q] * inv, acc[8 * q + 1] * inv),
-                        pack_bf16(acc[8 * q + 2] * inv, acc[8 * q + 3] * inv),
-                        pack_bf16(acc[8 * q + 4] * inv, acc[8 * q + 5] * inv),
-                        pack_bf16(acc[8 * q + 6] * inv, acc[8 * q + 7] * inv));
-  if (lane == 0 && a.lse) a.lse[grow] = any ? mx + logf(wsum) : -INFINITY;
+  for (int h = 0; h < NH; ++h) {
+    any[h] = TREE ? wsum[h] != 0.f : wsum[h] > 0.f;
+    inv[h] = any[h] ? 1.f / wsum[h] : 0.f;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float f = inv[TREE ? q / 4 : 0];
+    w[q] = pack_bf16(acc[2 * q] * f, acc[2 * q + 1] * f);
+  }
+  bf16* dst = a.o_lat + grow * a.g.Dc + d;
+#pragma unroll
+  for (int q = 0; q < NV; ++q) {
+    if constexpr (TREE)
+      *reinterpret_cast<uint2*>(dst + q * step) = make_uint2(w[2 * q], w[2 * q + 1]);
+    else
+      *reinterpret_cast<uint4*>(dst + q * step) =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+  if (lane == 0 && a.lse) a.lse[grow] = any[0] ? mx[0] + logf(wsum[0]) : -INFINITY;
 }
 
 template <int CSPLIT>
@@ -180,7 +204,7 @@ __device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws
 
 __global__ void __launch_bounds__(256)
     combine_tree_kernel(const __grid_constant__ AttnArgs a, int clusters) {
-  __shared__ float red[8 * 32 * 17];
+  __shared__ float red[8 * 32 * 19];
   __shared__ int4 cut[MAXC + 1];
   __shared__ int first[MAXC], pieces[MAXC];
   __shared__ int n_sh, most_sh;
