@@ -12,7 +12,7 @@ namespace {
 using tc::pack_bf16;
 
 // CSPLIT warps per row of a split tile, 8 / CSPLIT rows per CTA: warp k of a row merges
-// pieces k, k + CSPLIT, ... (with several warps per row, four pieces' loads in
+// pieces k, k + CSPLIT, ... (with several warps per row, the loads of four pieces, of float32 two, in
 // flight at a time) and the row's warps add their sums in shared memory.  One warp per
 // row suits tiles cut in a few pieces (the chunk shapes); more suit a tile cut across
 // every cluster (decode of a few sequences).  A lane holds 16 latent dims (d_c = 512): of bf16
@@ -96,13 +96,14 @@ __device__ __forceinline__ void combine_row(const AttnArgs& a, const float* ws_l
   if (row_ok && (TREE || mx[0] > -INFINITY)) {
     int p = part;
     if constexpr (CSPLIT > 1) {
-      for (; p + 3 * CSPLIT < np; p += 4 * CSPLIT) {
-        float lp[4][NH];
-        uint4 v[4][NV];
+      constexpr int U = TREE ? 2 : 4;                // pieces in flight: 128 bytes a lane
+      for (; p + (U - 1) * CSPLIT < np; p += U * CSPLIT) {
+        float lp[U][NH];
+        uint4 v[U][NV];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) load(slot(p + u * CSPLIT), lp[u], v[u]);
+        for (int u = 0; u < U; ++u) load(slot(p + u * CSPLIT), lp[u], v[u]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add(lp[u], v[u]);
+        for (int u = 0; u < U; ++u) add(lp[u], v[u]);
       }
     }
     for (; p < np; p += CSPLIT) {
@@ -202,7 +203,7 @@ __device__ __forceinline__ void combine_tiles(const AttnArgs& a, const float* ws
   }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
     combine_tree_kernel(const __grid_constant__ AttnArgs a, int clusters) {
   __shared__ float red[8 * 32 * 19];
   __shared__ int4 cut[MAXC + 1];
