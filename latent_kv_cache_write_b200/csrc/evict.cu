@@ -14,9 +14,9 @@
 // then ballots and scans that keep the rows' order.  It is bound by its instructions (one SM per
 // sequence) and the latency of its passes.  Where at most MOVE_HERE rows can move (accepted nodes, a full
 // cache that drops a few rows per step) the block also moves them; otherwise a second launch lets the
-// whole GPU copy the listed rows, each read and written once (bound by HBM).  32 sequences of up to
-// 8192 rows of 576 bf16, to 4096: 40 us, of which the plan some 8 (12 with every pass run and its counts cleared
-// between barriers) and the move 25 (5 TB/s); 4 full sequences that drop 16 rows: 10 us.
+// whole GPU copy the listed rows, each read and written once (bound by HBM).  A pass over 32 sequences
+// of up to 8192 rows of 576 bf16, to 4096, with the copy that puts their state back: 44 us; alone and with
+// cold caches the plan takes 14 and the move 28.  4 sequences that drop up to 16 rows each: 12 us.
 #include "launch.h"
 #include "tc_ptx.cuh"
 #include "window.cuh"

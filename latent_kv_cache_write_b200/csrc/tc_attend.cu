@@ -79,9 +79,11 @@ constexpr int TREE_MAXR = 32;   // rounds of whole tiles a draft-tree cluster pl
 //          off).  V = 3 sends a block at once, keys 32-63 into the peer's P buffer, which is free
 //          once its PV has read the P of its previous block (the PV's commit says so); V = 4 sends
 //          both halves through the merged buffer.  A warp hands a buffer back for itself.
-//          32 trees of 24 nodes, 128 heads, 5096 rows: V = 3 1.25 ms (0.87 PFLOP/s); with one
+//          32 trees of 24 nodes, 128 heads, 5096 rows, over and over on the same inputs: V = 3
+//          1.25 to 1.33 ms from GPU to GPU (0.82 to 0.87 PFLOP/s); where it took 1.25, with one
 //          barrier for the whole block 1.35, with three K/V stages and a landing buffer of its own
-//          1.46, with the fp16 exchange of V = 0 1.05.
+//          1.46, with the fp16 exchange of V = 0 1.05.  P is rounded to bf16, the tensor cores' operand
+//          type, and the output once more: 2.0e-3 of it where one rounding makes 1.7e-3.
 // K/V ring, box-major: latent box q (dims 64q..64q+63 of this CTA's half, 128-byte
 // swizzle) of stage s at OFF_KV + (q * NST + s) * BOXB; RoPE box q of RoPE slot r at
 // OFF_KVR + (q * NSTR + r) * RBB (NSTR = NST and r = s except for V = 1).
@@ -342,9 +344,9 @@ struct TreeWalk {
 // Costs in key blocks: of a segment (the switch: Q reload, output epilogue, pipeline refill), and of
 // split tiles (the merge).  Measured on B200 (video chunk, long window and decode shapes).
 constexpr int SEG_COST = 7, COMBINE_COST = 16;
-// Draft trees, what it costs to split tiles when every cluster has one piece of one tile: 8 to 9 us,
-// against some 1.2 us per block, for a merge launch; and, where the launch is made anyway (3.5 to 5
-// us that merge nothing), for the pieces.
+// Draft trees, what it costs to split tiles when every cluster has one piece of one tile: 8 to 11 us
+// (24 to 72 pieces), against some 1.2 us per block, for a merge launch; and, where the launch is made
+// anyway (3.5 to 5 us that merge nothing), for the pieces.
 constexpr int MERGE_COST = 7, PIECE_COST = 3;
 
 // Where cluster u's equal share of a line of W positions starts.
@@ -456,8 +458,8 @@ __device__ __forceinline__ void tree_plan(const AttnArgs& a, const TreeSched& sc
   if (W > 0) {
     // With no more tiles than clusters, a cluster takes one piece of one tile: no more than `len`
     // blocks, the fewest for which the clusters suffice, if that pays for the merge (1 sequence of
-    // 900 rows, 128 heads: 31.7 -> 21.3 us; 32 of 1500: 44 -> 41), else a whole tile (70 sequences of up to 800 rows:
-    // 49 us by equal shares, where short neighbours meet in a cluster, -> 34).
+    // 900 rows, 128 heads: 30 -> 21 us; 32 of 1500: 44 -> 42), else a whole tile (70 sequences of up to
+    // 800 rows: 49 us by equal shares, where short neighbours meet in a cluster, -> 34).
     const float share = (float)W / (float)G;
     uint32_t len = 0;
     if (T <= (uint32_t)G) {

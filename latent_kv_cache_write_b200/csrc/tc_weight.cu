@@ -4,7 +4,9 @@
 // With the log-sum-exps known this is a product S^T = K . Q^T whose epilogue is one exponential
 // and one multiply-add per score, summed along the rows.  Keys are the M side (TMEM lanes), rows the
 // N side (columns), so a thread owns a key and its sum never leaves the thread.  Nothing of S is
-// stored; the sums of a key are joined in one place, without atomics, so the order is fixed.
+// stored; the sums of a key are joined in one place, without atomics, so the order is fixed.  The
+// scores' sums are the tensor cores' float32, which cut what does not fit: of normal values weights come
+// out some 1.5e-6 of themselves low (128 heads, 16 nodes, 3000 rows; 1e-7 where the sums are exact).
 // Groups of 128 rows whose query weights are all 0 (rejected nodes) are left out.
 //
 // A CTA pair (cta_group::2) takes 256 keys at a time, 128 per CTA, and 256 rows per MMA, of which
@@ -13,11 +15,12 @@
 //   RES_K: the keys' tile (9 boxes of 128 rows x 64 dims, 144 KB) stays in shared memory while the
 //          rows stream past it in 4 stages.  A tile of 256 x 256 x 576 takes 6600 to 7200 clk, the
 //          rate that cuBLAS's bf16 GEMM reaches here; the rest of a call is the start (plan, first
-//          loads) and clusters with fewer units than others.  8 trees of up to 16 nodes, 128
-//          heads, over up to 4096 rows: 74 us against a floor of 48.
+//          loads) and clusters with fewer units than others.  A pass over 8 trees of up to 16
+//          nodes, 128 heads, up to 8100 rows, its inputs new each time: 77 us against a floor of 48.
 //   RES_Q: at most 128 rows per sequence (single tokens, small trees): the rows stay and the keys
 //          stream, read once from HBM, which bounds it (64 sequences of 8191 rows, one token
-//          each: 115 us against a floor of 94; a kernel that only streams them by TMA takes 102).
+//          each: a pass on new inputs 131 us, 110 over and over on the same ones, against a floor
+//          of 94; a kernel that only streams them by TMA takes 102).
 //   STREAM: d_R = 512 with more rows: 256 KB of keys do not fit, both operands stream.
 //
 // A cluster has one to four pairs.  It takes whole units (256 keys), and its pairs share the tiles of
@@ -57,8 +60,8 @@ struct WLay {
   static constexpr int NRES = MODE == STREAM ? 0 : NSL;               // resident boxes
   static constexpr int SBOX = MODE == RES_K ? QBOX : (MODE == RES_Q ? KBOX : KBOX + QBOX);
   // slices of a stage, stages.  A stage costs the loading and the MMA thread some 500 clk of waits
-  // and arrivals whatever it holds: single slices bound RES_Q by that (129 us where three take 115;
-  // with d_R = 512 two took as long as one).
+  // and arrivals whatever it holds: single slices bound RES_Q by that (64 x 8191 rows without other
+  // work between the calls: 129 us where three take 115; with d_R = 512 two took as long as one).
   static constexpr int SPS = MODE == RES_Q && NSL == 9 ? 3 : 1;
   static constexpr int NST = MODE == RES_K ? 4 : (MODE == RES_Q ? (NSL == 9 ? 3 : 5) : 6);
   static constexpr int STAGE = SPS * SBOX;
